@@ -321,6 +321,60 @@ int sinkattn_append_kv_fp8(const void *k, const void *v, const float *k_scale,
                            void *v_pages, const sinkattn_paged_desc *desc, void *workspace,
                            size_t ws_bytes, sinkattn_stream_t stream);
 
+/* ------------------------------------------------- queries and keys before attention --
+ * Per-head RMS norm and rotary position embedding of a step's queries and keys in one pass, for
+ * prefills, decodes and appends alike (sinkattn_decode_append_rope covers gpt-oss decode steps
+ * alone).  For each row x of head_dim D, in fp32 with one rounding of the result to bf16:
+ *     y = x / sqrt(mean(x^2) + eps) * weight      (weight given; else y = x)
+ * and, with R = rotary_dim, for each pair (a, b) = (i, i + R/2), or (2i, 2i + 1) if interleaved,
+ * i < R/2, at the token's position p:
+ *     z_a = mscale (y_a cos(p theta_i) - y_b sin(p theta_i))
+ *     z_b = mscale (y_b cos(p theta_i) + y_a sin(p theta_i))
+ * z = y for the elements from R on.  With w_i = base^(-2i/R) the rates theta_i are
+ *     PLAIN       w_i
+ *     LINEAR      w_i / factor
+ *     YARN        (1 - y_i) w_i + y_i w_i / factor with the ramp y_i of sinkattn_rope_desc, D there
+ *                 being R; mscale = 1 + 0.1 ln(factor) (elsewhere 1)
+ *     WAVELENGTH  the same mix with y_i = clamp((beta_fast - n_i) / (beta_fast - beta_slow), 0, 1),
+ *                 n_i = original_context w_i / (2 pi) the pair's turns over the original context:
+ *                 pairs of at least beta_fast turns keep their rate, of at most beta_slow turns
+ *                 are slowed by the factor
+ * Angles are within ~1e-6 rad for positions below 2^24. */
+#define SINKATTN_ROTARY_PLAIN 0
+#define SINKATTN_ROTARY_LINEAR 1
+#define SINKATTN_ROTARY_YARN 2
+#define SINKATTN_ROTARY_WAVELENGTH 3
+
+typedef struct sinkattn_rotary_desc {
+    double base;              /* frequency base (> 1) */
+    double factor;            /* >= 1; not read for PLAIN */
+    double beta_fast;         /* YARN, WAVELENGTH: > beta_slow > 0 */
+    double beta_slow;
+    int32_t original_context; /* YARN, WAVELENGTH: context length before scaling (> 0) */
+    int32_t scaling;          /* SINKATTN_ROTARY_* */
+    int32_t rotary_dim;       /* R: a multiple of 16, 16 .. head_dim */
+    int32_t interleaved;      /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+} sinkattn_rotary_desc;
+
+/* q, k:       bf16, row t at q + t * q_row_stride elements ([Hq, D] dense, the stride >= Hq * D
+ *             and a multiple of 8; k alike with Hkv), e.g. parts of a fused projection's rows.
+ *             Either may be NULL together with its output.
+ * q_weight, k_weight: fp32 [D] or NULL (no norm), 16-byte aligned.  The sum of squares is taken
+ *             in fp32: rows with entries of 2^60 or more overflow it.
+ * positions:  int32 [total_tokens], each below 2^24; a negative one marks padding: the token's
+ *             output rows are left as they were.  Not read without a rotation.
+ * rotary:     host pointer, read during the call; NULL: no rotation
+ * q_out, k_out: bf16 [total_tokens, Hq, D] and [total_tokens, Hkv, D], dense.  q_out == q (k_out
+ *             == k) with dense rows works in place; any other overlap is rejected.
+ * desc:       heads and head_dim (the other fields are checked, not used)
+ * workspace:  optional (may be NULL): if given (>= 256 bytes), a position of 2^24 or more sets
+ *             SINKATTN_STATUS_BAD_LENGTH there; its rows are left as they were either way. */
+int sinkattn_qk_norm_rope(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                          const float *q_weight, const float *k_weight, float eps, const int32_t *positions,
+                          int32_t total_tokens, const sinkattn_rotary_desc *rotary, void *q_out, void *k_out,
+                          const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                          sinkattn_stream_t stream);
+
 /* ------------------------------------------------------- decode, no allocation --
  * No counterpart on the source pages: an addition for callers that cannot allocate
  * device memory where they run attention - code whose device memory is owned by

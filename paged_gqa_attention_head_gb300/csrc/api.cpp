@@ -273,6 +273,58 @@ int rope_table(const sinkattn_rope_desc *r, int D, DecodeArgs *a) {
     return SINKATTN_OK;
 }
 
+// Whether the byte ranges of two tensors of `rows` rows share a byte (a row of `len` elements of
+// 2 bytes, rows `stride` elements apart); a missing tensor shares nothing.
+bool overlap(const void *a, int64_t a_stride, int64_t a_len, const void *b, int64_t b_stride, int64_t b_len,
+             int64_t rows) {
+    if (!a || !b || rows <= 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + 2 * (uintptr_t)((rows - 1) * b_stride + b_len) &&
+           b0 < a0 + 2 * (uintptr_t)((rows - 1) * a_stride + a_len);
+}
+
+// The turn per position of each pair of a sinkattn_rotary_desc (its formulas in
+// include/sinkattn.h), in double on the host, as float pairs hi + lo.
+int rotary_table(const sinkattn_rotary_desc *r, int D, RotaryArgs *a) {
+    if (!(r->base > 1.0) || !(r->base < INFINITY)) return SINKATTN_ERR_INVALID_ARG;
+    if (r->rotary_dim <= 0 || r->rotary_dim > D || (r->interleaved != 0 && r->interleaved != 1))
+        return SINKATTN_ERR_INVALID_ARG;
+    if (r->rotary_dim % 16) return SINKATTN_ERR_UNSUPPORTED;
+    const bool scaled = r->scaling != SINKATTN_ROTARY_PLAIN;
+    const bool bands = r->scaling == SINKATTN_ROTARY_YARN || r->scaling == SINKATTN_ROTARY_WAVELENGTH;
+    if (r->scaling < SINKATTN_ROTARY_PLAIN || r->scaling > SINKATTN_ROTARY_WAVELENGTH) return SINKATTN_ERR_INVALID_ARG;
+    if (scaled && (!(r->factor >= 1.0) || !(r->factor < INFINITY))) return SINKATTN_ERR_INVALID_ARG;
+    if (bands && (r->original_context <= 0 || !(r->beta_slow > 0.0) || !(r->beta_fast > r->beta_slow) ||
+                  !(r->beta_fast < INFINITY)))
+        return SINKATTN_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586476925286766559;
+    const int R = r->rotary_dim;
+    double lo = 0.0, span = 1.0;
+    if (r->scaling == SINKATTN_ROTARY_YARN) {
+        const double lnb = log(r->base);
+        lo = fmax(0.0, floor(R * log(r->original_context / (two_pi * r->beta_fast)) / (2.0 * lnb)));
+        const double hi = fmin(R - 1.0, ceil(R * log(r->original_context / (two_pi * r->beta_slow)) / (2.0 * lnb)));
+        span = fmax(hi - lo, 0.001);
+    }
+    for (int i = 0; i < R / 2; ++i) {
+        const double w = pow(r->base, -2.0 * i / R);
+        double y = 0.0;  // share of the slowed-down rate
+        if (r->scaling == SINKATTN_ROTARY_LINEAR) y = 1.0;
+        if (r->scaling == SINKATTN_ROTARY_YARN) y = fmin(1.0, fmax(0.0, (i - lo) / span));
+        if (r->scaling == SINKATTN_ROTARY_WAVELENGTH) {
+            const double turns = r->original_context * w / two_pi;
+            y = fmin(1.0, fmax(0.0, (r->beta_fast - turns) / (r->beta_fast - r->beta_slow)));
+        }
+        const double th = scaled ? (1.0 - y) * w + y * (w / r->factor) : w;
+        a->hi[i] = (float)th;
+        a->lo[i] = (float)(th - (double)a->hi[i]);
+    }
+    a->rotary_dim = R;
+    a->interleaved = r->interleaved;
+    a->mscale = r->scaling == SINKATTN_ROTARY_YARN ? (float)(1.0 + 0.1 * log(r->factor)) : 1.f;
+    return SINKATTN_OK;
+}
+
 // A decode's launches once its arguments are prepared: the one-launch plan for a short
 // sliding window, else the split-KV kernel and the merge.
 int launch_decode_pair(const DecodePrep &P, const CUtensorMap &kmap, const CUtensorMap &vmap,
@@ -649,6 +701,54 @@ int sinkattn_prefill_fp8(const void *q, const void *k, const void *v, const int3
     return prefill_common(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, prefix_block_table,
                           prefix_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, true, k_scale,
                           v_scale, true, stream);
+}
+
+int sinkattn_qk_norm_rope(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
+                          const float *q_weight, const float *k_weight, float eps, const int32_t *positions,
+                          int32_t total_tokens, const sinkattn_rotary_desc *rotary, void *q_out, void *k_out,
+                          const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                          sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    RotaryArgs a;
+    a.rotary_dim = 0;
+    a.interleaved = 0;
+    a.mscale = 1.f;
+    if (rotary && (rc = rotary_table(rotary, desc->head_dim, &a))) return rc;
+    if (!(eps >= 0.f) || !(eps < INFINITY)) return SINKATTN_ERR_INVALID_ARG;
+    if (workspace && (ws_bytes < kStatusBytes || !aligned(workspace, kAlign))) return SINKATTN_ERR_INVALID_ARG;
+    if (total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
+    if ((!q && !k) || !q != !q_out || !k != !k_out || (rotary && !positions)) return SINKATTN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
+        !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4))
+        return SINKATTN_ERR_INVALID_ARG;
+    const int64_t rq = (int64_t)desc->num_qo_heads * desc->head_dim, rk = (int64_t)desc->num_kv_heads * desc->head_dim;
+    if ((q && (q_row_stride < rq || q_row_stride % 8)) || (k && (k_row_stride < rk || k_row_stride % 8)))
+        return SINKATTN_ERR_INVALID_ARG;
+    // in place row by row, or apart: anything else would read rows already written
+    const int64_t T = total_tokens;
+    if ((overlap(q_out, rq, rq, q, q_row_stride, rq, T) && !(q_out == q && q_row_stride == rq)) ||
+        (overlap(k_out, rk, rk, k, k_row_stride, rk, T) && !(k_out == k && k_row_stride == rk)) ||
+        overlap(q_out, rq, rq, k, k_row_stride, rk, T) || overlap(k_out, rk, rk, q, q_row_stride, rq, T) ||
+        overlap(q_out, rq, rq, k_out, rk, rk, T))
+        return SINKATTN_ERR_INVALID_ARG;
+    a.q = q;
+    a.k = k;
+    a.q_stride = q_row_stride;
+    a.k_stride = k_row_stride;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.positions = positions;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.T = total_tokens;
+    a.Hq = desc->num_qo_heads;
+    a.Hkv = desc->num_kv_heads;
+    a.splits = 1;
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_rc(launch_qk_norm_rope(desc->head_dim, a, (cudaStream_t)stream), "query/key preparation launch");
 }
 
 int sinkattn_append_kv(const void *k, const void *v, const int32_t *cu_seqlens,

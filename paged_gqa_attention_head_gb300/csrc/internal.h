@@ -87,6 +87,24 @@ struct AppendArgs {
 };
 cudaError_t launch_append_kv(const AppendArgs &a, cudaStream_t stream);
 
+constexpr int kRotaryMaxPos = 1 << 24;  // positions stay exact floats below this
+struct RotaryArgs {
+    const void *q, *k;           // bf16 [T] rows of [Hq, D] / [Hkv, D], `stride` elements apart; or nullptr
+    int64_t q_stride, k_stride;
+    const float *q_weight, *k_weight;  // [D] or nullptr: no norm
+    float eps;
+    const int32_t *positions;    // [T] (not read when rotary_dim is 0)
+    void *q_out, *k_out;         // bf16 [T, Hq, D], [T, Hkv, D]
+    int T, Hq, Hkv;
+    int splits;                  // warps a token's rows are split over (set by the launch)
+    uint32_t *status;            // or nullptr
+    int rotary_dim;              // leading elements of a row that turn; 0: no rotation
+    int interleaved;
+    float mscale;
+    float hi[64], lo[64];        // turn per position of each pair, as a float pair
+};
+cudaError_t launch_qk_norm_rope(int D, const RotaryArgs &a, cudaStream_t stream);
+
 struct PrefillArgs {
     const int32_t *cu_seqlens;  // [n + 1]
     const int32_t *prefix_block_table;  // [n, max_pages] or nullptr

@@ -26,6 +26,7 @@ PAGE_SIZE = 16
 
 # every symbol the header declares, with (restype, argtypes)
 _P, _I32, _F, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_I64 = ctypes.c_int64
 
 
 class PagedDesc(ctypes.Structure):
@@ -39,6 +40,12 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double),
                 ("original_context", _I32), ("beta_fast", ctypes.c_double),
                 ("beta_slow", ctypes.c_double)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("original_context", _I32), ("scaling", _I32),
+                ("rotary_dim", _I32), ("interleaved", _I32)]
 
 
 _DP = ctypes.POINTER(PagedDesc)
@@ -70,6 +77,8 @@ SIGNATURES = {
                                                    _P, _SZ, _P]),
     "sinkattn_append_kv_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _DP, _P, _SZ,
                                               _P]),
+    "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
+                                             ctypes.POINTER(RotaryDesc), _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
 }
 
@@ -544,3 +553,104 @@ def decode_noalloc(q, k_pages, v_pages, block_table, seq_lens, sinks=None, scale
                                           ctypes.byref(desc), _ptr(status), _stream(dev)),
            "sinkattn_decode_noalloc")
     return out, lse
+
+
+# ---------------------------------------------------------------- shared checks
+def _status_buffer(device: torch.device) -> Optional[torch.Tensor]:
+    """The status word that calls without scratch share (bits are OR-ed in, so streams may share it):
+    workspace(256, device, "append"), read with get_status.  None while a capture runs before the
+    buffer exists: the calls then report nothing."""
+    if (device, "append") not in _workspaces and torch.cuda.is_current_stream_capturing():
+        return None
+    return workspace(256, device, "append")
+
+
+def _need_cuda(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
+    return t.device
+
+
+def _need_rows(t: torch.Tensor, name: str, device: torch.device) -> int:
+    """Checks bf16 rows [T, H, D], each row's [H, D] dense (a part of wider rows will do), and
+    returns the row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return t.stride(0) if T > 1 else H * D
+
+
+# ---------------------------------------------------------------- queries and keys
+ROTARY_SCALING = {"none": 0, "linear": 1, "yarn": 2, "wavelength": 3}
+
+
+def rotary_desc(base: float, rotary_dim: int, factor: float = 1.0, scaling: str = "none",
+                original_context: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                interleaved: bool = False) -> RotaryDesc:
+    """Rotation of the first rotary_dim elements of each head (a multiple of 16): pairs (i, i +
+    rotary_dim / 2), or (2i, 2i + 1) if interleaved; scaling "none", "linear", "yarn" or
+    "wavelength" (SINKATTN_ROTARY_* in include/sinkattn.h)."""
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}, got {scaling!r}")
+    return RotaryDesc(float(base), float(factor), float(beta_fast), float(beta_slow), int(original_context),
+                      ROTARY_SCALING[scaling], int(rotary_dim), int(bool(interleaved)))
+
+
+def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, q_out=None, k_out=None, workspace_buf=None):
+    """Per-head RMS norm and rotary embedding of a step's queries and keys in one pass
+    (sinkattn_qk_norm_rope).  q [T, Hq, D], k [T, Hkv, D] bf16, each token's heads dense (parts of a
+    fused projection's rows will do); k may be None.  positions int32 [T] (negative: padding, the
+    rows are left as they were); q_weight / k_weight float32 [D] or None (no norm); rotary None: no
+    rotation.  q_out / k_out dense, or q / k themselves if dense.  Returns (q_out, k_out)."""
+    dev = _need_cuda(q, "q")
+    qs = _need_rows(q, "q", dev)
+    T, Hq, D = q.shape
+    ks, Hkv = 0, Hq
+    if k is not None:
+        ks, Hkv = _need_rows(k, "k", dev), k.shape[1]
+        if tuple(k.shape) != (T, Hkv, D):
+            raise ValueError("k must be [T, Hkv, D] matching q")
+    if rotary is not None:
+        if not isinstance(rotary, RotaryDesc):
+            raise TypeError("rotary must be a RotaryDesc (see rotary_desc)")
+        _need(positions, "positions", torch.int32, dev, 1)
+        if positions.shape[0] != T:
+            raise ValueError("positions must have one entry per token")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _need(w, name, torch.float32, dev, 1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must have head_dim entries")
+    outs = []
+    for name, x, o in (("q_out", q, q_out), ("k_out", k, k_out)):
+        if x is None:
+            if o is not None:
+                raise ValueError(f"{name} given without its input")
+        elif o is None:
+            o = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _need(o, name, torch.bfloat16, dev, 3)
+            if tuple(o.shape) != tuple(x.shape):
+                raise ValueError(f"{name} must have its input's shape")
+        outs.append(o)
+    desc = paged_desc(0, Hq, Hkv, D, 0, 0)
+    with torch.cuda.device(dev):
+        ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
+        _check(load().sinkattn_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                            _ptr(positions) if rotary is not None else None, T,
+                                            None if rotary is None else ctypes.byref(rotary), _ptr(outs[0]),
+                                            _ptr(outs[1]), ctypes.byref(desc), _ptr(ws), 0 if ws is None else ws.numel(),
+                                            _stream(dev)),
+               "sinkattn_qk_norm_rope")
+    return outs[0], outs[1]
