@@ -72,7 +72,8 @@ typedef enum sinkattn_error {
 #define SINKATTN_STATUS_BAD_LENGTH 0x2u     /* a length < 0 or > max_pages_per_seq * page_size */
 #define SINKATTN_STATUS_BAD_CU_SEQLENS 0x4u /* cu_seqlens not non-decreasing from 0 to total */
 #define SINKATTN_STATUS_WAIT_TIMEOUT 0x8u   /* a pipeline wait hit its iteration limit */
-#define SINKATTN_STATUS_VALUE_RANGE 0x10u   /* prefill: a V value with |v| >= 2^22 or not finite */
+#define SINKATTN_STATUS_VALUE_RANGE 0x10u   /* prefill: a V value with |v| >= 2^22 or not finite;
+                                             * INT8 append: a K or V value not finite */
 
 /* Shapes of a paged KV cache and of the heads that read it. */
 typedef struct sinkattn_paged_desc {
@@ -320,6 +321,38 @@ int sinkattn_append_kv_fp8(const void *k, const void *v, const float *k_scale,
                            const int32_t *block_table, const int32_t *start_pos, void *k_pages,
                            void *v_pages, const sinkattn_paged_desc *desc, void *workspace,
                            size_t ws_bytes, sinkattn_stream_t stream);
+
+/* ------------------------------------------------------------ INT8 KV cache --
+ * A KV cache of one byte per element with a scale for each page (16 tokens) and KV head, which
+ * needs no calibration and follows the data as it comes:
+ *   - k_pages, v_pages: int8 [num_pages, Hkv, 16, D] (the same HND layout), codes in -127 .. 127;
+ *   - kv_scales: fp32 [num_pages, Hkv, 2], 8-byte aligned: of K and of V, one pair beside the
+ *     other (a page's pair is one read).  Value of an element = scale * code.  Scales must be
+ *     finite and not negative; those of a page that holds no tokens are not used.
+ * An element is off by at most half its page's scale per rounding, i.e. 1/254 of the largest
+ * magnitude among the page's 16 x D rows of that head.
+ *
+ * sinkattn_append_kv_int8: new bf16 rows into the slots that sinkattn_append_kv would write.
+ * For the new rows of one (page, head), with amax their largest finite magnitude:
+ *     cand = amax / 127 rounded up to 8 significant bits (below 2^-100: 0)
+ *     s'   = cand if these rows begin at the page's slot 0, else max(s, cand), s the stored scale
+ *     code = x / s' rounded to the nearest integer, ties to even (0 if s' is 0)
+ * If s' > s, the codes c of the page's slots before the new rows become c * s / s', rounded the
+ * same way: a page filled token by token rounds its early rows again each time its scale grows.
+ * Slots behind the new rows are left as they were.  (With scales of more than 8 significant
+ * bits, written by other means, a quotient within 2^-12 of a tie may round either way.)
+ * Infinities take the code +-127 and NaN the code 0, and both set SINKATTN_STATUS_VALUE_RANGE.
+ * k, v:          bf16, row t at k + t * k_row_stride elements (>= Hkv * D, a multiple of 8):
+ *                [Hkv, D] dense, so K and V may lie inside a fused projection's rows
+ * kv_scales:     updated in place with the pages
+ * workspace:     optional, as for sinkattn_append_kv
+ * Two sequences of one call must not write to the same page.
+ * Other arguments and errors as for sinkattn_append_kv. */
+int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                            const int32_t *cu_seqlens, int32_t total_tokens, const int32_t *block_table,
+                            const int32_t *start_pos, void *k_pages, void *v_pages, float *kv_scales,
+                            const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                            sinkattn_stream_t stream);
 
 /* ------------------------------------------------- queries and keys before attention --
  * Per-head RMS norm and rotary position embedding of a step's queries and keys in one pass, for

@@ -703,6 +703,46 @@ int sinkattn_prefill_fp8(const void *q, const void *k, const void *v, const int3
                           v_scale, true, stream);
 }
 
+int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                            const int32_t *cu_seqlens, int32_t total_tokens, const int32_t *block_table,
+                            const int32_t *start_pos, void *k_pages, void *v_pages, float *kv_scales,
+                            const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                            sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
+    if (!k || !v || !cu_seqlens || !block_table || !start_pos || !k_pages || !v_pages || !kv_scales)
+        return SINKATTN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+        !aligned(kv_scales, 8) || !aligned(cu_seqlens, 4) || !aligned(block_table, 4) || !aligned(start_pos, 4))
+        return SINKATTN_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)desc->num_kv_heads * desc->head_dim;
+    if (k_row_stride < row || v_row_stride < row || k_row_stride % 8 || v_row_stride % 8)
+        return SINKATTN_ERR_INVALID_ARG;
+    if (workspace && (ws_bytes < kStatusBytes || !aligned(workspace, kAlign))) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_pages < 1 || desc->max_pages_per_seq < 1) return SINKATTN_ERR_INVALID_ARG;
+    AppendInt8Args a;
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_row_stride;
+    a.v_stride = v_row_stride;
+    a.cu_seqlens = cu_seqlens;
+    a.block_table = block_table;
+    a.start_pos = start_pos;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.kv_scales = kv_scales;
+    a.T = total_tokens;
+    a.n = desc->num_seqs;
+    a.Hkv = desc->num_kv_heads;
+    a.num_pages = desc->num_pages;
+    a.max_pages = desc->max_pages_per_seq;
+    a.group = 1;
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_rc(launch_append_int8(desc->head_dim, a, (cudaStream_t)stream), "int8 append launch");
+}
+
 int sinkattn_qk_norm_rope(const void *q, int64_t q_row_stride, const void *k, int64_t k_row_stride,
                           const float *q_weight, const float *k_weight, float eps, const int32_t *positions,
                           int32_t total_tokens, const sinkattn_rotary_desc *rotary, void *q_out, void *k_out,

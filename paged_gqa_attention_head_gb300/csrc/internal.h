@@ -87,6 +87,20 @@ struct AppendArgs {
 };
 cudaError_t launch_append_kv(const AppendArgs &a, cudaStream_t stream);
 
+struct AppendInt8Args {
+    const void *k, *v;           // bf16 [T] rows of [Hkv, D], `stride` elements apart
+    int64_t k_stride, v_stride;
+    const int32_t *cu_seqlens;
+    const int32_t *block_table;
+    const int32_t *start_pos;
+    void *k_pages, *v_pages;     // int8 [num_pages, Hkv, 16, D]
+    float *kv_scales;            // [num_pages, Hkv, 2]
+    int T, n, Hkv, num_pages, max_pages;
+    int group;                   // tokens a warp looks at (set by the launch)
+    uint32_t *status;            // or nullptr
+};
+cudaError_t launch_append_int8(int D, AppendInt8Args a, cudaStream_t stream);
+
 constexpr int kRotaryMaxPos = 1 << 24;  // positions stay exact floats below this
 struct RotaryArgs {
     const void *q, *k;           // bf16 [T] rows of [Hq, D] / [Hkv, D], `stride` elements apart; or nullptr

@@ -20,7 +20,11 @@ Recipe (shared by every workload):
   * FP8 E4M3 caches: per-KV-head scales s_g = (4.5 / 448) * (1 + g / (2 Hkv)),
     codes = torch's float8_e4m3fn cast of the standard normal float32 values
     divided by s_g and clipped to [-448, 448]; poisoned slots hold the NaN code
-    0x7F.
+    0x7F;
+  * INT8 caches: each (page, KV head) of standard normal float32 values times a magnitude of its
+    own, e^U(-1.5, 1.5), quantised by its largest value (scale = that / 127 rounded up to 8
+    significant bits); poisoned slots hold the code -128, which no value takes, and distractor
+    pages NaN scales.
 
 Random streams are keyed by (seed, stream id, chunk index) through numpy's
 SeedSequence, so a tensor's contents do not depend on the thread count or on
@@ -43,7 +47,7 @@ BF16_NAN_BITS = 0x7FC0
 E4M3_NAN_CODE = 0x7F
 
 # stream ids: one per kind of tensor so that draws are independent
-_S_LENS, _S_Q, _S_K, _S_V, _S_SINK, _S_PERM, _S_KNEW, _S_VNEW, _S_PREFIX = range(9)
+_S_LENS, _S_Q, _S_K, _S_V, _S_SINK, _S_PERM, _S_KNEW, _S_VNEW, _S_PREFIX, _S_MAG = range(10)
 
 
 def _rng(seed: int, stream: int, chunk: int = 0) -> np.random.Generator:
@@ -121,9 +125,37 @@ def normal_e4m3(shape, head_scales: torch.Tensor, seed: int, stream: int) -> tor
     return out.reshape(shape)
 
 
+def int8_scale(amax: torch.Tensor) -> torch.Tensor:
+    """amax / 127 rounded up to 8 significant bits (float32)."""
+    bits = (amax.float() / 127.0).view(torch.int32)
+    return ((bits + 0xFFFF) & -65536).view(torch.float32)
+
+
+def normal_int8(shape, seed: int, stream: int):
+    """INT8 codes of pages [num_pages, Hkv, 16, D] and their scales [num_pages, Hkv]."""
+    pages, heads = shape[:2]
+    mag = np.exp(_rng(seed, _S_MAG, stream).uniform(-1.5, 1.5, size=(pages, heads))).astype(np.float32)
+    codes, scales = torch.empty(shape, dtype=torch.int8), torch.empty(pages, heads)
+    step = max(1, _CHUNK // int(np.prod(shape[1:])))
+
+    def work(i: int) -> None:
+        lo, hi = i * step, min(pages, (i + 1) * step)
+        x = _rng(seed, stream, i).standard_normal((hi - lo,) + tuple(shape[1:]), dtype=np.float32)
+        x = torch.from_numpy(x * mag[lo:hi, :, None, None])
+        scales[lo:hi] = int8_scale(x.abs().amax(dim=(2, 3)))
+        codes[lo:hi] = torch.round(x / scales[lo:hi, :, None, None]).clamp(-127, 127).to(torch.int8)
+
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as ex:
+        list(ex.map(work, range((pages + step - 1) // step)))
+    return codes, scales
+
+
 def poison_rows_(t: torch.Tensor) -> None:
-    """Fill a bf16 tensor (view) with NaN; a uint8 (E4M3 code) tensor with the NaN code."""
-    if t.dtype == torch.uint8:
+    """Fill a bf16 tensor (view) with NaN; a uint8 (E4M3 code) tensor with the NaN code; an int8
+    tensor with the code -128."""
+    if t.dtype == torch.int8:
+        t.fill_(-128)
+    elif t.dtype == torch.uint8:
         t.fill_(E4M3_NAN_CODE)
     else:
         t.view(torch.int16).fill_(BF16_NAN_BITS)
@@ -146,8 +178,8 @@ def draw_lengths(spec, count: int, seed: int) -> list[int]:
 
 @dataclass
 class PagedCache:
-    """KV pages [num_pages, Hkv, 16, D] (bf16, or uint8 E4M3 codes with per-head
-    scales) plus the block table of each sequence."""
+    """KV pages [num_pages, Hkv, 16, D] (bf16, uint8 E4M3 codes with per-head scales, or int8
+    codes with per-page scales) plus the block table of each sequence."""
     k_pages: torch.Tensor
     v_pages: torch.Tensor
     block_table: torch.Tensor  # [num_seqs, max_pages_per_seq] int32, unused = -1
@@ -155,6 +187,7 @@ class PagedCache:
     num_pages: int = 0
     k_scale: Optional[torch.Tensor] = None  # [Hkv] float32 (FP8 caches only)
     v_scale: Optional[torch.Tensor] = None
+    kv_scales: Optional[torch.Tensor] = None  # [num_pages, Hkv, 2] float32 (INT8 caches only)
 
     @property
     def fp8(self) -> bool:
@@ -173,8 +206,12 @@ def make_paged_cache(lens: list[int], num_kv_heads: int, head_dim: int, seed: in
     maxp = max_pages_per_seq if max_pages_per_seq is not None else max(1, max(npages_seq, default=1))
     perm = _rng(seed, _S_PERM).permutation(num_pages).astype(np.int64)
     shape = (num_pages, num_kv_heads, PAGE_SIZE, head_dim)
-    ks = vs = None
-    if kv_dtype == "fp8":
+    ks = vs = kv_scales = None
+    if kv_dtype == "int8":
+        k_pages, k_sc = normal_int8(shape, seed, k_stream)
+        v_pages, v_sc = normal_int8(shape, seed, v_stream)
+        kv_scales = torch.stack([k_sc, v_sc], dim=-1).contiguous()
+    elif kv_dtype == "fp8":
         if fp8_unit_scales:  # codes are the N(0,1) values themselves
             ks = vs = torch.ones(num_kv_heads, dtype=torch.float32)
         else:
@@ -198,12 +235,17 @@ def make_paged_cache(lens: list[int], num_kv_heads: int, head_dim: int, seed: in
             poison_rows_(v_pages[last, :, L % PAGE_SIZE:, :])
     if poison and num_pages > used:
         idx = torch.from_numpy(perm[used:])
+        if kv_dtype == "int8":
+            kv_scales[idx] = math.nan
         for pages in (k_pages, v_pages):
-            if kv_dtype == "fp8":
+            if kv_dtype == "int8":
+                pages[idx] = -128
+            elif kv_dtype == "fp8":
                 pages[idx] = E4M3_NAN_CODE
             else:
                 pages.view(torch.int16)[idx] = BF16_NAN_BITS
-    return PagedCache(k_pages, v_pages, bt, torch.tensor(lens, dtype=torch.int32), num_pages, ks, vs)
+    return PagedCache(k_pages, v_pages, bt, torch.tensor(lens, dtype=torch.int32), num_pages, ks, vs,
+                      kv_scales)
 
 
 @dataclass
@@ -226,7 +268,7 @@ class DecodeInputs:
         lens = self.cache.lens.long()
         if window > 0:
             lens = lens.clamp(max=window)
-        elem = 1 if self.cache.fp8 else 2
+        elem = self.cache.k_pages.element_size()
         return int(lens.sum()) * 2 * self.num_kv_heads * self.head_dim * elem
 
 
@@ -234,8 +276,8 @@ def make_decode(lens_spec, batch: int, num_qo_heads: int, num_kv_heads: int, hea
                 seed: int = 0, sinks: bool = True, scale: Optional[float] = None,
                 poison: bool = True, distractor_frac: float = 0.05,
                 kv_dtype: str = "bf16", fp8_unit_scales: bool = False) -> DecodeInputs:
-    """kv_dtype "bf16" or "fp8" (E4M3 codes with per-KV-head scales; fp8_unit_scales:
-    all scales 1, the codes then encode the N(0,1) values directly)."""
+    """kv_dtype "bf16", "fp8" (E4M3 codes with per-KV-head scales; fp8_unit_scales:
+    all scales 1, the codes then encode the N(0,1) values directly) or "int8"."""
     lens = draw_lengths(lens_spec, batch, seed)
     cache = make_paged_cache(lens, num_kv_heads, head_dim, seed, distractor_frac, poison,
                              kv_dtype=kv_dtype, fp8_unit_scales=fp8_unit_scales)

@@ -77,6 +77,8 @@ SIGNATURES = {
                                                    _P, _SZ, _P]),
     "sinkattn_append_kv_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _DP, _P, _SZ,
                                               _P]),
+    "sinkattn_append_kv_int8": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _DP, _P,
+                                               _SZ, _P]),
     "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
                                              ctypes.POINTER(RotaryDesc), _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
@@ -654,3 +656,42 @@ def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_we
                                             _stream(dev)),
                "sinkattn_qk_norm_rope")
     return outs[0], outs[1]
+
+
+# ---------------------------------------------------------------- INT8 cache
+def _need_int8_cache(k_pages, v_pages, kv_scales, device):
+    _need(k_pages, "k_pages", torch.int8, device, 4)
+    _need(v_pages, "v_pages", torch.int8, device, 4)
+    _need(kv_scales, "kv_scales", torch.float32, device, 3)
+    if v_pages.shape != k_pages.shape or k_pages.shape[2] != PAGE_SIZE:
+        raise ValueError("k_pages / v_pages must both be [num_pages, Hkv, 16, D]")
+    if tuple(kv_scales.shape) != (k_pages.shape[0], k_pages.shape[1], 2):
+        raise ValueError("kv_scales must be [num_pages, Hkv, 2] (of K and of V)")
+
+
+def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, kv_scales,
+                   workspace_buf=None):
+    """Quantise new bf16 K/V rows into an INT8 cache in place (sinkattn_append_kv_int8): k_pages /
+    v_pages int8 [num_pages, Hkv, 16, D], kv_scales float32 [num_pages, Hkv, 2], all three updated;
+    k, v [T, Hkv, D], each token's heads dense (parts of a fused projection's rows will do)."""
+    dev = _need_cuda(k, "k")
+    ks, vs = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(start_pos, "start_pos", torch.int32, dev, 1)
+    _need_int8_cache(k_pages, v_pages, kv_scales, dev)
+    T, Hkv, D = k.shape
+    n = cu_seqlens.shape[0] - 1
+    if tuple(v.shape) != (T, Hkv, D) or (k_pages.shape[1], k_pages.shape[3]) != (Hkv, D):
+        raise ValueError("k, v must be [T, Hkv, D] matching the pages")
+    if n < 0 or block_table.shape[0] != n or start_pos.shape[0] != n:
+        raise ValueError("block_table / start_pos rows must equal the sequences of cu_seqlens")
+    desc = paged_desc(n, Hkv, Hkv, D, k_pages.shape[0], block_table.shape[1])
+    with torch.cuda.device(dev):
+        ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
+        _check(load().sinkattn_append_kv_int8(_ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), T, _ptr(block_table),
+                                              _ptr(start_pos), _ptr(k_pages), _ptr(v_pages), _ptr(kv_scales),
+                                              ctypes.byref(desc), _ptr(ws), 0 if ws is None else ws.numel(),
+                                              _stream(dev)),
+               "sinkattn_append_kv_int8")
+    return k_pages, v_pages, kv_scales
