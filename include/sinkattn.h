@@ -21,7 +21,7 @@
  *     token j of sequence b is slot j % page_size of page block_table[b][j / page_size]
  *     block_table: int32 [num_seqs, max_pages_per_seq], row-major
  *
- * Supported: bf16 data (and FP8 E4M3 KV caches for decode, append and the prefix of a
+ * Supported: bf16 data (and FP8 E4M3 and INT8 KV caches for decode, append and the prefix of a
  * chunked prefill, see below),
  * fp32 sinks, head_dim 64 or 128, page_size 16, num_qo_heads / num_kv_heads in
  * {1, 2, 4, 8, 16}.
@@ -353,6 +353,18 @@ int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, 
                             const int32_t *start_pos, void *k_pages, void *v_pages, float *kv_scales,
                             const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
                             sinkattn_stream_t stream);
+
+/* The decode over such a cache (q, block_table, seq_lens, sinks, scale, out, lse, descriptor,
+ * window and status as for sinkattn_decode; workspace of sinkattn_decode_workspace_size).
+ * Codes enter the products exactly, scales multiply fp32 sums; q is taken in fp16 times a power
+ * of two of its (sequence, KV head): an entry keeps its 8 bits unless it is more than 2^28 times
+ * smaller than the largest of its group.  The probabilities are rounded to fp16 (relative
+ * 2^-11 each at most), as in sinkattn_decode_fp8.  (With a sliding window it runs the split-KV
+ * kernel too, over the visible pages.) */
+int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
+                         const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
+                         void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                         sinkattn_stream_t stream);
 
 /* ------------------------------------------------- queries and keys before attention --
  * Per-head RMS norm and rotary position embedding of a step's queries and keys in one pass, for

@@ -134,7 +134,9 @@ struct DecodeLayout {
     int ctas8, warps_per_cta8, smem8, total_warps8;  // FP8 cache kernel
 };
 
-int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
+// int8: ctas8 / smem8 are those of the decode over an INT8 cache, on a grid of at most the FP8
+// kernel's size (the slots are sized for that one).
+int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L, bool int8 = false) {
     int device = 0;
     int rc = cuda_rc(cudaGetDevice(&device), "cudaGetDevice");
     if (rc) return rc;
@@ -144,10 +146,17 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
                                      &L->smem, &ring),
                  "decode launch shape");
     if (rc) return rc;
-    rc = cuda_rc(decode_fp8_launch_shape(d->head_dim, G, d->num_seqs, device, &L->ctas8,
+    rc = cuda_rc(decode_fp8_launch_shape(d->head_dim, G, d->num_seqs, device, false, &L->ctas8,
                                          &L->warps_per_cta8, &L->smem8),
                  "fp8 decode launch shape");
     if (rc) return rc;
+    int ctas_int8 = 0;
+    if (int8) {
+        rc = cuda_rc(decode_fp8_launch_shape(d->head_dim, G, d->num_seqs, device, true, &ctas_int8,
+                                             &L->warps_per_cta8, &L->smem8),
+                     "int8 decode launch shape");
+        if (rc) return rc;
+    }
     // Both grids are (SMs x CTAs per SM); keep the CTAs per SM, on fewer SMs' worth of CTAs
     // where max_sms asks for it.  The bf16 split-KV grid also stops at kDecodeInflightBytes of
     // page copies in flight: with every SM at full occupancy its rings hold 25-29 MB, and HBM
@@ -182,6 +191,10 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
     L->acc = off;
     off += slots * G * d->head_dim * sizeof(float);
     L->total = align_up(off);
+    if (int8) {
+        if (ctas_int8 < L->ctas8) L->ctas8 = ctas_int8;
+        L->total_warps8 = L->ctas8 * L->warps_per_cta8;
+    }
     return SINKATTN_OK;
 }
 
@@ -194,7 +207,7 @@ struct DecodePrep {
 int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq_lens,
                    const float *sinks, float scale, void *out, float *lse,
                    const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
-                   DecodePrep *P) {
+                   DecodePrep *P, bool int8 = false) {
     int rc = check_decode_desc(desc);
     if (rc) return rc;
     if (!q || !block_table || !seq_lens || !out || !workspace) return SINKATTN_ERR_INVALID_ARG;
@@ -202,7 +215,7 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || (sinks && !aligned(sinks, 4)) ||
         (lse && !aligned(lse, 4)))
         return SINKATTN_ERR_INVALID_ARG;
-    rc = decode_layout(desc, &P->layout);
+    rc = decode_layout(desc, &P->layout, int8);
     if (rc) return rc;
     if (ws_bytes < P->layout.total) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
     DecodeArgs &a = P->args;
@@ -231,6 +244,7 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
     a.part_acc = reinterpret_cast<float *>(ws + P->layout.acc);
     a.k_scale = nullptr;
     a.v_scale = nullptr;
+    a.kv_scales = nullptr;
     a.k_new = nullptr;
     a.v_new = nullptr;
     a.k_pages_w = nullptr;
@@ -580,6 +594,32 @@ int sinkattn_decode_fp8(const void *q, const void *k_pages, const void *v_pages,
                                          ws_bytes, stream);
     if (rc) return rc;
     return sinkattn_decode_merge(seq_lens, sinks, out, lse, desc, workspace, ws_bytes, stream);
+}
+
+int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
+                         const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
+                         void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                         sinkattn_stream_t stream) {
+    // an empty batch is a no-op (its data pointers may be NULL)
+    if (desc && desc->num_seqs == 0) return check_decode_desc(desc);
+    if (!k_pages || !v_pages || !kv_scales || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+        !aligned(kv_scales, 8))
+        return SINKATTN_ERR_INVALID_ARG;
+    DecodePrep P;
+    int rc = prepare_decode(q, block_table, seq_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, &P, true);
+    if (rc) return rc;
+    CUtensorMap kmap, vmap;
+    rc = encode_pages_map_fp8(&kmap, k_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
+    if (rc) return rc;
+    rc = encode_pages_map_fp8(&vmap, v_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
+    if (rc) return rc;
+    P.args.kv_scales = kv_scales;
+    P.args.total_warps = P.layout.total_warps8;
+    rc = cuda_rc(launch_decode_fp8(desc->head_dim, P.args, kmap, vmap, P.layout.ctas8, P.layout.smem8,
+                                   (cudaStream_t)stream),
+                 "int8 split-KV decode launch");
+    if (rc) return rc;
+    return cuda_rc(launch_decode_merge(desc->head_dim, P.args, (cudaStream_t)stream), "merge launch");
 }
 
 int sinkattn_prefill_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {

@@ -38,6 +38,7 @@ struct DecodeArgs {
     float *part_acc;        // [slots, G, D] partial unnormalised outputs
     const float *k_scale;   // FP8 cache: [Hkv] per-KV-head scales, or nullptr (1)
     const float *v_scale;
+    const float *kv_scales;  // INT8 cache: [num_pages, Hkv, 2] scales (K, V); nullptr: not an INT8 cache
     const void *k_new;      // decode with append: bf16 [B, Hkv, D] new rows, or nullptr
     const void *v_new;
     void *k_pages_w;        // the cache the new rows are written into (decode with append)
@@ -69,7 +70,8 @@ cudaError_t launch_decode_window(int D, const DecodeArgs &a, const CUtensorMap &
                                  const CUtensorMap &vmap, cudaStream_t stream);
 
 // The same for the decode over an FP8 E4M3 cache (uint8 tensor maps, one box per page).
-cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
+// int8: the kernel over an INT8 cache (a.kv_scales set at the launch).
+cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, bool int8, int *ctas, int *warps_per_cta,
                                     int *smem_bytes);
 cudaError_t launch_decode_fp8(int D, const DecodeArgs &a, const CUtensorMap &kmap,
                               const CUtensorMap &vmap, int ctas, int smem_bytes, cudaStream_t stream);

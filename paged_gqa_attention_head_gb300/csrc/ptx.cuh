@@ -256,6 +256,20 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t w) {
     return r;
 }
 
+// Two INT8 codes of a word whose sign bits were flipped (code + 128 in each byte; bits 0-15 or
+// 16-31) to an f16 pair, exact: under the high byte of 1024 (0x64) a byte is 1152 + code.
+__device__ __forceinline__ uint32_t f16x2_minus_1152(uint32_t h) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+    return r;
+}
+__device__ __forceinline__ uint32_t int8x2_lo_to_f16x2(uint32_t w) {
+    return f16x2_minus_1152(__byte_perm(w, 0x64646464u, 0x4140));
+}
+__device__ __forceinline__ uint32_t int8x2_hi_to_f16x2(uint32_t w) {
+    return f16x2_minus_1152(__byte_perm(w, 0x64646464u, 0x4342));
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -79,6 +79,7 @@ SIGNATURES = {
                                               _P]),
     "sinkattn_append_kv_int8": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _DP, _P,
                                                _SZ, _P]),
+    "sinkattn_decode_int8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
                                              ctypes.POINTER(RotaryDesc), _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
@@ -151,6 +152,31 @@ def workspace(nbytes: int, device: torch.device, tag: str = "default") -> torch.
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         _workspaces[key] = ws
+    return ws
+
+
+_stream_workspaces: dict = {}
+_retired_workspaces: list = []  # replaced by larger ones; a captured graph may hold their addresses
+
+
+def _stream_workspace(nbytes: int, device: torch.device, tag: str) -> torch.Tensor:
+    """Default scratch of a call on the current stream: one buffer per (device, stream, tag), so
+    that calls on two streams never share one.  While the stream is captured the call gets a buffer
+    of its own in the graph's memory, whose header the graph clears at each replay; so no two
+    graphs, and no graph and an eager call, share one."""
+    stream = _stream(device)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _check(load().sinkattn_workspace_init(_ptr(ws), ws.numel(), stream), "sinkattn_workspace_init")
+        return ws
+    key = (device, stream, tag)
+    ws = _stream_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _retired_workspaces.append(ws)
+            nbytes = max(nbytes, 2 * ws.numel())
+        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        _stream_workspaces[key] = ws
     return ws
 
 
@@ -695,3 +721,30 @@ def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, k
                                               _stream(dev)),
                "sinkattn_append_kv_int8")
     return k_pages, v_pages, kv_scales
+
+
+def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=None, scale=None, out=None,
+                lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0, wait_limit_us=0):
+    """Split-KV paged decode over an INT8 cache with a scale per page and KV head
+    (sinkattn_decode_int8).  Returns (out, lse)."""
+    dev = _need_cuda(q, "q")
+    _need(q, "q", torch.bfloat16, dev, 3)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need_int8_cache(k_pages, v_pages, kv_scales, dev)
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [B, Hq]")
+    with torch.cuda.device(dev):
+        if workspace_buf is None:
+            desc = paged_desc(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], k_pages.shape[0],
+                              block_table.shape[1], window=window, max_sms=max_sms, wait_limit_us=wait_limit_us)
+            workspace_buf = _stream_workspace(decode_workspace_size(desc), dev, "decode")
+        desc, out, lse, ws, scale = _decode_prep(q, k_pages, v_pages, block_table, seq_lens, sinks, scale, out, lse,
+                                                 workspace_buf, return_lse, window, kv_dtype=torch.int8,
+                                                 max_sms=max_sms, wait_limit_us=wait_limit_us)
+        _check(load().sinkattn_decode_int8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_scales), _ptr(block_table),
+                                           _ptr(seq_lens), _ptr(sinks), scale, _ptr(out), _ptr(lse),
+                                           ctypes.byref(desc), _ptr(ws), ws.numel(), _stream(dev)),
+               "sinkattn_decode_int8")
+    return out, lse
