@@ -73,7 +73,8 @@ typedef enum sinkattn_error {
 #define SINKATTN_STATUS_BAD_CU_SEQLENS 0x4u /* cu_seqlens not non-decreasing from 0 to total */
 #define SINKATTN_STATUS_WAIT_TIMEOUT 0x8u   /* a pipeline wait hit its iteration limit */
 #define SINKATTN_STATUS_VALUE_RANGE 0x10u   /* prefill: a V value with |v| >= 2^22 or not finite;
-                                             * INT8 append: a K or V value not finite */
+                                             * INT8 append: a K or V value not finite;
+                                             * INT8 prefill: a V scale of 2^15 or more */
 
 /* Shapes of a paged KV cache and of the heads that read it. */
 typedef struct sinkattn_paged_desc {
@@ -365,6 +366,19 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
                          const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
                          void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
                          sinkattn_stream_t stream);
+
+/* Chunked prefill over such a prefix: sinkattn_prefill with the prefix pages in INT8 (all four
+ * prefix pointers, the scales and the prefix lengths are required; prefix lengths may be 0); the
+ * new tokens' k, v stay bf16.  Prefix codes enter the products exactly, each page's scales join
+ * the softmax in fp32; V scales of 2^15 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then
+ * unspecified), and below 2^-24 the fp16 P loses bits.  Other arguments, workspace and errors as
+ * for sinkattn_prefill. */
+int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                          int32_t total_tokens, const void *k_pages, const void *v_pages,
+                          const float *kv_scales, const int32_t *prefix_block_table,
+                          const int32_t *prefix_lens, const float *sinks, float scale, void *out, float *lse,
+                          const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                          sinkattn_stream_t stream);
 
 /* ------------------------------------------------- queries and keys before attention --
  * Per-head RMS norm and rotary position embedding of a step's queries and keys in one pass, for

@@ -636,7 +636,7 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
                    const int32_t *prefix_block_table, const int32_t *prefix_lens, const float *sinks,
                    float scale, void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace,
                    size_t ws_bytes, bool fp8, const float *k_scale, const float *v_scale,
-                   bool causal, sinkattn_stream_t stream) {
+                   bool causal, sinkattn_stream_t stream, const float *kv_scales = nullptr) {
     int rc = check_heads(desc);
     if (rc) return rc;
     if (!causal && desc->window > 0) return SINKATTN_ERR_INVALID_ARG;
@@ -666,7 +666,7 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
     if ((rc = encode_rows_map(&vmap, v, total_tokens, Hkv, D, 128))) return rc;
     if (fp8 && !has_prefix) return SINKATTN_ERR_INVALID_ARG;
     if ((k_scale && !aligned(k_scale, 4)) || (v_scale && !aligned(v_scale, 4))) return SINKATTN_ERR_INVALID_ARG;
-    if (has_prefix && fp8) {
+    if (has_prefix && (fp8 || kv_scales)) {  // one-byte codes
         if ((rc = encode_pages_map_fp8(&kpmap, k_pages, desc->num_pages, Hkv, D, false))) return rc;
         if ((rc = encode_pages_map_fp8(&vpmap, v_pages, desc->num_pages, Hkv, D, false))) return rc;
     } else if (has_prefix) {
@@ -705,6 +705,7 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
     a.sched = static_cast<uint32_t *>(workspace) + 16;  // header bytes 64..71
     a.k_scale = k_scale;
     a.v_scale = v_scale;
+    a.kv_scales = kv_scales;
     cudaError_t e = launch_prefill(a, qmap, kmap, vmap, kpmap, vpmap, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) return SINKATTN_ERR_UNSUPPORTED;
     return cuda_rc(e, "prefill launch");
@@ -741,6 +742,23 @@ int sinkattn_prefill_fp8(const void *q, const void *k, const void *v, const int3
     return prefill_common(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, prefix_block_table,
                           prefix_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, true, k_scale,
                           v_scale, true, stream);
+}
+
+int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                          int32_t total_tokens, const void *k_pages, const void *v_pages,
+                          const float *kv_scales, const int32_t *prefix_block_table,
+                          const int32_t *prefix_lens, const float *sinks, float scale, void *out, float *lse,
+                          const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                          sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
+    if (!k_pages || !v_pages || !kv_scales || !aligned(kv_scales, 8) || !prefix_block_table || !prefix_lens)
+        return SINKATTN_ERR_INVALID_ARG;
+    return prefill_common(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, prefix_block_table,
+                          prefix_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, false, nullptr,
+                          nullptr, true, stream, kv_scales);
 }
 
 int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,

@@ -141,6 +141,7 @@ struct PrefillArgs {
     bool launch_dependents;            // the next kernel on the stream may start at once
     uint32_t *sched;                   // [2] in the workspace header: next item, CTAs done (zero between calls)
     const float *k_scale, *v_scale;    // FP8 prefix: [Hkv] per-KV-head scales, or nullptr (1)
+    const float *kv_scales;            // INT8 prefix: [num_pages, Hkv, 2] scales (K, V); nullptr: not INT8
 };
 // Tensor maps: q [T, Hq, D], k/v [T, Hkv, D] (new tokens), kp/vp prefix pages.
 cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &qmap, const CUtensorMap &kmap,

@@ -73,6 +73,20 @@ constexpr int kLocateMax = 1024;  // requests / levels of the shared-memory tile
 // the producer posts to it again.
 constexpr int kItemRing = 16;
 
+// INT8 prefix: what the softmax needs of the eight pages of a key tile.  With the page's V
+// scale m * 2^e (m in [1, 2)) the V tile holds code * 2^e', exact in fp16, and P is taken times
+// rest = m * 2^(e - e'), which joins the exponent of P as add = log2(rest) and leaves the row
+// sum by mul = 1 / rest; e' is e where -24 <= e <= 8 (127 * 2^8 < 2^15), else the nearest end.
+// Tiles of new tokens use the same fields: k the score scale, add and mul the V exponents.
+struct PageScales {
+    float k[8];      // score factor: K scale * softmax scale * log2(e)
+    float add[8];    // V: what the exponent of P gains
+    float mul[8];    // V: what a sum of such P is multiplied by
+    uint32_t v2[8];  // V: 2^e' as a pair of fp16
+};
+constexpr int kPageScaleBytes = 128;
+static_assert(sizeof(PageScales) == kPageScaleBytes, "page scales");
+
 // QB: Q buffers.  Two at head_dim 64 with a sliding window, where items are one or two key
 // tiles long: the next item's Q tiles load while the current item's S products still read
 // its own (measured: 12 % faster window-128 prefill; 2 % slower causal prefill, whose longer
@@ -95,7 +109,8 @@ struct PrefillCfg {
     static constexpr int kOffLoc = kOffBar + ((kNumBars * 8 + 127) / 128) * 128;
     static constexpr int kOffMisc = kOffLoc + 4 * kLocateMax * 4;
     static constexpr int kOffSlot = kOffMisc + 256;  // [kItemRing] ItemSlot, 64 bytes each
-    static constexpr int kSmemBytes = 1024 + kOffSlot + kItemRing * 64;
+    static constexpr int kOffPage = kOffSlot + kItemRing * 64;  // INT8 prefix: [kStages] PageScales
+    static constexpr int kSmemBytes = 1024 + kOffPage + kStages * kPageScaleBytes;
     __host__ __device__ static constexpr uint32_t kColS(int b) { return 128u * b; }
     __host__ __device__ static constexpr uint32_t kColP(int p) {
         return kSplitP ? 128u * kSBufs + 64u * p : 128u * p;
@@ -181,10 +196,23 @@ __device__ __forceinline__ uint32_t f16x2_pow2(uint32_t h, uint32_t p2) {
     return r;
 }
 
+// Eight INT8 codes (two words) to one 16-byte vector: bf16 codes (kMode 3) or fp16 codes times
+// the power of two p2 (4), both exact.
+template <int kMode>
+__device__ __forceinline__ uint4 int8x8(uint32_t w0, uint32_t w1, uint32_t p2) {
+    w0 ^= 0x80808080u;
+    w1 ^= 0x80808080u;
+    const uint32_t h0 = int8x2_lo_to_f16x2(w0), h1 = int8x2_hi_to_f16x2(w0);
+    const uint32_t h2 = int8x2_lo_to_f16x2(w1), h3 = int8x2_hi_to_f16x2(w1);
+    if (kMode == 3) return make_uint4(f16x2_to_bf16x2(h0), f16x2_to_bf16x2(h1), f16x2_to_bf16x2(h2), f16x2_to_bf16x2(h3));
+    return make_uint4(f16x2_pow2(h0, p2), f16x2_pow2(h1, p2), f16x2_pow2(h2, p2), f16x2_pow2(h3, p2));
+}
+
 // Eight E4M3 codes (two words) to one 16-byte vector: bf16 code values (kMode 0), fp16 code
 // values times sc (1), or fp16 code values times the power of two p2 (2).
 template <int kMode>
 __device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, float sc, uint32_t p2) {
+    if (kMode >= 3) return int8x8<kMode>(w0, w1, p2);
     const uint32_t h0 = e4m3x2_lo_to_f16x2(w0), h1 = e4m3x2_hi_to_f16x2(w0);
     const uint32_t h2 = e4m3x2_lo_to_f16x2(w1), h3 = e4m3x2_hi_to_f16x2(w1);
     if (kMode == 0) return make_uint4(f16x2_to_bf16x2(h0), f16x2_to_bf16x2(h1), f16x2_to_bf16x2(h2), f16x2_to_bf16x2(h3));
@@ -192,17 +220,20 @@ __device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, float sc, uint
     return make_uint4(f16x2_scaled(h0, sc), f16x2_scaled(h1, sc), f16x2_scaled(h2, sc), f16x2_scaled(h3, sc));
 }
 
-// One converter warp's quarter of an FP8 prefix tile (keys 32q .. 32q + 31, pages 2q and
-// 2q + 1) from its staged codes to 128-byte swizzled rows in place: bf16 code values for K,
-// fp16 code values times sc (kMode 1) or times the power of two p2 (kMode 2) for V.  Every
+// One converter warp's quarter of an FP8 or INT8 prefix tile (keys 32q .. 32q + 31, pages 2q and
+// 2q + 1) from its staged codes to 128-byte swizzled rows in place: bf16 code values for K
+// (kMode 0, INT8: 3), fp16 code values times sc (kMode 1) or times the power of two p2 (kMode 2;
+// INT8: 4, one for each page) for V.  Every
 // lane reads its codes of a page (or half page) before any lane writes, since the rows
 // written cover the codes staged.
 template <int D, int kMode>
-__device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane, float sc, uint32_t p2 = 0) {
+__device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane, float sc, uint32_t p2 = 0,
+                                                    const uint32_t *page_p2 = nullptr) {
     using C = PrefillCfg<D>;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const int p = 2 * q + i;
+        if (kMode == 4) p2 = page_p2[p];
         const uint8_t *src = t + C::kOffFp8Page(p);
         if (D == 64) {
             // lane: row r, codes 32h .. 32h + 31 -> 16-byte chunks 4h .. 4h + 3 of row 16p + r
@@ -495,8 +526,11 @@ static_assert(sizeof(ItemSlot) == 64, "item slot");
 // which each query row sees all keys of its request.  kFp8: the paged prefix is an FP8 E4M3 cache (value = scale[g] *
 // e4m3(code)); its tiles are staged as codes and converted in shared memory by the
 // converter warps - K to bf16 code values (exact; the K scale joins the score scale of
-// those tiles), V to fp16 value * 2^-k like the bf16 V tiles.
-template <int D, bool kWindow, bool kFp8, bool kCausal>
+// those tiles), V to fp16 value * 2^-k like the bf16 V tiles.  kInt8: it is an INT8 cache with a
+// scale per page and head: the same staging and conversion, the scales of a tile's eight pages
+// looked up by the producer with the pages and applied by the softmax page by page (16 columns
+// of S), so that no code or scale is rounded.
+template <int D, bool kWindow, bool kFp8, bool kCausal, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kpmap,
@@ -536,6 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *s_abort = misc + 1;
     int *s_vscale = misc + 32;  // [NS][4] exponent k of each 32-key quarter of each V tile
     ItemSlot *s_slot = reinterpret_cast<ItemSlot *>(smem + C::kOffSlot);  // the k-th item in slot k % kItemRing
+    PageScales *s_page = reinterpret_cast<PageScales *>(smem + C::kOffPage);  // INT8: [NS]
+    constexpr bool kCodes = kFp8 || kInt8;  // the prefix tiles are staged as one-byte codes
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -658,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // prefix tile: lane p < 8 looks up page 8tt + p (issued before the wait below so
                 // the load overlaps it); nrow = its valid rows, pg = -1 for a missing page
                 int nrow = 0, pg = -1;
+                float2 psc = make_float2(1.f, 1.f);  // INT8: the page's scales (K, V)
                 if (tt < gm.n_pre && lane < 8) {
                     const int page = tt * 8 + lane;
                     nrow = min(kPageSize, max(0, gm.P - page * kPageSize));
@@ -668,6 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pg = -1;
                         }
                     }
+                    if (kInt8 && pg >= 0)
+                        psc = __ldg(reinterpret_cast<const float2 *>(a.kv_scales) + (int64_t)pg * a.Hkv + gm.g);
                 }
                 if (u > 0 &&
                     !wait_or_abort<true>(&bars.kv_empty[s], (uint32_t)((u - 1) & 1), s_abort, a.status, a.wait_limit_cycles)) {
@@ -676,8 +715,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint8_t *kt = sK + s * C::kKVBytes;
                 uint8_t *vt = sV + s * C::kKVBytes;
-                if (kFp8 && tt < gm.n_pre) {
-                    // eight FP8 pages of 16 tokens, as codes into their staging places: each
+                if (kInt8) {
+                    if (lane < 8) {
+                        PageScales &ps = s_page[s];
+                        if (tt < gm.n_pre) {
+                            const int e = (int)((__float_as_uint(psc.y) >> 23) & 0xFFu) - 127;
+                            const int e2 = min(max(e, -24), 8);
+                            // V scale / 2^e2 (a scale of 0: any factor, the values are 0 by e' alone)
+                            const float rest = psc.y > 0.f ? psc.y * __uint_as_float((uint32_t)(127 - e2) << 23) : 1.f;
+                            // 2^e2 in fp16: a normal from 2^-14 up, a subnormal below
+                            const uint32_t h = !(psc.y > 0.f) ? 0u : e2 >= -14 ? (uint32_t)(e2 + 15) << 10 : 1u << (e2 + 24);
+                            // never 0, so that a hidden key's -inf stays one
+                            ps.k[lane] = fmaxf(a.scale_log2 * psc.x, 1e-37f);
+                            ps.add[lane] = log2f(rest);
+                            ps.mul[lane] = 1.f / rest;
+                            ps.v2[lane] = h | h << 16;
+                            // P * rest must stay in fp16: P <= 2^8, so rest < 2^7
+                            if (!(psc.y < 32768.f)) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
+                        } else {
+                            ps.k[lane] = a.scale_log2;  // add and mul come from the converters
+                        }
+                    }
+                    __syncwarp();  // before lane 0 arrives on the stage's barriers
+                }
+                if (kCodes && tt < gm.n_pre) {
+                    // eight FP8 or INT8 pages of 16 tokens, as codes into their staging places: each
                     // whole valid page by a TMA issued from its own lane (one box of 16 rows x D
                     // bytes), the others by the warp (valid rows copied, the rest code 0 = 0.0)
                     const bool full = nrow == kPageSize && pg >= 0;
@@ -843,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     !warp_wait(C::kSplitP ? &bars.s_free[b] : &bars.pv_done[b], (use - 1) & 1))
                     break;
                 if (j == 0 && x == 0 && !warp_wait(&bars.q_full[k % C::kQBufs], (uint32_t)((k / C::kQBufs) & 1))) break;
-                if (x == 0 && !warp_wait(kFp8 ? &bars.k_conv[st] : &bars.k_full[st], sp)) break;
+                if (x == 0 && !warp_wait(kCodes ? &bars.k_conv[st] : &bars.k_full[st], sp)) break;
                 const uint64_t q0 = dq + (uint64_t)((((k % C::kQBufs) * 2 + x) * C::kQBytes) >> 4);
                 const uint64_t k0 = dk + (uint64_t)((st * C::kKVBytes) >> 4);
                 const bool last = j == n_kv - 1 && x == ntiles - 1;
@@ -924,15 +986,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float vmul8 = vsc * __uint_as_float((uint32_t)(127 - kexp8) << 23);
             for (int j = 0; j < gm.n_kv; ++j, ++kv) {
                 const int st = kv % NS;
-                const bool fp8_tile = kFp8 && (kWindow ? gm.t0 + j : j) < gm.n_pre;
-                if (kFp8) {
-                    // K: the FP8 prefix tiles to bf16 code values (the S products wait for this)
+                const bool fp8_tile = kCodes && (kWindow ? gm.t0 + j : j) < gm.n_pre;
+                if (kCodes) {
+                    // K: the FP8 (INT8) prefix tiles to bf16 code values (the S products wait for this)
                     if (!__all_sync(0xffffffffu, wait_or_abort<true>(&bars.k_full[st], (uint32_t)((kv / NS) & 1),
                                                                 s_abort, a.status, a.wait_limit_cycles))) {
                         ok = false;
                         break;
                     }
-                    if (fp8_tile) convert_fp8_quarter<D, 0>(sK + st * C::kKVBytes, q, lane, 1.f);
+                    if (fp8_tile) convert_fp8_quarter<D, kInt8 ? 3 : 0>(sK + st * C::kKVBytes, q, lane, 1.f);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.k_conv[st]);
@@ -945,7 +1007,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (fp8_tile) {
                     // V: code * 2^e8 (the softmax takes the rest of the scale), or fp16 of
                     // value * 2^-k, value = scale * e4m3(code), k of the item
-                    if (fold8)
+                    if (kInt8)
+                        convert_fp8_quarter<D, 4>(sV + st * C::kKVBytes, q, lane, 1.f, 0, s_page[st].v2);
+                    else if (fold8)
                         convert_fp8_quarter<D, 2>(sV + st * C::kKVBytes, q, lane, 1.f, p2e8);
                     else
                         convert_fp8_quarter<D, 1>(sV + st * C::kKVBytes, q, lane, vmul8);
@@ -1003,6 +1067,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (lane == 0) s_vscale[st * 4 + q] = kexp;
+                if (kInt8 && lane < 2) {
+                    s_page[st].add[2 * q + lane] = (float)kexp;
+                    s_page[st].mul[2 * q + lane] = sc;
+                }
                 fence_proxy_async_smem();  // the P.V MMA reads these through the async proxy
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.v_conv[st]);
@@ -1097,6 +1165,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // row max: eight chains of three-input maxima over 16 keys each
                 auto row_max = [&]() {
                     float mx8[8];
+                    float kf[8];
+                    if (kInt8) {  // the eight chains are the tile's eight pages (scales are not negative)
+                        const float4 k0 = *reinterpret_cast<const float4 *>(s_page[(tcount - 1) % NS].k);
+                        const float4 k1 = *reinterpret_cast<const float4 *>(s_page[(tcount - 1) % NS].k + 4);
+                        kf[0] = k0.x, kf[1] = k0.y, kf[2] = k0.z, kf[3] = k0.w;
+                        kf[4] = k1.x, kf[5] = k1.y, kf[6] = k1.z, kf[7] = k1.w;
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float *sf = reinterpret_cast<const float *>(sv) + 16 * e;
@@ -1104,12 +1179,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int t = 3; t < 15; t += 2) m = fmax3(m, sf[t], sf[t + 1]);
                         mx8[e] = fmaxf(m, sf[15]);
+                        if (kInt8) mx8[e] *= kf[e];
                     }
                     return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                  fmaxf(mx8[6], mx8[7]));
                 };
+                if (kInt8 && j == 0 &&  // the page scales are in place once the V tile is
+                    !wait_or_abort(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
+                                   a.wait_limit_cycles)) {
+                    ok = false;
+                    break;
+                }
                 if (j == 0) {
-                    const float mt = row_max() * sc;
+                    const float mt = kInt8 ? row_max() : row_max() * sc;
                     const float mn = fmaxf(m_used, mt);
                     l = (m_used == -INFINITY) ? 0.f : l * fast_exp2(m_used - mn);
                     m_used = mn;
@@ -1141,14 +1223,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                          make_float2(0.f, 0.f)};
                         uint32_t pp[16];
+                        // INT8: factor and exponent offset of the chunk's two pages
+                        float2 pk[2], pn[2], pmul = make_float2(0.f, 0.f);
+                        if (kInt8) {
+                            const PageScales &ps = s_page[vst];
+                            const float2 k2 = *reinterpret_cast<const float2 *>(ps.k + 2 * ch);
+                            const float2 a2 = *reinterpret_cast<const float2 *>(ps.add + 2 * ch);
+                            pmul = *reinterpret_cast<const float2 *>(ps.mul + 2 * ch);
+                            pk[0] = make_float2(k2.x, k2.x), pk[1] = make_float2(k2.y, k2.y);
+                            pn[0] = make_float2(neg0 + a2.x, neg0 + a2.x);
+                            pn[1] = make_float2(neg0 + a2.y, neg0 + a2.y);
+                        }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const int c = ch * 32 + 2 * e;
                             const float2 t2 = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])),
-                                                    sc2, ng2);
+                                                    kInt8 ? pk[e >> 3] : sc2, kInt8 ? pn[e >> 3] : ng2);
                             const float p0 = fast_exp2(t2.x);
                             const float p1 = fast_exp2(t2.y);
-                            acc[e & 3] = fadd2(acc[e & 3], make_float2(p0, p1));
+                            // INT8: sums of the first page in acc[0..1], of the second in acc[2..3]
+                            const int ai = kInt8 ? (e >> 3) * 2 + (e & 1) : e & 3;
+                            acc[ai] = fadd2(acc[ai], make_float2(p0, p1));
                             pp[e] = pack_f16x2(p0, p1);
                         }
                         if (ch == 0 && pwait) {
@@ -1159,9 +1254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::fence_after_sync();
                         }
                         if (!pfail) tc::st_32x32b_x16(tp + ch * 16, pp);
-                        tl += (((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
-                               ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y))) *
-                              (f8 ? mul8 : __uint_as_float((uint32_t)(127 - kc) << 23));
+                        if (kInt8)
+                            tl += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) * pmul.x +
+                                  ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y)) * pmul.y;
+                        else
+                            tl += (((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
+                                   ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y))) *
+                                  (f8 ? mul8 : __uint_as_float((uint32_t)(127 - kc) << 23));
                     }
                     return tl;
                 };
@@ -1176,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (__any_sync(0xffffffffu, need)) {
                         // the row max, a rescale of O and l, and P again (the P written above is
                         // overwritten before p_full; rows that need nothing write the same P)
-                        const float mt = row_max() * sc;
+                        const float mt = kInt8 ? row_max() : row_max() * sc;
                         // O_x must hold the P.V of this query tile's previous key tile, product i - ntiles
                         const uint32_t ip = i - ntiles;
                         if (!wait_or_abort(&bars.pv_done[ip % NBP], (ip / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
@@ -1278,12 +1377,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) cta_done(a.sched);
 }
 
-template <int D, bool kWindow, bool kFp8, bool kCausal = true>
+template <int D, bool kWindow, bool kFp8, bool kCausal = true, bool kInt8 = false>
 cudaError_t launch_d(const PrefillArgs &a, const CUtensorMap &qmap, const CUtensorMap &kmap,
                      const CUtensorMap &vmap, const CUtensorMap &kpmap, const CUtensorMap &vpmap,
                      cudaStream_t stream) {
     using C = PrefillCfg<D, (D == 64 && kWindow) ? 2 : 1>;
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, kWindow, kFp8, kCausal>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, kWindow, kFp8, kCausal, kInt8>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     int device = 0, sms = 0;
@@ -1292,7 +1391,7 @@ cudaError_t launch_d(const PrefillArgs &a, const CUtensorMap &qmap, const CUtens
     // persistent: one CTA per SM (shared memory and the 512 TMEM columns allow no more),
     // on at most max_sms SMs when the caller keeps the others for concurrent work
     if (a.max_sms > 0 && a.max_sms < sms) sms = a.max_sms;
-    prefill_kernel<D, kWindow, kFp8, kCausal><<<sms, kThreads, C::kSmemBytes, stream>>>(qmap, kmap, vmap, kpmap, vpmap, a);
+    prefill_kernel<D, kWindow, kFp8, kCausal, kInt8><<<sms, kThreads, C::kSmemBytes, stream>>>(qmap, kmap, vmap, kpmap, vpmap, a);
     return cudaGetLastError();
 }
 
@@ -1306,6 +1405,15 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &qmap, const 
         if (a.fp8_prefix || w || a.prefix_lens) return cudaErrorInvalidValue;
         if (a.D == 64) return launch_d<64, false, false, false>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
         if (a.D == 128) return launch_d<128, false, false, false>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
+        return cudaErrorNotSupported;
+    }
+    if (a.kv_scales) {
+        if (a.D == 64)
+            return w ? launch_d<64, true, false, true, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream)
+                     : launch_d<64, false, false, true, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
+        if (a.D == 128)
+            return w ? launch_d<128, true, false, true, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream)
+                     : launch_d<128, false, false, true, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
         return cudaErrorNotSupported;
     }
     if (a.fp8_prefix) {

@@ -80,6 +80,8 @@ SIGNATURES = {
     "sinkattn_append_kv_int8": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _DP, _P,
                                                _SZ, _P]),
     "sinkattn_decode_int8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P]),
+    "sinkattn_prefill_int8": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP,
+                                             _P, _SZ, _P]),
     "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
                                              ctypes.POINTER(RotaryDesc), _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
@@ -747,4 +749,53 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
                                            _ptr(seq_lens), _ptr(sinks), scale, _ptr(out), _ptr(lse),
                                            ctypes.byref(desc), _ptr(ws), ws.numel(), _stream(dev)),
                "sinkattn_decode_int8")
+    return out, lse
+
+
+def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_table, prefix_lens, sinks=None,
+                 scale=None, out=None, lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0,
+                 wait_limit_us=0):
+    """Chunked prefill over an INT8 paged prefix with a scale per page and KV head
+    (sinkattn_prefill_int8); the new tokens' q, k, v bf16.  Returns (out, lse)."""
+    dev = _need_cuda(q, "q")
+    _need(q, "q", torch.bfloat16, dev, 3)
+    _need(k, "k", torch.bfloat16, dev, 3)
+    _need(v, "v", torch.bfloat16, dev, 3)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    _need(prefix_block_table, "prefix_block_table", torch.int32, dev, 2)
+    _need(prefix_lens, "prefix_lens", torch.int32, dev, 1)
+    _need_int8_cache(k_pages, v_pages, kv_scales, dev)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    n = cu_seqlens.shape[0] - 1
+    if tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D) or (k_pages.shape[1], k_pages.shape[3]) != (Hkv, D):
+        raise ValueError("k / v must be [T, Hkv, D] matching q and the pages")
+    if n < 0 or prefix_block_table.shape[0] != n or prefix_lens.shape[0] != n:
+        raise ValueError("prefix_block_table / prefix_lens rows must equal the requests of cu_seqlens")
+    if sinks is not None:
+        _need(sinks, "sinks", torch.float32, dev, 1)
+        if sinks.shape[0] != Hq:
+            raise ValueError("sinks must have one entry per query head")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, dev, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is None and return_lse:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _need(lse, "lse", torch.float32, dev, 2)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError("lse must be [T, Hq]")
+    desc = paged_desc(n, Hq, Hkv, D, k_pages.shape[0], prefix_block_table.shape[1], window=window, max_sms=max_sms,
+                      wait_limit_us=wait_limit_us)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    with torch.cuda.device(dev):
+        ws = workspace_buf if workspace_buf is not None else _stream_workspace(256, dev, "prefill")
+        _check(load().sinkattn_prefill_int8(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), T, _ptr(k_pages),
+                                            _ptr(v_pages), _ptr(kv_scales), _ptr(prefix_block_table),
+                                            _ptr(prefix_lens), _ptr(sinks), scale, _ptr(out), _ptr(lse),
+                                            ctypes.byref(desc), _ptr(ws), ws.numel(), _stream(dev)),
+               "sinkattn_prefill_int8")
     return out, lse

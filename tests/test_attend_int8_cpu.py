@@ -66,3 +66,22 @@ def test_decode_int8_rejects(sa):
     x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         sa.decode_int8(x, None, None, None, None, None)
+
+
+def test_prefill_int8_rejects(sa):
+    lib, (buf, p) = sa.load(), _host()
+
+    def pre(q=p, k=p, v=p, cu=p, T=8, kp=p, vp=p, sc=p, bt=p, pl=p, out=p, ws=p, wb=256, scale=0.125, d=_desc(sa)):
+        return lib.sinkattn_prefill_int8(q, k, v, cu, T, kp, vp, sc, bt, pl, None, scale, out, None, ctypes.byref(d),
+                                         ws, wb, None)
+    for kw in (dict(q=None), dict(k=None), dict(v=None), dict(cu=None), dict(kp=None), dict(vp=None), dict(sc=None),
+               dict(bt=None), dict(pl=None), dict(out=None), dict(ws=None), dict(sc=p + 4), dict(out=p + 16), dict(T=-1),
+               dict(kp=p + 8), dict(scale=0.0), dict(scale=float("nan")), dict(d=_desc(sa, num_pages=0))):
+        assert pre(**kw) == 1, kw
+    assert pre(wb=128) == 3
+    assert pre(d=_desc(sa, head_dim=32)) == 2
+    assert pre(T=0, q=None, kp=None) == 0
+    assert pre(d=_desc(sa, num_seqs=0), q=None) == 0
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        sa.prefill_int8(x, x, x, None, None, None, None, None, None)
