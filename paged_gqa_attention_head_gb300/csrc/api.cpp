@@ -146,14 +146,14 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L, bool int8 = fal
                                      &L->smem, &ring),
                  "decode launch shape");
     if (rc) return rc;
-    rc = cuda_rc(decode_fp8_launch_shape(d->head_dim, G, d->num_seqs, device, false, &L->ctas8,
+    rc = cuda_rc(decode_fp8_launch_shape(d->head_dim, G, d->num_seqs, device, &L->ctas8,
                                          &L->warps_per_cta8, &L->smem8),
                  "fp8 decode launch shape");
     if (rc) return rc;
     int ctas_int8 = 0;
     if (int8) {
-        rc = cuda_rc(decode_fp8_launch_shape(d->head_dim, G, d->num_seqs, device, true, &ctas_int8,
-                                             &L->warps_per_cta8, &L->smem8),
+        rc = cuda_rc(decode_int8_launch_shape(d->head_dim, G, d->num_seqs, device, &ctas_int8,
+                                              &L->warps_per_cta8, &L->smem8),
                      "int8 decode launch shape");
         if (rc) return rc;
     }
@@ -608,6 +608,7 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
     DecodePrep P;
     int rc = prepare_decode(q, block_table, seq_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, &P, true);
     if (rc) return rc;
+    if ((int64_t)desc->num_seqs * desc->num_qo_heads > (int64_t)INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;  // merge grid
     CUtensorMap kmap, vmap;
     rc = encode_pages_map_fp8(&kmap, k_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
     if (rc) return rc;
@@ -615,11 +616,11 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
     if (rc) return rc;
     P.args.kv_scales = kv_scales;
     P.args.total_warps = P.layout.total_warps8;
-    rc = cuda_rc(launch_decode_fp8(desc->head_dim, P.args, kmap, vmap, P.layout.ctas8, P.layout.smem8,
-                                   (cudaStream_t)stream),
+    rc = cuda_rc(launch_decode_int8(desc->head_dim, P.args, kmap, vmap, P.layout.ctas8, P.layout.smem8,
+                                    (cudaStream_t)stream),
                  "int8 split-KV decode launch");
     if (rc) return rc;
-    return cuda_rc(launch_decode_merge(desc->head_dim, P.args, (cudaStream_t)stream), "merge launch");
+    return cuda_rc(launch_merge_int8(desc->head_dim, P.args, (cudaStream_t)stream), "int8 merge launch");
 }
 
 int sinkattn_prefill_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {

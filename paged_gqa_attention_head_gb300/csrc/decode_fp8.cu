@@ -1,5 +1,4 @@
-// Split-KV paged decode with per-head sinks over a KV cache of one byte per element: FP8 E4M3
-// codes with a scale per KV head, or INT8 codes with a scale per page and KV head.
+// Split-KV paged decode with per-head sinks over an FP8 E4M3 KV cache.
 //
 // Same method and work plan as the bf16 decode ("GPT-OSS on Day 0", section "Sink
 // Attention": heads and the KV length are split, partial softmax states are merged,
@@ -29,16 +28,6 @@
 //   * Token rows are permuted (head_dim 64) and TMA swizzles each page (64-byte
 //     swizzle for head_dim 64, 128-byte for 128) so that every shared load above is
 //     free of bank conflicts.
-//
-// The INT8 cache (element value = s(page, g) * code, s one fp32 pair for K and V):
-//   * the same bytes, copies and MMAs; a code becomes its f16 value by putting its offset form
-//     (code + 128) under the exponent of 1024 and taking 1152 off, exact;
-//   * a page is one k-step of O^T and one m-tile of S^T, so its K scale multiplies that page's
-//     scores, and its V scale the fp32 product of that page's MMA as it joins the sum (one FMA
-//     an element): no scale is rounded, and pages of very different scales meet only in fp32;
-//   * q is divided by a power of two per (sequence, KV head) that puts its largest entry at
-//     2^14, and the scores take it back: any finite bf16 q, of any size, keeps its 8 bits;
-//   * no code is NaN or infinite, so the slots past a sequence's end need no clearing: P is 0.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -68,66 +57,18 @@ struct Fp8Cfg {
     static constexpr int kVWords = D / 32;  // 32-bit words of V a lane reads per token row
 };
 
-template <int D, bool kInt8>
+template <int D>
 int fp8_smem_bytes(int B) {
     using C = Fp8Cfg<D>;
-    // per (warp, stage): its barrier, and per page of its unit two ints (INT8: and two scales)
     return 1024 /* alignment slack */ + C::kWarps * C::kWarpBytes +
-           C::kWarps * C::kStages * (8 + 8 * C::kPPU + (kInt8 ? 8 * C::kPPU : 0)) + (3 * B + 1) * 4;
+           C::kWarps * C::kStages * (8 + 8 * C::kPPU) + (3 * B + 1) * 4;
 }
-
-// Byte offset of byte c of token row r inside a page buffer written by TMA with
-// this head_dim's swizzle (64-byte swizzle: 16-byte chunk bits 4-5 XOR address bits
-// 7-8; 128-byte swizzle: bits 4-6 XOR bits 7-9; buffers 1024-byte aligned).
-template <int D>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-    if (D == 64) return (uint32_t)(r * 64 + ((((c >> 4) ^ (r >> 1)) & 3) << 4) + (c & 15));
-    return (uint32_t)(r * 128 + ((((c >> 4) ^ r) & 7) << 4) + (c & 15));
-}
-
-// Physical token row of MMA token index k (0..15).  For head_dim 64 the order
-// 0,3,1,2,4,7,5,6 (and +8) puts the rows one load instruction touches into distinct
-// banks under the 64-byte swizzle; for 128 the identity already does.
-template <int D>
-__device__ __forceinline__ int tok_row(int k) {
-    if (D == 64) return (int)((0x65742130u >> (4 * (k & 7))) & 15u) + (k & 8);
-    return k;
-}
-
-
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
-    return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v, float mul) {
-    return pack_f16x2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
-}
-
-// The codes in bytes 0, 1 (lo) or 2, 3 (hi) of a word as an f16 pair, exact (INT8: offset codes).
-template <bool kInt8>
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-    return kInt8 ? int8x2_lo_to_f16x2(w) : e4m3x2_lo_to_f16x2(w);
-}
-template <bool kInt8>
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-    return kInt8 ? int8x2_hi_to_f16x2(w) : e4m3x2_hi_to_f16x2(w);
-}
-
-// D(16x8, f32) += A(16x16, f16, row) * B(16x8, f16, col)
-__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 
 // NH: 8-head tiles of the query group (1 for G <= 8, 2 for G = 16).  The second bound is the
 // CTAs an SM each variant is built for (its register budget; the occupancy each already had):
 // left to itself the compiler held the two-tile head_dim-128 variant near 210 registers, and
 // with the whole 2-CTA budget (up to 255) it ran the Qwen3-shape FP8 batch 6.6 % faster.
-template <int D, int NH, bool kWindow, bool kInt8>
+template <int D, int NH, bool kWindow>
 __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 3) : (NH == 1 ? 3 : 2))
     decode_fp8_kernel(const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
@@ -139,8 +80,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kWarps * C::kWarpBytes);
     int *s_nvalid = reinterpret_cast<int *>(bars + C::kWarps * S);  // [warp][stage][page]
     int *s_lo = s_nvalid + C::kWarps * S * U;  // [warp][stage][page] first key in the window
-    float2 *s_scale = reinterpret_cast<float2 *>(s_lo + C::kWarps * S * U);  // INT8: [warp][stage][page] (K, V)
-    int *s_prefix = kInt8 ? reinterpret_cast<int *>(s_scale + C::kWarps * S * U) : s_lo + C::kWarps * S * U;
+    int *s_prefix = s_lo + C::kWarps * S * U;
     int *s_len = s_prefix + a.B + 1;
     int *s_first = s_len + a.B;
 
@@ -172,7 +112,6 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
     uint64_t *wbar = bars + wid * S;
     int *wnv = s_nvalid + wid * S * U;
     int *wlo = s_lo + wid * S * U;
-    float2 *wsc = s_scale + wid * S * U;
 
     Cursor cur;
     {
@@ -205,22 +144,14 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
 
     // Block-table window: lane l holds the entry of visible page win_p0 + l of sequence
     // win_b (-1 past its last page).  pp is warp-uniform.
-    // INT8: win_sc holds the scales of that page for KV head win_g.
-    int win_b = -1, win_p0 = 0, win_val = -1, win_g = -1;
-    float2 win_sc = make_float2(0.f, 0.f);
-    auto page_entry = [&](int b, int g, int first, int npv, int pp) -> int {
+    int win_b = -1, win_p0 = 0, win_val = -1;
+    auto page_entry = [&](int b, int first, int npv, int pp) -> int {
         const int p0 = pp & ~31;
-        const bool moved = b != win_b || p0 != win_p0;
-        if (moved) {
+        if (b != win_b || p0 != win_p0) {
             win_b = b;
             win_p0 = p0;
             const int q = p0 + lane;
             win_val = q < npv ? a.block_table[(int64_t)b * a.max_pages + first + q] : -1;
-        }
-        if (kInt8 && (moved || g != win_g)) {
-            win_g = g;
-            if (win_val >= 0 && win_val < a.num_pages)
-                win_sc = __ldg(reinterpret_cast<const float2 *>(a.kv_scales) + (int64_t)win_val * a.Hkv + g);
         }
         return __shfl_sync(0xffffffffu, win_val, pp - p0);
     };
@@ -234,12 +165,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int pp = c.p * U + j;
-            pg[j] = pp < npv ? page_entry(c.b, c.g, first, npv, pp) : -2;  // -2: no such page
-            if (kInt8 && pp < npv) {  // a page without an entry keeps whatever scales: its nvalid is 0
-                const float ks = __shfl_sync(0xffffffffu, win_sc.x, pp & 31);
-                const float vs = __shfl_sync(0xffffffffu, win_sc.y, pp & 31);
-                if (lane == 0) wsc[stage * U + j] = make_float2(ks, vs);
-            }
+            pg[j] = pp < npv ? page_entry(c.b, first, npv, pp) : -2;  // -2: no such page
         }
         if (lane == 0) {
             uint8_t *kb = wbuf + stage * C::kStageBytes;
@@ -304,7 +230,6 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
     float acc[C::kMTiles][NH][4];
     float mr[NH][2], ls[NH][2];
     float sl = 0.f, vsc = 1.f;
-    float q_up = 1.f;  // INT8: the power of two taken off q
     int seg_p0 = cur.p;
     bool seg_start = true;
 
@@ -324,14 +249,12 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
         const uint8_t *kb = wbuf + stage * C::kStageBytes;  // K of page j at kb + j * kPageBytes
         const uint8_t *vb = kb + U * C::kPageBytes;         // V of page j at vb + j * kPageBytes
         int nv[U], klo[U];
-        float2 psc[U];  // INT8: the page's scales (0 for a page that is not there)
         uint32_t kw[U][2][C::kKWords];  // K rows gr, gr + 8: the lane's run of D/4 bytes
         uint32_t vw[U][4][C::kVWords];  // V rows of tokens 2t, 2t+1, 2t+8, 2t+9: D/8 bytes
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             nv[j] = wnv[stage * U + j];
             klo[j] = kWindow ? wlo[stage * U + j] : 0;
-            if (kInt8) psc[j] = nv[j] > 0 ? wsc[stage * U + j] : make_float2(0.f, 0.f);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -361,7 +284,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
                 // is not 0, so those V rows become zeros
                 const bool live = vrow[i] < nv[j];
 #pragma unroll
-                for (int e = 0; e < C::kVWords; ++e) vw[j][i][e] = kInt8 ? w[e] ^ 0x80808080u : live ? w[e] : 0u;
+                for (int e = 0; e < C::kVWords; ++e) vw[j][i][e] = live ? w[e] : 0u;
             }
         }
         fence_proxy_async_smem();
@@ -374,7 +297,6 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
         if (seg_start) {
             const __nv_bfloat16 *qg = reinterpret_cast<const __nv_bfloat16 *>(a.q) +
                                       ((int64_t)cur.b * a.Hq + (int64_t)cur.g * a.G) * D;
-            uint32_t mx = 0;  // INT8: the largest finite |q| of the lane, as bf16 bits
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt) {
                 const int h = nt * 8 + gr;
@@ -384,38 +306,11 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
                     if (h < a.G)
                         w = *reinterpret_cast<const uint4 *>(qg + h * D + t4 * (D / 4) + 8 * i);
                     // elements 8i .. 8i+7 of the lane's run: k-steps 2i and 2i + 1
-                    if (kInt8) {  // as bf16 first
-                        qf[2 * i][nt][0] = w.x;
-                        qf[2 * i][nt][1] = w.y;
-                        qf[2 * i + 1][nt][0] = w.z;
-                        qf[2 * i + 1][nt][1] = w.w;
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t lo = u[e] & 0x7FFFu, hi = (u[e] >> 16) & 0x7FFFu;
-                            mx = max(mx, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-                        }
-                        continue;
-                    }
                     qf[2 * i][nt][0] = bf16x2_to_f16x2(w.x);
                     qf[2 * i][nt][1] = bf16x2_to_f16x2(w.y);
                     qf[2 * i + 1][nt][0] = bf16x2_to_f16x2(w.z);
                     qf[2 * i + 1][nt][1] = bf16x2_to_f16x2(w.w);
                 }
-            }
-            if (kInt8) {
-                // times 2^(14 - e), e the exponent of the group's largest entry (kept where both
-                // powers are normal floats)
-                const int ex = min(max((int)(__reduce_max_sync(0xffffffffu, mx) >> 7), 20), 254);
-                const float down = __uint_as_float((uint32_t)(268 - ex) << 23);  // 2^(14 - (ex - 127))
-                q_up = __uint_as_float((uint32_t)(ex - 14) << 23);               // its inverse
-#pragma unroll
-                for (int kk = 0; kk < C::kKSteps; ++kk)
-#pragma unroll
-                    for (int nt = 0; nt < NH; ++nt) {
-                        qf[kk][nt][0] = bf16x2_to_f16x2(qf[kk][nt][0], down);
-                        qf[kk][nt][1] = bf16x2_to_f16x2(qf[kk][nt][1], down);
-                    }
             }
 #pragma unroll
             for (int mt = 0; mt < C::kMTiles; ++mt)
@@ -427,8 +322,8 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
                 mr[nt][0] = mr[nt][1] = -INFINITY;
                 ls[nt][0] = ls[nt][1] = 0.f;
             }
-            sl = a.scale_log2 * (!kInt8 && a.k_scale ? a.k_scale[cur.g] : 1.f);
-            vsc = !kInt8 && a.v_scale ? a.v_scale[cur.g] : 1.f;
+            sl = a.scale_log2 * (a.k_scale ? a.k_scale[cur.g] : 1.f);
+            vsc = a.v_scale ? a.v_scale[cur.g] : 1.f;
             seg_p0 = cur.p;
             seg_start = false;
         }
@@ -441,10 +336,8 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
             for (int nt = 0; nt < NH; ++nt) s[j][nt][0] = s[j][nt][1] = s[j][nt][2] = s[j][nt][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < C::kKSteps; ++kk) {
-                const uint32_t w0 = kInt8 ? kw[j][0][kk] ^ 0x80808080u : kw[j][0][kk];
-                const uint32_t w1 = kInt8 ? kw[j][1][kk] ^ 0x80808080u : kw[j][1][kk];
-                const uint32_t a0 = codes_lo<kInt8>(w0), a2 = codes_hi<kInt8>(w0);
-                const uint32_t a1 = codes_lo<kInt8>(w1), a3 = codes_hi<kInt8>(w1);
+                const uint32_t a0 = e4m3x2_lo_to_f16x2(kw[j][0][kk]), a2 = e4m3x2_hi_to_f16x2(kw[j][0][kk]);
+                const uint32_t a1 = e4m3x2_lo_to_f16x2(kw[j][1][kk]), a3 = e4m3x2_hi_to_f16x2(kw[j][1][kk]);
 #pragma unroll
                 for (int nt = 0; nt < NH; ++nt)
                     mma_f16_16816(s[j][nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
@@ -452,11 +345,10 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt) {
                 const bool ok0 = rk0 < nv[j] && rk0 >= klo[j], ok1 = rk1 < nv[j] && rk1 >= klo[j];
-                const float f = kInt8 ? psc[j].x * q_up * sl : sl;
-                s[j][nt][0] = ok0 ? s[j][nt][0] * f : -INFINITY;
-                s[j][nt][1] = ok0 ? s[j][nt][1] * f : -INFINITY;
-                s[j][nt][2] = ok1 ? s[j][nt][2] * f : -INFINITY;
-                s[j][nt][3] = ok1 ? s[j][nt][3] * f : -INFINITY;
+                s[j][nt][0] = ok0 ? s[j][nt][0] * sl : -INFINITY;
+                s[j][nt][1] = ok0 ? s[j][nt][1] * sl : -INFINITY;
+                s[j][nt][2] = ok1 ? s[j][nt][2] * sl : -INFINITY;
+                s[j][nt][3] = ok1 ? s[j][nt][3] * sl : -INFINITY;
             }
         }
         uint32_t pb[U][NH][2];
@@ -510,21 +402,13 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int mt = 2 * mp + e;
-                    const uint32_t a0 = e ? codes_hi<kInt8>(x00) : codes_lo<kInt8>(x00);
-                    const uint32_t a1 = e ? codes_hi<kInt8>(x01) : codes_lo<kInt8>(x01);
-                    const uint32_t a2 = e ? codes_hi<kInt8>(x10) : codes_lo<kInt8>(x10);
-                    const uint32_t a3 = e ? codes_hi<kInt8>(x11) : codes_lo<kInt8>(x11);
+                    const uint32_t a0 = e ? e4m3x2_hi_to_f16x2(x00) : e4m3x2_lo_to_f16x2(x00);
+                    const uint32_t a1 = e ? e4m3x2_hi_to_f16x2(x01) : e4m3x2_lo_to_f16x2(x01);
+                    const uint32_t a2 = e ? e4m3x2_hi_to_f16x2(x10) : e4m3x2_lo_to_f16x2(x10);
+                    const uint32_t a3 = e ? e4m3x2_hi_to_f16x2(x11) : e4m3x2_lo_to_f16x2(x11);
 #pragma unroll
-                    for (int nt = 0; nt < NH; ++nt) {
-                        if (kInt8) {
-                            float o[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16_16816(o, a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[mt][nt][i] = fmaf(o[i], psc[j].y, acc[mt][nt][i]);
-                        } else {
-                            mma_f16_16816(acc[mt][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
-                        }
-                    }
+                    for (int nt = 0; nt < NH; ++nt)
+                        mma_f16_16816(acc[mt][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
                 }
             }
         }
@@ -590,17 +474,17 @@ __global__ void __launch_bounds__(Fp8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 
     }
 }
 
-template <int D, int NH, bool kInt8>
+template <int D, int NH>
 cudaError_t fp8_shape_for(int B, int device, int *ctas, int *warps, int *smem) {
     using C = Fp8Cfg<D>;
-    const int bytes = fp8_smem_bytes<D, kInt8>(B);
+    const int bytes = fp8_smem_bytes<D>(B);
     int optin = 0, sms = 0, occ = 1 << 30;
     cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
     if (e != cudaSuccess) return e;
-    const void *kernels[2] = {reinterpret_cast<const void *>(decode_fp8_kernel<D, NH, false, kInt8>),
-                              reinterpret_cast<const void *>(decode_fp8_kernel<D, NH, true, kInt8>)};
+    const void *kernels[2] = {reinterpret_cast<const void *>(decode_fp8_kernel<D, NH, false>),
+                              reinterpret_cast<const void *>(decode_fp8_kernel<D, NH, true>)};
     for (const void *k : kernels) {
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, k);
@@ -623,11 +507,10 @@ cudaError_t fp8_shape_for(int B, int device, int *ctas, int *warps, int *smem) {
 
 }  // namespace
 
-cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, bool int8, int *ctas, int *warps_per_cta,
+cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
                                     int *smem_bytes) {
     struct Entry {
         int device, D, NH, B, ctas, warps, smem;
-        bool int8;
     };
     static std::mutex mu;
     static std::vector<Entry> cache;
@@ -635,7 +518,7 @@ cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, bool int8, 
     {
         std::lock_guard<std::mutex> lock(mu);
         for (const Entry &e : cache)
-            if (e.device == device && e.D == D && e.NH == NH && e.B == B && e.int8 == int8) {
+            if (e.device == device && e.D == D && e.NH == NH && e.B == B) {
                 *ctas = e.ctas;
                 *warps_per_cta = e.warps;
                 *smem_bytes = e.smem;
@@ -643,54 +526,44 @@ cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, bool int8, 
             }
     }
     cudaError_t e;
-#define SINKATTN_FP8_SHAPE(DD, NN)                                                     \
-    e = int8 ? fp8_shape_for<DD, NN, true>(B, device, ctas, warps_per_cta, smem_bytes) \
-             : fp8_shape_for<DD, NN, false>(B, device, ctas, warps_per_cta, smem_bytes)
     if (D == 64 && NH == 1)
-        SINKATTN_FP8_SHAPE(64, 1);
+        e = fp8_shape_for<64, 1>(B, device, ctas, warps_per_cta, smem_bytes);
     else if (D == 64)
-        SINKATTN_FP8_SHAPE(64, 2);
+        e = fp8_shape_for<64, 2>(B, device, ctas, warps_per_cta, smem_bytes);
     else if (D == 128 && NH == 1)
-        SINKATTN_FP8_SHAPE(128, 1);
+        e = fp8_shape_for<128, 1>(B, device, ctas, warps_per_cta, smem_bytes);
     else if (D == 128)
-        SINKATTN_FP8_SHAPE(128, 2);
+        e = fp8_shape_for<128, 2>(B, device, ctas, warps_per_cta, smem_bytes);
     else
         return cudaErrorInvalidValue;
-#undef SINKATTN_FP8_SHAPE
     if (e == cudaSuccess) {
         std::lock_guard<std::mutex> lock(mu);
         if (cache.size() > 256) cache.clear();
-        cache.push_back({device, D, NH, B, *ctas, *warps_per_cta, *smem_bytes, int8});
+        cache.push_back({device, D, NH, B, *ctas, *warps_per_cta, *smem_bytes});
     }
     return e;
 }
 
 cudaError_t launch_decode_fp8(int D, const DecodeArgs &a, const CUtensorMap &kmap,
                               const CUtensorMap &vmap, int ctas, int smem_bytes, cudaStream_t stream) {
-    const bool w = a.window > 0, two = a.G > 8, int8 = a.kv_scales != nullptr;
-#define SINKATTN_FP8_KERNEL(DD, NN, WW, II) \
-    decode_fp8_kernel<DD, NN, WW, II><<<ctas, Fp8Cfg<DD>::kThreads, smem_bytes, stream>>>(kmap, vmap, a)
-#define SINKATTN_FP8_LAUNCH(DD, NN)                                                            \
-    if (w) {                                                                                   \
-        if (int8) SINKATTN_FP8_KERNEL(DD, NN, true, true); else SINKATTN_FP8_KERNEL(DD, NN, true, false);   \
-    } else {                                                                                   \
-        if (int8) SINKATTN_FP8_KERNEL(DD, NN, false, true); else SINKATTN_FP8_KERNEL(DD, NN, false, false); \
-    }
+    const bool w = a.window > 0;
+    const bool two = a.G > 8;
+#define SINKATTN_FP8_LAUNCH(DD, NN, WW) \
+    decode_fp8_kernel<DD, NN, WW><<<ctas, Fp8Cfg<DD>::kThreads, smem_bytes, stream>>>(kmap, vmap, a)
     if (D == 64) {
         if (two) {
-            SINKATTN_FP8_LAUNCH(64, 2)
+            if (w) SINKATTN_FP8_LAUNCH(64, 2, true); else SINKATTN_FP8_LAUNCH(64, 2, false);
         } else {
-            SINKATTN_FP8_LAUNCH(64, 1)
+            if (w) SINKATTN_FP8_LAUNCH(64, 1, true); else SINKATTN_FP8_LAUNCH(64, 1, false);
         }
     } else {
         if (two) {
-            SINKATTN_FP8_LAUNCH(128, 2)
+            if (w) SINKATTN_FP8_LAUNCH(128, 2, true); else SINKATTN_FP8_LAUNCH(128, 2, false);
         } else {
-            SINKATTN_FP8_LAUNCH(128, 1)
+            if (w) SINKATTN_FP8_LAUNCH(128, 1, true); else SINKATTN_FP8_LAUNCH(128, 1, false);
         }
     }
 #undef SINKATTN_FP8_LAUNCH
-#undef SINKATTN_FP8_KERNEL
     return cudaGetLastError();
 }
 

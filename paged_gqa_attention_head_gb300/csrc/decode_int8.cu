@@ -1,0 +1,713 @@
+// Split-KV paged decode with per-head sinks over an INT8 cache with one scale for each page and
+// KV head (element value = s(page, g) * code; one fp32 pair of scales, K and V).
+//
+// The plan, the copies and the products are those of the FP8 decode: every warp takes an equal
+// run of two-page units, S^T = K Q^T and O^T = V^T P^T on m16n8k16 f16 MMAs with the 16 tokens of
+// a page, then head_dim, on the M axis and the query heads on N; the contraction index permuted so
+// that a lane's K fragment is one run of D/4 bytes and its V fragment D/8 bytes of four rows.
+// What the scales and the codes change:
+//   * a code becomes its f16 value by putting its offset form (code + 128) under the exponent of
+//     1024 and taking 1152 off: exact, five instructions for four codes;
+//   * K: a page's scale multiplies its 16 scores, together with the softmax scale;
+//   * V: P of a page is taken times s / 2^E, with 2^E the power of two above the largest V scale
+//     the warp has met in this (sequence, head): one rounding to f16, and O^T is summed in the
+//     MMA's fp32 accumulators over all pages.  When a larger scale comes, O^T and E move by
+//     an exact power of two.  (Taking each page's product apart and adding it with an FMA per
+//     element rounds no scale at all, and cost 64 FMAs a page at head_dim 128 and 16 heads,
+//     a tenth of the instructions.  Rounding P times the scale is as exact as rounding P for
+//     every page within 2^22 of the largest, and beyond that is off by 2^-33 of the largest.)
+//   * q times a power of two per (sequence, KV head) that puts its largest entry at 2^14 is exact
+//     in f16 whatever its size; the scores take the power back;
+//   * no code is NaN or infinite: slots past a sequence's end need no clearing, P is 0 there.
+// The running maximum moves only when a score passes it by more than 8 (log2): P is taken as
+// 2^(s - m + 7), at most 2^15, so a stale maximum costs no precision and the votes, the column
+// maxima and the rescale of O^T drop out of almost every unit.
+#include <math.h>
+
+#include <mutex>
+#include <vector>
+
+#include "decode_common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace sinkattn {
+
+namespace {
+
+template <int D>
+struct Int8Cfg {
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kPPU = 2;  // pages per work unit (32 tokens)
+    static constexpr int kStages = 2;
+    static constexpr int kPageBytes = kPageSize * D;           // one (page, head) of K or of V codes
+    static constexpr int kStageBytes = 2 * kPPU * kPageBytes;  // the unit's K pages, then V pages
+    static constexpr int kWarpBytes = kStages * kStageBytes;
+    static constexpr int kKSteps = D / 16;  // S^T k-steps over head_dim
+    static constexpr int kMTiles = D / 16;  // O^T m-tiles over head_dim
+    static constexpr int kKWords = D / 16;  // 32-bit words of K a lane reads per token row
+    static constexpr int kVWords = D / 32;  // 32-bit words of V a lane reads per token row
+};
+
+constexpr float kPShift = 7.f;   // P = 2^(s - m + kPShift)
+constexpr float kMaxSlack = 8.f; // the running maximum moves when a score passes it by more
+
+template <int D>
+int int8_smem_bytes(int B) {
+    using C = Int8Cfg<D>;
+    // per (warp, stage): its barrier, and per page of its unit two ints and two scales
+    return 1024 /* alignment slack */ + C::kWarps * C::kWarpBytes + C::kWarps * C::kStages * (8 + 16 * C::kPPU) +
+           (3 * B + 1) * 4;
+}
+
+// NH: 8-head tiles of the query group (1 for G <= 8, 2 for G = 16).
+template <int D, int NH, bool kWindow>
+__global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 3) : (NH == 1 ? 3 : 2))
+    decode_int8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const DecodeArgs a) {
+    using C = Int8Cfg<D>;
+    constexpr int S = C::kStages, U = C::kPPU;
+    // the merge may take its place on the SMs; it waits for this grid before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kWarps * C::kWarpBytes);
+    float2 *s_scale = reinterpret_cast<float2 *>(bars + C::kWarps * S);  // [warp][stage][page] (K, V)
+    int *s_nvalid = reinterpret_cast<int *>(s_scale + C::kWarps * S * U);  // [warp][stage][page]
+    int *s_lo = s_nvalid + C::kWarps * S * U;  // [warp][stage][page] first key in the window
+    int *s_prefix = s_lo + C::kWarps * S * U;
+    int *s_len = s_prefix + a.B + 1;
+    int *s_first = s_len + a.B;
+
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    if (tid == 0) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
+    if (lane < S) mbar_init(&bars[wid * S + lane], 1);
+    fence_mbar_init();
+    scan_pages<U>(a, s_prefix, s_len, s_first);  // contains __syncthreads
+
+    const int64_t T = (int64_t)a.Hkv * s_prefix[a.B];
+    int64_t per = (T + a.total_warps - 1) / a.total_warps;
+    if (per < kMinUnitsPerWarp) per = kMinUnitsPerWarp;
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= a.B; b += blockDim.x) a.ws_prefix[b] = s_prefix[b];
+        if (tid == 0) {
+            a.ws_plan[0] = T;
+            a.ws_plan[1] = per;
+        }
+    }
+    const int wglob = blockIdx.x * C::kWarps + wid;
+    const int64_t u_begin = (int64_t)wglob * per;
+    if (u_begin >= T) return;  // warp-uniform; no block-wide barrier follows
+    const int n_units = (int)min(per, T - u_begin);
+
+    uint8_t *wbuf = smem + wid * C::kWarpBytes;
+    uint64_t *wbar = bars + wid * S;
+    int *wnv = s_nvalid + wid * S * U;
+    int *wlo = s_lo + wid * S * U;
+    float2 *wsc = s_scale + wid * S * U;
+
+    Cursor cur;
+    {
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)a.Hkv * s_prefix[mid] <= u_begin)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        cur.b = lo;
+        cur.pb = s_prefix[lo + 1] - s_prefix[lo];
+        const int64_t local = u_begin - (int64_t)a.Hkv * s_prefix[lo];
+        cur.g = (int)(local / cur.pb);
+        cur.p = (int)(local % cur.pb);
+    }
+    auto advance = [&](Cursor &c) {
+        if (++c.p == c.pb) {
+            c.p = 0;
+            if (++c.g == a.Hkv) {
+                c.g = 0;
+                do {
+                    ++c.b;
+                    c.pb = c.b < a.B ? s_prefix[c.b + 1] - s_prefix[c.b] : 1;
+                } while (c.b < a.B && c.pb == 0);
+            }
+        }
+    };
+
+    // Block-table window: lane l holds the entry of visible page win_p0 + l of sequence
+    // win_b (-1 past its last page) and that page's scales for KV head win_g.
+    int win_b = -1, win_p0 = 0, win_val = -1, win_g = -1;
+    float2 win_sc = make_float2(0.f, 0.f);
+    auto page_entry = [&](int b, int g, int first, int npv, int pp) -> int {
+        const int p0 = pp & ~31;
+        const bool moved = b != win_b || p0 != win_p0;
+        if (moved) {
+            win_b = b;
+            win_p0 = p0;
+            const int q = p0 + lane;
+            win_val = q < npv ? a.block_table[(int64_t)b * a.max_pages + first + q] : -1;
+        }
+        if (moved || g != win_g) {
+            win_g = g;
+            if (win_val >= 0 && win_val < a.num_pages)
+                win_sc = __ldg(reinterpret_cast<const float2 *>(a.kv_scales) + (int64_t)win_val * a.Hkv + g);
+        }
+        return __shfl_sync(0xffffffffu, win_val, pp - p0);
+    };
+
+    const uint64_t policy = l2_policy_evict_first();
+    auto produce = [&](int stage, const Cursor &c) {
+        const int first = kWindow ? s_first[c.b] : 0;
+        const int L = s_len[c.b];
+        const int npv = (L + kPageSize - 1) / kPageSize - first;  // pages the query sees
+        int pg[U];
+        float2 sc[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int pp = c.p * U + j;
+            pg[j] = pp < npv ? page_entry(c.b, c.g, first, npv, pp) : -2;  // -2: no such page
+            sc[j].x = __shfl_sync(0xffffffffu, win_sc.x, pp & 31);
+            sc[j].y = __shfl_sync(0xffffffffu, win_sc.y, pp & 31);
+        }
+        if (lane == 0) {
+            uint8_t *kb = wbuf + stage * C::kStageBytes;
+            uint32_t bytes = 0;
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int page = first + c.p * U + j;  // page index within the sequence
+                const bool ok = pg[j] >= 0 && pg[j] < a.num_pages;
+                bad |= pg[j] != -2 && !ok;
+                wnv[stage * U + j] = ok ? min(kPageSize, L - kPageSize * page) : 0;
+                wsc[stage * U + j] = ok ? sc[j] : make_float2(0.f, 0.f);
+                // keys before the sliding window in this page are hidden
+                if (kWindow) wlo[stage * U + j] = max(0, L - a.window - kPageSize * page);
+                if (ok) bytes += 2 * C::kPageBytes;
+            }
+            if (bad) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+            uint64_t *bar = &wbar[stage];
+            if (bytes) {
+                mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (pg[j] >= 0 && pg[j] < a.num_pages) {
+                        tma_load_4d_hint(kb + j * C::kPageBytes, &kmap, bar, 0, 0, c.g, pg[j], policy);
+                        tma_load_4d_hint(kb + (U + j) * C::kPageBytes, &vmap, bar, 0, 0, c.g, pg[j],
+                                         policy);
+                    }
+            } else {
+                mbar_arrive(bar);
+            }
+        }
+    };
+
+    Cursor pc = cur;
+    const int n_pro = min(S, n_units);
+    for (int u = 0; u < n_pro; ++u) {
+        produce(u, pc);
+        advance(pc);
+    }
+
+    const int gr = lane >> 2, t4 = lane & 3;
+    // K: this lane's MMA rows are tokens gr and gr + 8; its bytes are [t4 * D/4, +D/4)
+    const int rk0 = tok_row<D>(gr), rk1 = rk0 + 8;
+    uint32_t koff[2][C::kKWords / 4];
+#pragma unroll
+    for (int i = 0; i < C::kKWords / 4; ++i) {
+        koff[0][i] = swz<D>(rk0, t4 * (D / 4) + 16 * i);
+        koff[1][i] = swz<D>(rk1, t4 * (D / 4) + 16 * i);
+    }
+    // V: tokens 2t, 2t+1, 2t+8, 2t+9 of the MMA's k axis; bytes [gr * D/8, +D/8)
+    uint32_t voff[4];
+    {
+        const int ks[4] = {2 * t4, 2 * t4 + 1, 2 * t4 + 8, 2 * t4 + 9};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) voff[i] = swz<D>(tok_row<D>(ks[i]), gr * (D / 8));
+    }
+
+    uint32_t qf[C::kKSteps][NH][2];
+    float acc[C::kMTiles][NH][4];
+    float mr[NH][2], ls[NH][2];
+    float f0 = 0.f;                   // score factor but for the page's scale
+    float v_top = 0.f, v_inv = 0.f;   // 2^E and 2^-E
+    int seg_p0 = cur.p;
+    bool seg_start = true;
+
+    for (int u = 0; u < n_units; ++u) {
+        const int stage = u % S;
+        if (!__all_sync(0xffffffffu, mbar_wait_sleep(&wbar[stage], (uint32_t)((u / S) & 1), a.wait_limit_ns))) {
+            // give up (all lanes together: the outcome is voted): record it, let the copies
+            // already issued land, leave
+            if (lane == 0) set_status(a.status, SINKATTN_STATUS_WAIT_TIMEOUT);
+            for (int v = u; v < min(n_units, u + S); ++v)
+                mbar_wait(&wbar[v % S], (uint32_t)((v / S) & 1), kDrainLimitNs);
+            return;
+        }
+        if (seg_start) {
+            const __nv_bfloat16 *qg = reinterpret_cast<const __nv_bfloat16 *>(a.q) +
+                                      ((int64_t)cur.b * a.Hq + (int64_t)cur.g * a.G) * D;
+            uint32_t mx = 0;  // the largest finite |q| of the lane, as bf16 bits
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) {
+                const int h = nt * 8 + gr;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {  // 8 bf16 per 16-byte load
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (h < a.G)
+                        w = *reinterpret_cast<const uint4 *>(qg + h * D + t4 * (D / 4) + 8 * i);
+                    // elements 8i .. 8i+7 of the lane's run: k-steps 2i and 2i + 1
+                    qf[2 * i][nt][0] = w.x;
+                    qf[2 * i][nt][1] = w.y;
+                    qf[2 * i + 1][nt][0] = w.z;
+                    qf[2 * i + 1][nt][1] = w.w;
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t lo = x[e] & 0x7FFFu, hi = (x[e] >> 16) & 0x7FFFu;
+                        mx = max(mx, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                    }
+                }
+            }
+            // q times 2^(14 - e), e the exponent of the group's largest entry (kept where both
+            // powers are normal floats), with the sign of the score scale
+            const int ex = min(max((int)(__reduce_max_sync(0xffffffffu, mx) >> 7), 20), 254);
+            const float down = copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), a.scale_log2);
+            f0 = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(ex - 14) << 23);
+#pragma unroll
+            for (int kk = 0; kk < C::kKSteps; ++kk)
+#pragma unroll
+                for (int nt = 0; nt < NH; ++nt) {
+                    qf[kk][nt][0] = bf16x2_to_f16x2_times(qf[kk][nt][0], down);
+                    qf[kk][nt][1] = bf16x2_to_f16x2_times(qf[kk][nt][1], down);
+                }
+#pragma unroll
+            for (int mt = 0; mt < C::kMTiles; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NH; ++nt)
+                    acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) {
+                mr[nt][0] = mr[nt][1] = -INFINITY;
+                ls[nt][0] = ls[nt][1] = 0.f;
+            }
+            v_top = v_inv = 0.f;
+            seg_p0 = cur.p;
+            seg_start = false;
+        }
+
+        const uint8_t *kb = wbuf + stage * C::kStageBytes;  // K of page j at kb + j * kPageBytes
+        const uint8_t *vb = kb + U * C::kPageBytes;         // V of page j at vb + j * kPageBytes
+        int nv[U], klo[U];
+        float2 psc[U];
+        // S^T = K Q^T per page: rows tokens, columns heads
+        float s[U][NH][4];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            nv[j] = wnv[stage * U + j];
+            klo[j] = kWindow ? wlo[stage * U + j] : 0;
+            psc[j] = wsc[stage * U + j];
+            uint32_t kw[2][C::kKWords];  // K rows gr, gr + 8: the lane's run of D/4 bytes
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < C::kKWords / 4; ++i) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(kb + j * C::kPageBytes + koff[r][i]);
+                    kw[r][4 * i] = w.x ^ 0x80808080u;
+                    kw[r][4 * i + 1] = w.y ^ 0x80808080u;
+                    kw[r][4 * i + 2] = w.z ^ 0x80808080u;
+                    kw[r][4 * i + 3] = w.w ^ 0x80808080u;
+                }
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) s[j][nt][0] = s[j][nt][1] = s[j][nt][2] = s[j][nt][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < C::kKSteps; ++kk) {
+                const uint32_t a0 = int8x2_lo_to_f16x2(kw[0][kk]), a2 = int8x2_hi_to_f16x2(kw[0][kk]);
+                const uint32_t a1 = int8x2_lo_to_f16x2(kw[1][kk]), a3 = int8x2_hi_to_f16x2(kw[1][kk]);
+#pragma unroll
+                for (int nt = 0; nt < NH; ++nt)
+                    mma_f16_16816(s[j][nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
+            }
+        }
+        // Take the unit's V into registers and hand the stage back to the copy engine: the next
+        // copy then overlaps the rest of this unit's arithmetic.
+        uint32_t vw[U][4][C::kVWords];  // V rows of tokens 2t, 2t+1, 2t+8, 2t+9: D/8 bytes
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *src = vb + j * C::kPageBytes + voff[i];
+                if (D == 64) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                    vw[j][i][0] = x.x;
+                    vw[j][i][1] = x.y;
+                } else {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                    vw[j][i][0] = x.x;
+                    vw[j][i][1] = x.y;
+                    vw[j][i][2 % C::kVWords] = x.z;
+                    vw[j][i][3 % C::kVWords] = x.w;
+                }
+            }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (u + S < n_units) {
+            produce(stage, pc);
+            advance(pc);
+        }
+
+        // scores, hidden keys at -inf (every page but a sequence's last, and a window's first, is whole)
+        bool raise = false;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const float f = f0 * psc[j].x;
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) {
+                s[j][nt][0] *= f;
+                s[j][nt][1] *= f;
+                s[j][nt][2] *= f;
+                s[j][nt][3] *= f;
+            }
+            if (nv[j] < kPageSize || (kWindow && klo[j] > 0)) {  // warp-uniform
+                const bool ok0 = rk0 < nv[j] && rk0 >= klo[j], ok1 = rk1 < nv[j] && rk1 >= klo[j];
+#pragma unroll
+                for (int nt = 0; nt < NH; ++nt) {
+                    s[j][nt][0] = ok0 ? s[j][nt][0] : -INFINITY;
+                    s[j][nt][1] = ok0 ? s[j][nt][1] : -INFINITY;
+                    s[j][nt][2] = ok1 ? s[j][nt][2] : -INFINITY;
+                    s[j][nt][3] = ok1 ? s[j][nt][3] : -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt)
+                raise |= fmaxf(s[j][nt][0], s[j][nt][2]) > mr[nt][0] + kMaxSlack ||
+                         fmaxf(s[j][nt][1], s[j][nt][3]) > mr[nt][1] + kMaxSlack;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = s[0][nt][e];
+#pragma unroll
+                    for (int j = 0; j < U; ++j) x = fmax3(x, s[j][nt][e], s[j][nt][2 + e]);
+                    x = col_max(x);
+                    const float mn = x > mr[nt][e] + kMaxSlack ? x : mr[nt][e];
+                    const float al = mr[nt][e] == -INFINITY ? 0.f : fast_exp2(mr[nt][e] - mn);
+                    mr[nt][e] = mn;
+                    ls[nt][e] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < C::kMTiles; ++mt) {
+                        acc[mt][nt][e] *= al;
+                        acc[mt][nt][2 + e] *= al;
+                    }
+                }
+        }
+        // a V scale above every one so far: O^T to the next power of two, exactly
+        const float vmx = fmaxf(psc[0].y, psc[1].y);
+        if (vmx > v_top) {  // warp-uniform
+            const float top = __uint_as_float((__float_as_uint(vmx) + 0x7FFFFFu) & 0x7F800000u);
+            const float inv = 1.0f / top, move = v_top * inv;
+#pragma unroll
+            for (int mt = 0; mt < C::kMTiles; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[mt][nt][i] *= move;
+            v_top = top;
+            v_inv = inv;
+        }
+        uint32_t pb[U][NH][2];
+#pragma unroll
+        for (int nt = 0; nt < NH; ++nt) {
+            const float r0 = mr[nt][0] == -INFINITY ? 0.f : mr[nt][0] - kPShift;
+            const float r1 = mr[nt][1] == -INFINITY ? 0.f : mr[nt][1] - kPShift;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const float w = psc[j].y * v_inv;
+                const float p0 = fast_exp2(s[j][nt][0] - r0), p1 = fast_exp2(s[j][nt][1] - r1);
+                const float p2 = fast_exp2(s[j][nt][2] - r0), p3 = fast_exp2(s[j][nt][3] - r1);
+                ls[nt][0] += p0 + p2;
+                ls[nt][1] += p1 + p3;
+                // P^T fragments: transpose (token, head) blocks to (head, token)
+                pb[j][nt][0] = movmatrix_t(pack_f16x2(p0 * w, p1 * w));
+                pb[j][nt][1] = movmatrix_t(pack_f16x2(p2 * w, p3 * w));
+            }
+        }
+
+        // O^T += V^T P^T, one 16-token k-step per page
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            // word layout per token row: [half 0 (rows gr): D/64 words][half 1 (rows gr+8)]
+#pragma unroll
+            for (int mp = 0; mp < C::kMTiles / 2; ++mp) {  // m-tiles 2mp, 2mp + 1
+                const int wi = (mp >> 1), sel = (mp & 1) ? 0x7362 : 0x5140;
+                const uint32_t x00 = __byte_perm(vw[j][0][wi], vw[j][1][wi], sel) ^ 0x80808080u;  // half 0, tokens 2t, 2t+1
+                const uint32_t x01 = __byte_perm(vw[j][0][wi + D / 64], vw[j][1][wi + D / 64], sel) ^ 0x80808080u;  // half 1
+                const uint32_t x10 = __byte_perm(vw[j][2][wi], vw[j][3][wi], sel) ^ 0x80808080u;  // half 0, tokens + 8
+                const uint32_t x11 = __byte_perm(vw[j][2][wi + D / 64], vw[j][3][wi + D / 64], sel) ^ 0x80808080u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int mt = 2 * mp + e;
+                    const uint32_t a0 = e ? int8x2_hi_to_f16x2(x00) : int8x2_lo_to_f16x2(x00);
+                    const uint32_t a1 = e ? int8x2_hi_to_f16x2(x01) : int8x2_lo_to_f16x2(x01);
+                    const uint32_t a2 = e ? int8x2_hi_to_f16x2(x10) : int8x2_lo_to_f16x2(x10);
+                    const uint32_t a3 = e ? int8x2_hi_to_f16x2(x11) : int8x2_lo_to_f16x2(x11);
+#pragma unroll
+                    for (int nt = 0; nt < NH; ++nt)
+                        mma_f16_16816(acc[mt][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
+                }
+            }
+        }
+
+        const bool seg_end = (cur.p == cur.pb - 1) || (u == n_units - 1);
+        if (seg_end) {
+            const bool whole = seg_p0 == 0 && cur.p == cur.pb - 1;
+            const int64_t slot = (int64_t)wglob + (int64_t)cur.b * a.Hkv + cur.g;
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float L = col_sum(ls[nt][e]);
+                    const int hc = nt * 8 + 2 * t4 + e;  // column (head in the group)
+                    // reference of the state: probabilities were taken against mr - kPShift
+                    const float m = mr[nt][e] == -INFINITY ? -INFINITY : mr[nt][e] - kPShift;
+                    if (hc >= a.G) continue;
+                    const int h = cur.g * a.G + hc;
+                    if (whole) {
+                        const float sk = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
+                        const float M = fmaxf(m, sk);
+                        float scl = 0.f, lse2 = -INFINITY;
+                        if (M != -INFINITY) {
+                            const float wm = m == -INFINITY ? 0.f : exp2f(m - M);
+                            const float den = L * wm + (sk == -INFINITY ? 0.f : exp2f(sk - M));
+                            scl = wm / den;
+                            lse2 = M + log2f(den);
+                        }
+                        // the lane's D/8 outputs of this head are contiguous: half 0 (MMA
+                        // rows gr) then half 1 (rows gr + 8), D/16 each
+                        uint32_t w[D / 16];
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int j = 0; j < D / 32; ++j)
+                                w[hf * (D / 32) + j] = pack_bf16x2(acc[2 * j][nt][2 * hf + e] * scl * v_top,
+                                                                   acc[2 * j + 1][nt][2 * hf + e] * scl * v_top);
+                        __nv_bfloat16 *og = reinterpret_cast<__nv_bfloat16 *>(a.out) +
+                                            ((int64_t)cur.b * a.Hq + h) * D + gr * (D / 8);
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i)
+                            *reinterpret_cast<uint4 *>(og + 8 * i) =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                        if (a.lse && gr == 0) a.lse[(int64_t)cur.b * a.Hq + h] = lse2 * kLn2;
+                    } else {
+                        const int64_t row = slot * a.G + hc;
+                        float f[D / 8];
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int mt = 0; mt < D / 16; ++mt) f[hf * (D / 16) + mt] = acc[mt][nt][2 * hf + e] * v_top;
+                        float *pa = a.part_acc + row * D + gr * (D / 8);
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i)
+                            *reinterpret_cast<float4 *>(pa + 4 * i) =
+                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        if (gr == 0) *reinterpret_cast<float2 *>(a.part_ml + row * 2) = make_float2(m, L);
+                    }
+                }
+            seg_start = true;
+        }
+        advance(cur);
+    }
+}
+
+// Log-sum-exp merge of the partial states of one (sequence, query head), the sink counted once.
+// A block of 128 threads: D/4 threads span the head's outputs, the others split the states (8 ways
+// at head_dim 64, 4 at 128), so that the loads of many states are in flight at once; each part
+// keeps its own maximum, and the parts meet in shared memory in a fixed order.  It is launched as
+// a programmatic dependent of the split-KV kernel: its blocks are set up while that one ends.
+template <int D>
+__global__ void __launch_bounds__(128) merge_int8_kernel(const DecodeArgs a) {
+    constexpr int kQuads = D / 4, kParts = 128 / kQuads;
+    __shared__ float4 s_o[kParts][kQuads];
+    __shared__ float2 s_ml[kParts];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, g = h / a.G, r = h % a.G;
+    const int d4 = threadIdx.x % kQuads, part = threadIdx.x / kQuads;
+    const int p0 = a.ws_prefix[b], pb = a.ws_prefix[b + 1] - p0;
+    const int64_t row = (int64_t)b * a.Hq + h;
+    __nv_bfloat16 *og = reinterpret_cast<__nv_bfloat16 *>(a.out) + row * D + d4 * 4;
+    if (pb == 0) {
+        if (part == 0) *reinterpret_cast<uint2 *>(og) = make_uint2(0u, 0u);
+        if (threadIdx.x == 0 && a.lse) a.lse[row] = a.sinks ? a.sinks[h] : -INFINITY;
+        return;
+    }
+    const int64_t start = (int64_t)a.Hkv * p0 + (int64_t)g * pb, last = start + pb - 1;
+    const int64_t per = a.ws_plan[1];
+    const int64_t w_lo = start / per, w_hi = last / per;
+    if (w_lo == w_hi) return;  // finished by the split-KV kernel
+    const int nsplit = (int)(w_hi - w_lo + 1);
+    const int64_t slot0 = w_lo + (int64_t)b * a.Hkv + g;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = part; s < nsplit; s += kParts) m = fmaxf(m, a.part_ml[((slot0 + s) * a.G + r) * 2]);
+    if (m != -INFINITY) {
+#pragma unroll 4
+        for (int s = part; s < nsplit; s += kParts) {
+            const int64_t at = (slot0 + s) * a.G + r;
+            const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+            const float4 v = *reinterpret_cast<const float4 *>(a.part_acc + at * D + d4 * 4);
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+            l = fmaf(ml.y, w, l);
+            o.x = fmaf(v.x, w, o.x);
+            o.y = fmaf(v.y, w, o.y);
+            o.z = fmaf(v.z, w, o.z);
+            o.w = fmaf(v.w, w, o.w);
+        }
+    }
+    s_o[part][d4] = o;
+    if (d4 == 0) s_ml[part] = make_float2(m, l);
+    __syncthreads();
+    if (part > 0) return;
+    const float sk = a.sinks ? a.sinks[h] * kLog2e : -INFINITY;
+    float M = sk;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) M = fmaxf(M, s_ml[i].x);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float lse2 = -INFINITY;
+    if (M != -INFINITY) {
+        float den = sk == -INFINITY ? 0.f : exp2f(sk - M);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const float2 ml = s_ml[i];
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            const float4 v = s_o[i][d4];
+            den = fmaf(ml.y, w, den);
+            sum.x = fmaf(v.x, w, sum.x);
+            sum.y = fmaf(v.y, w, sum.y);
+            sum.z = fmaf(v.z, w, sum.z);
+            sum.w = fmaf(v.w, w, sum.w);
+        }
+        const float inv = 1.f / den;
+        sum.x *= inv;
+        sum.y *= inv;
+        sum.z *= inv;
+        sum.w *= inv;
+        lse2 = M + log2f(den);
+    }
+    *reinterpret_cast<uint2 *>(og) = make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+    if (d4 == 0 && a.lse) a.lse[row] = lse2 * kLn2;
+}
+
+template <int D, int NH>
+cudaError_t int8_shape_for(int B, int device, int *ctas, int *warps, int *smem) {
+    using C = Int8Cfg<D>;
+    const int bytes = int8_smem_bytes<D>(B);
+    int optin = 0, sms = 0, occ = 1 << 30;
+    cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e != cudaSuccess) return e;
+    const void *kernels[2] = {reinterpret_cast<const void *>(decode_int8_kernel<D, NH, false>),
+                              reinterpret_cast<const void *>(decode_int8_kernel<D, NH, true>)};
+    for (const void *k : kernels) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, k);
+        if (e != cudaSuccess) return e;
+        const int ceiling = optin - (int)fa.sharedSizeBytes;
+        if (bytes > ceiling) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ceiling);
+        if (e != cudaSuccess) return e;
+        int o = 0;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, k, C::kThreads, bytes);
+        if (e != cudaSuccess) return e;
+        occ = min(occ, o);
+    }
+    if (occ < 1) return cudaErrorInvalidConfiguration;
+    *ctas = sms * occ;
+    *warps = C::kWarps;
+    *smem = bytes;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t decode_int8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
+                                     int *smem_bytes) {
+    struct Entry {
+        int device, D, NH, B, ctas, warps, smem;
+    };
+    static std::mutex mu;
+    static std::vector<Entry> cache;
+    const int NH = G > 8 ? 2 : 1;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        for (const Entry &e : cache)
+            if (e.device == device && e.D == D && e.NH == NH && e.B == B) {
+                *ctas = e.ctas;
+                *warps_per_cta = e.warps;
+                *smem_bytes = e.smem;
+                return cudaSuccess;
+            }
+    }
+    cudaError_t e;
+    if (D == 64 && NH == 1)
+        e = int8_shape_for<64, 1>(B, device, ctas, warps_per_cta, smem_bytes);
+    else if (D == 64)
+        e = int8_shape_for<64, 2>(B, device, ctas, warps_per_cta, smem_bytes);
+    else if (D == 128 && NH == 1)
+        e = int8_shape_for<128, 1>(B, device, ctas, warps_per_cta, smem_bytes);
+    else if (D == 128)
+        e = int8_shape_for<128, 2>(B, device, ctas, warps_per_cta, smem_bytes);
+    else
+        return cudaErrorInvalidValue;
+    if (e == cudaSuccess) {
+        std::lock_guard<std::mutex> lock(mu);
+        if (cache.size() > 256) cache.clear();
+        cache.push_back({device, D, NH, B, *ctas, *warps_per_cta, *smem_bytes});
+    }
+    return e;
+}
+
+cudaError_t launch_decode_int8(int D, const DecodeArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                               int ctas, int smem_bytes, cudaStream_t stream) {
+    const bool w = a.window > 0, two = a.G > 8;
+#define SINKATTN_INT8_LAUNCH(DD, NN, WW) \
+    decode_int8_kernel<DD, NN, WW><<<ctas, Int8Cfg<DD>::kThreads, smem_bytes, stream>>>(kmap, vmap, a)
+    if (D == 64) {
+        if (two) {
+            if (w) SINKATTN_INT8_LAUNCH(64, 2, true); else SINKATTN_INT8_LAUNCH(64, 2, false);
+        } else {
+            if (w) SINKATTN_INT8_LAUNCH(64, 1, true); else SINKATTN_INT8_LAUNCH(64, 1, false);
+        }
+    } else {
+        if (two) {
+            if (w) SINKATTN_INT8_LAUNCH(128, 2, true); else SINKATTN_INT8_LAUNCH(128, 2, false);
+        } else {
+            if (w) SINKATTN_INT8_LAUNCH(128, 1, true); else SINKATTN_INT8_LAUNCH(128, 1, false);
+        }
+    }
+#undef SINKATTN_INT8_LAUNCH
+    return cudaGetLastError();
+}
+
+cudaError_t launch_merge_int8(int D, const DecodeArgs &a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.B * (unsigned)a.Hq);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return D == 64 ? cudaLaunchKernelEx(&cfg, merge_int8_kernel<64>, a)
+                   : cudaLaunchKernelEx(&cfg, merge_int8_kernel<128>, a);
+}
+
+}  // namespace sinkattn

@@ -70,11 +70,18 @@ cudaError_t launch_decode_window(int D, const DecodeArgs &a, const CUtensorMap &
                                  const CUtensorMap &vmap, cudaStream_t stream);
 
 // The same for the decode over an FP8 E4M3 cache (uint8 tensor maps, one box per page).
-// int8: the kernel over an INT8 cache (a.kv_scales set at the launch).
-cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, bool int8, int *ctas, int *warps_per_cta,
+cudaError_t decode_fp8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
                                     int *smem_bytes);
 cudaError_t launch_decode_fp8(int D, const DecodeArgs &a, const CUtensorMap &kmap,
                               const CUtensorMap &vmap, int ctas, int smem_bytes, cudaStream_t stream);
+
+// The same for the decode over an INT8 cache (a.kv_scales set); its own merge of the partial
+// states, launched so that it is in place when the split-KV kernel ends.
+cudaError_t decode_int8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
+                                     int *smem_bytes);
+cudaError_t launch_decode_int8(int D, const DecodeArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                               int ctas, int smem_bytes, cudaStream_t stream);
+cudaError_t launch_merge_int8(int D, const DecodeArgs &a, cudaStream_t stream);
 
 struct AppendArgs {
     const void *k, *v;  // bf16 [T, Hkv, D]
