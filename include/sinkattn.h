@@ -356,12 +356,16 @@ int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, 
                             sinkattn_stream_t stream);
 
 /* The decode over such a cache (q, block_table, seq_lens, sinks, scale, out, lse, descriptor,
- * window and status as for sinkattn_decode; workspace of sinkattn_decode_workspace_size).
+ * window and status as for sinkattn_decode).  Workspace: sinkattn_decode_int8_workspace_size
+ * bytes, 256-byte aligned, its 256-byte header zero before the first call (every call leaves it so
+ * but for status bits); calls that share one must be ordered on the GPU.
  * Codes enter the products exactly, scales multiply fp32 sums; q is taken in fp16 times a power
  * of two of its (sequence, KV head): an entry keeps its 8 bits unless it is more than 2^28 times
  * smaller than the largest of its group.  The probabilities are rounded to fp16 (relative
  * 2^-11 each at most), as in sinkattn_decode_fp8.  (With a sliding window it runs the split-KV
  * kernel too, over the visible pages.) */
+int sinkattn_decode_int8_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
+
 int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
                          const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
                          void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,

@@ -134,9 +134,7 @@ struct DecodeLayout {
     int ctas8, warps_per_cta8, smem8, total_warps8;  // FP8 cache kernel
 };
 
-// int8: ctas8 / smem8 are those of the decode over an INT8 cache, on a grid of at most the FP8
-// kernel's size (the slots are sized for that one).
-int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L, bool int8 = false) {
+int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
     int device = 0;
     int rc = cuda_rc(cudaGetDevice(&device), "cudaGetDevice");
     if (rc) return rc;
@@ -150,13 +148,6 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L, bool int8 = fal
                                          &L->warps_per_cta8, &L->smem8),
                  "fp8 decode launch shape");
     if (rc) return rc;
-    int ctas_int8 = 0;
-    if (int8) {
-        rc = cuda_rc(decode_int8_launch_shape(d->head_dim, G, d->num_seqs, device, &ctas_int8,
-                                              &L->warps_per_cta8, &L->smem8),
-                     "int8 decode launch shape");
-        if (rc) return rc;
-    }
     // Both grids are (SMs x CTAs per SM); keep the CTAs per SM, on fewer SMs' worth of CTAs
     // where max_sms asks for it.  The bf16 split-KV grid also stops at kDecodeInflightBytes of
     // page copies in flight: with every SM at full occupancy its rings hold 25-29 MB, and HBM
@@ -191,10 +182,37 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L, bool int8 = fal
     L->acc = off;
     off += slots * G * d->head_dim * sizeof(float);
     L->total = align_up(off);
-    if (int8) {
-        if (ctas_int8 < L->ctas8) L->ctas8 = ctas_int8;
-        L->total_warps8 = L->ctas8 * L->warps_per_cta8;
-    }
+    return SINKATTN_OK;
+}
+
+// The INT8 decode's workspace: the same parts for its own grid (ctas8, smem8, total_warps8), with a
+// partial state for each chunk of its plan.
+int decode_int8_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
+    int device = 0, sms = 0;
+    int rc = cuda_rc(cudaGetDevice(&device), "cudaGetDevice");
+    if (rc) return rc;
+    const int G = d->num_qo_heads / d->num_kv_heads;
+    rc = cuda_rc(decode_int8_launch_shape(d->head_dim, G, d->num_seqs, device, &L->ctas8, &L->warps_per_cta8,
+                                          &L->smem8),
+                 "int8 decode launch shape");
+    if (rc) return rc;
+    rc = cuda_rc(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute");
+    if (rc) return rc;
+    if (sms > 0 && d->max_sms > 0 && d->max_sms < sms) L->ctas8 = L->ctas8 / sms * d->max_sms;
+    L->total_warps8 = L->ctas8 * L->warps_per_cta8;
+    L->ctas = L->smem = L->total_warps = L->warps_per_cta = 0;  // not this kernel's
+    const size_t slots = (size_t)L->total_warps8 * decode_int8_chunks_per_warp() + 1 +
+                         (size_t)d->num_seqs * d->num_kv_heads;
+    size_t off = kStatusBytes;
+    L->prefix = off;
+    off += align_up(((size_t)d->num_seqs + 1) * 4);
+    L->plan = off;
+    off += kAlign;
+    L->ml = off;
+    off += align_up(slots * G * 2 * sizeof(float));
+    L->acc = off;
+    off += slots * G * d->head_dim * sizeof(float);
+    L->total = align_up(off);
     return SINKATTN_OK;
 }
 
@@ -215,7 +233,7 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || (sinks && !aligned(sinks, 4)) ||
         (lse && !aligned(lse, 4)))
         return SINKATTN_ERR_INVALID_ARG;
-    rc = decode_layout(desc, &P->layout, int8);
+    rc = int8 ? decode_int8_layout(desc, &P->layout) : decode_layout(desc, &P->layout);
     if (rc) return rc;
     if (ws_bytes < P->layout.total) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
     DecodeArgs &a = P->args;
@@ -244,6 +262,8 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
     a.part_acc = reinterpret_cast<float *>(ws + P->layout.acc);
     a.k_scale = nullptr;
     a.v_scale = nullptr;
+    a.sched = nullptr;
+    a.min_chunk = 0;
     a.kv_scales = nullptr;
     a.k_new = nullptr;
     a.v_new = nullptr;
@@ -596,6 +616,17 @@ int sinkattn_decode_fp8(const void *q, const void *k_pages, const void *v_pages,
     return sinkattn_decode_merge(seq_lens, sinks, out, lse, desc, workspace, ws_bytes, stream);
 }
 
+int sinkattn_decode_int8_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
+    if (!bytes) return SINKATTN_ERR_INVALID_ARG;
+    int rc = check_decode_desc(desc);
+    if (rc) return rc;
+    DecodeLayout L;
+    rc = decode_int8_layout(desc, &L);
+    if (rc) return rc;
+    *bytes = L.total;
+    return SINKATTN_OK;
+}
+
 int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
                          const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
                          void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
@@ -616,6 +647,8 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
     if (rc) return rc;
     P.args.kv_scales = kv_scales;
     P.args.total_warps = P.layout.total_warps8;
+    P.args.sched = static_cast<uint32_t *>(workspace) + 32;  // header bytes 128..131
+    P.args.min_chunk = decode_int8_min_chunk(desc->head_dim, P.args.G);
     rc = cuda_rc(launch_decode_int8(desc->head_dim, P.args, kmap, vmap, P.layout.ctas8, P.layout.smem8,
                                     (cudaStream_t)stream),
                  "int8 split-KV decode launch");

@@ -4,10 +4,15 @@
 // The plan, the copies and the products are those of the FP8 decode: every warp takes an equal
 // run of two-page units, S^T = K Q^T and O^T = V^T P^T on m16n8k16 f16 MMAs with the 16 tokens of
 // a page, then head_dim, on the M axis and the query heads on N; the contraction index permuted so
-// that a lane's K fragment is one run of D/4 bytes and its V fragment D/8 bytes of four rows.
+// that a lane's K fragment is one run of D/4 bytes; V comes by transposing 8x8 loads of its byte
+// pairs, which lay the pair of one lane's two tokens beside each other.
 // What the scales and the codes change:
-//   * a code becomes its f16 value by putting its offset form (code + 128) under the exponent of
-//     1024 and taking 1152 off: exact, five instructions for four codes;
+//   * a code is taken as the f16 subnormal (code + 128) 2^-24, whose bits are the code's with the
+//     sign flipped: one AND-XOR for two codes (a shift more for the other two of a word).  The
+//     128 comes off in the MMAs' accumulators: the K products start from -128 2^-24 sum(q), and
+//     what the P of a unit add too much is one MMA of a constant -128 2^-24 against them, added to
+//     O^T.  (As values - the offset form under the exponent of 1024, less 1152 - a page cost 27
+//     instructions more at head_dim 64.)  The detour through 128 costs the fp32 sums under 2 bits;
 //   * K: a page's scale multiplies its 16 scores, together with the softmax scale;
 //   * V: P of a page is taken times s / 2^E, with 2^E the power of two above the largest V scale
 //     the warp has met in this (sequence, head): one rounding to f16, and O^T is summed in the
@@ -19,6 +24,12 @@
 //   * q times a power of two per (sequence, KV head) that puts its largest entry at 2^14 is exact
 //     in f16 whatever its size; the scores take the power back;
 //   * no code is NaN or infinite: slots past a sequence's end need no clearing, P is 0 there.
+// The list of units is cut into chunks of equal length; a warp starts with the chunk of its number
+// and, where there are more chunks than warps, takes further ones from a counter in the workspace
+// header, so that the warps that HBM serves faster do more of the work (equal shares left a tenth
+// of the warps idle on average).  A chunk's partial state has the chunk's number, so no result
+// depends on who took it.  The warp's copy side runs ahead of its arithmetic, over chunk borders
+// too, and leaves what the arithmetic needs to know of a unit beside its pages.
 // The running maximum moves only when a score passes it by more than 8 (log2): P is taken as
 // 2^(s - m + 7), at most 2^15, so a stale maximum costs no precision and the votes, the column
 // maxima and the rescale of O^T drop out of almost every unit.
@@ -35,11 +46,13 @@ namespace sinkattn {
 
 namespace {
 
-template <int D>
+template <int D, int NH>
 struct Int8Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kPPU = 2;  // pages per work unit (32 tokens)
+    // Pages per work unit: 8 KB of K and V for one tile of heads, half of it where the second
+    // tile's accumulators leave few registers; 16 KB a warp in flight.
+    static constexpr int kPPU = (D == 64 ? 4 : 2);
     static constexpr int kStages = 2;
     static constexpr int kPageBytes = kPageSize * D;           // one (page, head) of K or of V codes
     static constexpr int kStageBytes = 2 * kPPU * kPageBytes;  // the unit's K pages, then V pages
@@ -47,26 +60,57 @@ struct Int8Cfg {
     static constexpr int kKSteps = D / 16;  // S^T k-steps over head_dim
     static constexpr int kMTiles = D / 16;  // O^T m-tiles over head_dim
     static constexpr int kKWords = D / 16;  // 32-bit words of K a lane reads per token row
-    static constexpr int kVWords = D / 32;  // 32-bit words of V a lane reads per token row
 };
 
+constexpr int kChunks = 1;       // chunks per warp, at most
 constexpr float kPShift = 7.f;   // P = 2^(s - m + kPShift)
 constexpr float kMaxSlack = 8.f; // the running maximum moves when a score passes it by more
 
-template <int D>
+template <int D, int NH>
 int int8_smem_bytes(int B) {
-    using C = Int8Cfg<D>;
-    // per (warp, stage): its barrier, and per page of its unit two ints and two scales
-    return 1024 /* alignment slack */ + C::kWarps * C::kWarpBytes + C::kWarps * C::kStages * (8 + 16 * C::kPPU) +
+    using C = Int8Cfg<D, NH>;
+    // per (warp, stage): its barrier, a UnitMeta, and a PageMeta for each page of its unit
+    return 1024 /* alignment slack */ + C::kWarps * C::kWarpBytes + C::kWarps * C::kStages * (8 + 16 + 16 * C::kPPU) +
            (3 * B + 1) * 4;
 }
 
+// What the arithmetic needs of a unit: whose it is, and of one of its pages.
+struct __align__(16) UnitMeta {
+    int b, g;   // sequence, KV head
+    int flags;  // kStart | kEnd | kWhole
+    int chunk;
+};
+constexpr int kStart = 1, kEnd = 2, kWhole = 4;  // first / last unit of a segment; the segment is all of (b, g)
+struct __align__(16) PageMeta {
+    float ks, vs;  // K scale * 2^24, V scale (0 for a page that is not there)
+    int nv, lo;    // its keys lo .. nv - 1 are visible
+};
+
+// Codes 0 and 2 (even) or 1 and 3 (odd) of a word as f16 pairs of (code + 128) 2^-24.
+__device__ __forceinline__ uint32_t sub_even(uint32_t w) {
+    uint32_t r;  // (w & mask) ^ sign in one instruction
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(0x00FF00FFu), "r"(0x00800080u));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_odd(uint32_t w) { return sub_even(w >> 8); }
+// D = A B + C with C's columns c0 and c1 in every row.
+__device__ __forceinline__ void mma_f16_16816_from(float (&d)[4], float c0, float c1, uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+constexpr uint32_t kMinus128 = 0x80808080u;  // an f16 pair of -128 * 2^-24
+constexpr float kUp24 = 16777216.f;          // 2^24
+
 // NH: 8-head tiles of the query group (1 for G <= 8, 2 for G = 16).
 template <int D, int NH, bool kWindow>
-__global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 : 3) : (NH == 1 ? 3 : 2))
+__global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 ? 2 : 3)
     decode_int8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const DecodeArgs a) {
-    using C = Int8Cfg<D>;
+    using C = Int8Cfg<D, NH>;
     constexpr int S = C::kStages, U = C::kPPU;
     // the merge may take its place on the SMs; it waits for this grid before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -74,10 +118,9 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kWarps * C::kWarpBytes);
-    float2 *s_scale = reinterpret_cast<float2 *>(bars + C::kWarps * S);  // [warp][stage][page] (K, V)
-    int *s_nvalid = reinterpret_cast<int *>(s_scale + C::kWarps * S * U);  // [warp][stage][page]
-    int *s_lo = s_nvalid + C::kWarps * S * U;  // [warp][stage][page] first key in the window
-    int *s_prefix = s_lo + C::kWarps * S * U;
+    UnitMeta *s_unit = reinterpret_cast<UnitMeta *>(bars + C::kWarps * S);     // [warp][stage]
+    PageMeta *s_meta = reinterpret_cast<PageMeta *>(s_unit + C::kWarps * S);  // [warp][stage][page]
+    int *s_prefix = reinterpret_cast<int *>(s_meta + C::kWarps * S * U);
     int *s_len = s_prefix + a.B + 1;
     int *s_first = s_len + a.B;
 
@@ -91,8 +134,15 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
     scan_pages<U>(a, s_prefix, s_len, s_first);  // contains __syncthreads
 
     const int64_t T = (int64_t)a.Hkv * s_prefix[a.B];
+    // units of a chunk: an equal share of each warp, or of kChunks parts of it where the parts are
+    // still kMinChunk units (whose partial state then is a few percent of the bytes read)
     int64_t per = (T + a.total_warps - 1) / a.total_warps;
     if (per < kMinUnitsPerWarp) per = kMinUnitsPerWarp;
+    if (per >= 2 * a.min_chunk) {
+        const int64_t part = (T + (int64_t)a.total_warps * kChunks - 1) / ((int64_t)a.total_warps * kChunks);
+        per = part > a.min_chunk ? part : a.min_chunk;
+    }
+    const int n_chunks = (int)((T + per - 1) / per);
     if (blockIdx.x == 0) {
         for (int b = tid; b <= a.B; b += blockDim.x) a.ws_prefix[b] = s_prefix[b];
         if (tid == 0) {
@@ -100,156 +150,170 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
             a.ws_plan[1] = per;
         }
     }
-    const int wglob = blockIdx.x * C::kWarps + wid;
-    const int64_t u_begin = (int64_t)wglob * per;
-    if (u_begin >= T) return;  // warp-uniform; no block-wide barrier follows
-    const int n_units = (int)min(per, T - u_begin);
+    int p_chunk = blockIdx.x * C::kWarps + wid;  // the copy side's chunk
+    if (p_chunk >= n_chunks) return;  // warp-uniform; no block-wide barrier follows
 
     uint8_t *wbuf = smem + wid * C::kWarpBytes;
     uint64_t *wbar = bars + wid * S;
-    int *wnv = s_nvalid + wid * S * U;
-    int *wlo = s_lo + wid * S * U;
-    float2 *wsc = s_scale + wid * S * U;
+    UnitMeta *wunit = s_unit + wid * S;
+    PageMeta *wmeta = s_meta + wid * S * U;
 
-    Cursor cur;
-    {
+    // The copy side: its position, the units left of its chunk, and the chunk after it (asked for
+    // when it began this one).
+    Cursor pc;
+    int p_left = 0, p_seg0 = 0, produced = 0;
+    uint32_t p_next = 0;
+    auto begin_chunk = [&]() {
+        const int64_t u0 = (int64_t)p_chunk * per;
+        p_left = (int)min(per, T - u0);
         int lo = 0, hi = a.B - 1;
         while (lo < hi) {
             int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)a.Hkv * s_prefix[mid] <= u_begin)
+            if ((int64_t)a.Hkv * s_prefix[mid] <= u0)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        cur.b = lo;
-        cur.pb = s_prefix[lo + 1] - s_prefix[lo];
-        const int64_t local = u_begin - (int64_t)a.Hkv * s_prefix[lo];
-        cur.g = (int)(local / cur.pb);
-        cur.p = (int)(local % cur.pb);
-    }
-    auto advance = [&](Cursor &c) {
-        if (++c.p == c.pb) {
-            c.p = 0;
-            if (++c.g == a.Hkv) {
-                c.g = 0;
-                do {
-                    ++c.b;
-                    c.pb = c.b < a.B ? s_prefix[c.b + 1] - s_prefix[c.b] : 1;
-                } while (c.b < a.B && c.pb == 0);
-            }
-        }
+        pc.b = lo;
+        pc.pb = s_prefix[lo + 1] - s_prefix[lo];
+        const int local = (int)(u0 - (int64_t)a.Hkv * s_prefix[lo]);
+        pc.g = local / pc.pb;
+        pc.p = local % pc.pb;
+        p_seg0 = pc.p;
+        p_next = (uint32_t)n_chunks;
+        if (n_chunks > a.total_warps && lane == 0) p_next = (uint32_t)a.total_warps + atomicAdd(a.sched, 1u);
     };
+    begin_chunk();
 
     // Block-table window: lane l holds the entry of visible page win_p0 + l of sequence
-    // win_b (-1 past its last page) and that page's scales for KV head win_g.
-    int win_b = -1, win_p0 = 0, win_val = -1, win_g = -1;
-    float2 win_sc = make_float2(0.f, 0.f);
-    auto page_entry = [&](int b, int g, int first, int npv, int pp) -> int {
-        const int p0 = pp & ~31;
-        const bool moved = b != win_b || p0 != win_p0;
-        if (moved) {
-            win_b = b;
-            win_p0 = p0;
-            const int q = p0 + lane;
-            win_val = q < npv ? a.block_table[(int64_t)b * a.max_pages + first + q] : -1;
-        }
-        if (moved || g != win_g) {
-            win_g = g;
-            if (win_val >= 0 && win_val < a.num_pages)
-                win_sc = __ldg(reinterpret_cast<const float2 *>(a.kv_scales) + (int64_t)win_val * a.Hkv + g);
-        }
-        return __shfl_sync(0xffffffffu, win_val, pp - p0);
+    // win_b (-1 past its last page) and that page's scales for KV head win_g; the entries of
+    // the next 32 pages are loaded with it, and their scales halfway through it.
+    int win_b = -1, win_p0 = 0, win_g = -1, win_val = -1, nxt_val = -1;
+    float2 win_sc = make_float2(0.f, 0.f), nxt_sc = win_sc;
+    bool nxt_ready = false;
+    auto entry = [&](int b, int first, int npv, int q) {
+        return q < npv ? a.block_table[(int64_t)b * a.max_pages + first + q] : -1;
     };
-
+    auto scales = [&](int pg, int g) {
+        return pg >= 0 && pg < a.num_pages
+                   ? __ldg(reinterpret_cast<const float2 *>(a.kv_scales) + (int64_t)pg * a.Hkv + g)
+                   : make_float2(0.f, 0.f);
+    };
     const uint64_t policy = l2_policy_evict_first();
-    auto produce = [&](int stage, const Cursor &c) {
+    // The next unit, if there is one, into a stage: lanes 0 .. U - 1 take a page each.
+    auto produce = [&](int stage) {
+        if (p_left == 0) {
+            const uint32_t next = __shfl_sync(0xffffffffu, p_next, 0);
+            if (next >= (uint32_t)n_chunks) return;
+            p_chunk = (int)next;
+            begin_chunk();
+        }
+        const Cursor c = pc;
+        --p_left;
+        ++produced;
+        int flags = 0;
+        if (c.p == p_seg0) flags |= kStart;
+        if (c.p == c.pb - 1 || p_left == 0) flags |= kEnd;
+        if (c.p == c.pb - 1 && p_seg0 == 0) flags |= kWhole;
+        if (++pc.p == pc.pb) {
+            pc.p = p_seg0 = 0;
+            if (++pc.g == a.Hkv) {
+                pc.g = 0;
+                do {
+                    ++pc.b;
+                    pc.pb = pc.b < a.B ? s_prefix[pc.b + 1] - s_prefix[pc.b] : 1;
+                } while (pc.b < a.B && pc.pb == 0);
+            }
+        }
         const int first = kWindow ? s_first[c.b] : 0;
         const int L = s_len[c.b];
         const int npv = (L + kPageSize - 1) / kPageSize - first;  // pages the query sees
-        int pg[U];
-        float2 sc[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int pp = c.p * U + j;
-            pg[j] = pp < npv ? page_entry(c.b, c.g, first, npv, pp) : -2;  // -2: no such page
-            sc[j].x = __shfl_sync(0xffffffffu, win_sc.x, pp & 31);
-            sc[j].y = __shfl_sync(0xffffffffu, win_sc.y, pp & 31);
-        }
-        if (lane == 0) {
-            uint8_t *kb = wbuf + stage * C::kStageBytes;
-            uint32_t bytes = 0;
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int page = first + c.p * U + j;  // page index within the sequence
-                const bool ok = pg[j] >= 0 && pg[j] < a.num_pages;
-                bad |= pg[j] != -2 && !ok;
-                wnv[stage * U + j] = ok ? min(kPageSize, L - kPageSize * page) : 0;
-                wsc[stage * U + j] = ok ? sc[j] : make_float2(0.f, 0.f);
-                // keys before the sliding window in this page are hidden
-                if (kWindow) wlo[stage * U + j] = max(0, L - a.window - kPageSize * page);
-                if (ok) bytes += 2 * C::kPageBytes;
-            }
-            if (bad) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
-            uint64_t *bar = &wbar[stage];
-            if (bytes) {
-                mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-                for (int j = 0; j < U; ++j)
-                    if (pg[j] >= 0 && pg[j] < a.num_pages) {
-                        tma_load_4d_hint(kb + j * C::kPageBytes, &kmap, bar, 0, 0, c.g, pg[j], policy);
-                        tma_load_4d_hint(kb + (U + j) * C::kPageBytes, &vmap, bar, 0, 0, c.g, pg[j],
-                                         policy);
-                    }
+        const int pp0 = c.p * U, p0 = pp0 & ~31;
+        if (c.b != win_b || p0 != win_p0 || c.g != win_g) {  // warp-uniform
+            if (nxt_ready && c.b == win_b && c.g == win_g && p0 == win_p0 + 32) {
+                win_val = nxt_val;
+                win_sc = nxt_sc;
             } else {
-                mbar_arrive(bar);
+                if (c.b != win_b || p0 != win_p0) win_val = entry(c.b, first, npv, p0 + lane);
+                win_sc = scales(win_val, c.g);
             }
+            nxt_val = entry(c.b, first, npv, p0 + 32 + lane);
+            nxt_ready = false;
+            win_b = c.b;
+            win_p0 = p0;
+            win_g = c.g;
+        } else if (!nxt_ready && pp0 - p0 >= 16) {
+            nxt_sc = scales(nxt_val, c.g);
+            nxt_ready = true;
+        }
+        const int src = (pp0 + (lane & (U - 1))) & 31;
+        const int pg = __shfl_sync(0xffffffffu, win_val, src);
+        const float ks = __shfl_sync(0xffffffffu, win_sc.x, src), vs = __shfl_sync(0xffffffffu, win_sc.y, src);
+        const bool in = lane < U && pp0 + lane < npv, ok = in && pg >= 0 && pg < a.num_pages;
+        if (in && !ok) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+        if (lane < U) {
+            const int key0 = kPageSize * (first + pp0 + lane);  // position of the page's first key
+            PageMeta m;
+            m.ks = ok ? ks * kUp24 : 0.f;
+            m.vs = ok ? vs : 0.f;
+            m.nv = ok ? min(kPageSize, L - key0) : 0;
+            m.lo = kWindow ? max(0, L - a.window - key0) : 0;  // keys before the sliding window are hidden
+            wmeta[stage * U + lane] = m;
+        }
+        const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+        __syncwarp();  // the pages' metadata before the arrival
+        uint64_t *bar = &wbar[stage];
+        if (lane == 0) {
+            wunit[stage] = UnitMeta{c.b, c.g, flags, p_chunk};
+            if (oks)
+                mbar_arrive_expect_tx(bar, __popc(oks) * 2 * C::kPageBytes);
+            else
+                mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (ok) {
+            uint8_t *kb = wbuf + stage * C::kStageBytes + lane * C::kPageBytes;
+            tma_load_4d_hint(kb, &kmap, bar, 0, 0, c.g, pg, policy);
+            tma_load_4d_hint(kb + U * C::kPageBytes, &vmap, bar, 0, 0, c.g, pg, policy);
         }
     };
 
-    Cursor pc = cur;
-    const int n_pro = min(S, n_units);
-    for (int u = 0; u < n_pro; ++u) {
-        produce(u, pc);
-        advance(pc);
-    }
+#pragma unroll 1
+    for (int st = 0; st < S; ++st) produce(st);
 
     const int gr = lane >> 2, t4 = lane & 3;
     // K: this lane's MMA rows are tokens gr and gr + 8; its bytes are [t4 * D/4, +D/4)
-    const int rk0 = tok_row<D>(gr), rk1 = rk0 + 8;
     uint32_t koff[2][C::kKWords / 4];
 #pragma unroll
     for (int i = 0; i < C::kKWords / 4; ++i) {
-        koff[0][i] = swz<D>(rk0, t4 * (D / 4) + 16 * i);
-        koff[1][i] = swz<D>(rk1, t4 * (D / 4) + 16 * i);
+        koff[0][i] = swz<D>(gr, t4 * (D / 4) + 16 * i);
+        koff[1][i] = swz<D>(gr + 8, t4 * (D / 4) + 16 * i);
     }
-    // V: tokens 2t, 2t+1, 2t+8, 2t+9 of the MMA's k axis; bytes [gr * D/8, +D/8)
-    uint32_t voff[4];
-    {
-        const int ks[4] = {2 * t4, 2 * t4 + 1, 2 * t4 + 8, 2 * t4 + 9};
+    // V: the lane's row address of the transposing loads, 16 bytes of a token each: matrices 0 and 1
+    // are tokens 0-7 and 8-15 of one 16-byte column block, 2 and 3 of the next
+    uint32_t voff[D / 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) voff[i] = swz<D>(tok_row<D>(ks[i]), gr * (D / 8));
-    }
+    for (int i = 0; i < D / 32; ++i) voff[i] = swz<D>(lane & 15, 16 * (2 * i + (lane >> 4)));
 
     uint32_t qf[C::kKSteps][NH][2];
     float acc[C::kMTiles][NH][4];
     float mr[NH][2], ls[NH][2];
-    float f0 = 0.f;                   // score factor but for the page's scale
+    float qoff[NH][2];                // -128 * 2^-24 * sum of q, per head
+    float f0 = 0.f;                   // score factor but for the page's scale and 2^24
     float v_top = 0.f, v_inv = 0.f;   // 2^E and 2^-E
-    int seg_p0 = cur.p;
-    bool seg_start = true;
 
-    for (int u = 0; u < n_units; ++u) {
+    for (int u = 0; u < produced; ++u) {
         const int stage = u % S;
         if (!__all_sync(0xffffffffu, mbar_wait_sleep(&wbar[stage], (uint32_t)((u / S) & 1), a.wait_limit_ns))) {
             // give up (all lanes together: the outcome is voted): record it, let the copies
             // already issued land, leave
             if (lane == 0) set_status(a.status, SINKATTN_STATUS_WAIT_TIMEOUT);
-            for (int v = u; v < min(n_units, u + S); ++v)
+            for (int v = u; v < produced; ++v)
                 mbar_wait(&wbar[v % S], (uint32_t)((v / S) & 1), kDrainLimitNs);
             return;
         }
-        if (seg_start) {
+        const UnitMeta cur = wunit[stage];
+        if (cur.flags & kStart) {
             const __nv_bfloat16 *qg = reinterpret_cast<const __nv_bfloat16 *>(a.q) +
                                       ((int64_t)cur.b * a.Hq + (int64_t)cur.g * a.G) * D;
             uint32_t mx = 0;  // the largest finite |q| of the lane, as bf16 bits
@@ -283,9 +347,21 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
             for (int kk = 0; kk < C::kKSteps; ++kk)
 #pragma unroll
                 for (int nt = 0; nt < NH; ++nt) {
-                    qf[kk][nt][0] = bf16x2_to_f16x2_times(qf[kk][nt][0], down);
-                    qf[kk][nt][1] = bf16x2_to_f16x2_times(qf[kk][nt][1], down);
+                    // (elements 0, 1) and (2, 3) to (0, 2) and (1, 3), the order of the codes' pairs
+                    const uint32_t x = bf16x2_to_f16x2_times(qf[kk][nt][0], down);
+                    const uint32_t y = bf16x2_to_f16x2_times(qf[kk][nt][1], down);
+                    qf[kk][nt][0] = __byte_perm(x, y, 0x5410);
+                    qf[kk][nt][1] = __byte_perm(x, y, 0x7632);
                 }
+#pragma unroll
+            for (int nt = 0; nt < NH; ++nt) {
+                float o[4] = {0.f, 0.f, 0.f, 0.f};  // every row the same: columns 2 t4 and 2 t4 + 1
+#pragma unroll
+                for (int kk = 0; kk < C::kKSteps; ++kk)
+                    mma_f16_16816(o, kMinus128, kMinus128, kMinus128, kMinus128, qf[kk][nt][0], qf[kk][nt][1]);
+                qoff[nt][0] = o[0];
+                qoff[nt][1] = o[1];
+            }
 #pragma unroll
             for (int mt = 0; mt < C::kMTiles; ++mt)
 #pragma unroll
@@ -297,8 +373,6 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
                 ls[nt][0] = ls[nt][1] = 0.f;
             }
             v_top = v_inv = 0.f;
-            seg_p0 = cur.p;
-            seg_start = false;
         }
 
         const uint8_t *kb = wbuf + stage * C::kStageBytes;  // K of page j at kb + j * kPageBytes
@@ -309,56 +383,57 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
         float s[U][NH][4];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            nv[j] = wnv[stage * U + j];
-            klo[j] = kWindow ? wlo[stage * U + j] : 0;
-            psc[j] = wsc[stage * U + j];
+            const PageMeta m = wmeta[stage * U + j];
+            nv[j] = m.nv;
+            klo[j] = kWindow ? m.lo : 0;
+            psc[j] = make_float2(m.ks, m.vs);
             uint32_t kw[2][C::kKWords];  // K rows gr, gr + 8: the lane's run of D/4 bytes
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int i = 0; i < C::kKWords / 4; ++i) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(kb + j * C::kPageBytes + koff[r][i]);
-                    kw[r][4 * i] = w.x ^ 0x80808080u;
-                    kw[r][4 * i + 1] = w.y ^ 0x80808080u;
-                    kw[r][4 * i + 2] = w.z ^ 0x80808080u;
-                    kw[r][4 * i + 3] = w.w ^ 0x80808080u;
+                    kw[r][4 * i] = w.x;
+                    kw[r][4 * i + 1] = w.y;
+                    kw[r][4 * i + 2] = w.z;
+                    kw[r][4 * i + 3] = w.w;
                 }
-#pragma unroll
-            for (int nt = 0; nt < NH; ++nt) s[j][nt][0] = s[j][nt][1] = s[j][nt][2] = s[j][nt][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < C::kKSteps; ++kk) {
-                const uint32_t a0 = int8x2_lo_to_f16x2(kw[0][kk]), a2 = int8x2_hi_to_f16x2(kw[0][kk]);
-                const uint32_t a1 = int8x2_lo_to_f16x2(kw[1][kk]), a3 = int8x2_hi_to_f16x2(kw[1][kk]);
+                const uint32_t a0 = sub_even(kw[0][kk]), a2 = sub_odd(kw[0][kk]);
+                const uint32_t a1 = sub_even(kw[1][kk]), a3 = sub_odd(kw[1][kk]);
 #pragma unroll
-                for (int nt = 0; nt < NH; ++nt)
-                    mma_f16_16816(s[j][nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
-            }
-        }
-        // Take the unit's V into registers and hand the stage back to the copy engine: the next
-        // copy then overlaps the rest of this unit's arithmetic.
-        uint32_t vw[U][4][C::kVWords];  // V rows of tokens 2t, 2t+1, 2t+8, 2t+9: D/8 bytes
-#pragma unroll
-        for (int j = 0; j < U; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t *src = vb + j * C::kPageBytes + voff[i];
-                if (D == 64) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
-                    vw[j][i][0] = x.x;
-                    vw[j][i][1] = x.y;
-                } else {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                    vw[j][i][0] = x.x;
-                    vw[j][i][1] = x.y;
-                    vw[j][i][2 % C::kVWords] = x.z;
-                    vw[j][i][3 % C::kVWords] = x.w;
+                for (int nt = 0; nt < NH; ++nt) {
+                    if (kk == 0)
+                        mma_f16_16816_from(s[j][nt], qoff[nt][0], qoff[nt][1], a0, a1, a2, a3, qf[0][nt][0], qf[0][nt][1]);
+                    else
+                        mma_f16_16816(s[j][nt], a0, a1, a2, a3, qf[kk][nt][0], qf[kk][nt][1]);
                 }
             }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (u + S < n_units) {
-            produce(stage, pc);
-            advance(pc);
+        }
+        // V of a page, by transposing loads of its byte pairs: v[mt][0] the pairs (16mt + 2gr, + 1) of
+        // tokens 2 t4 and 2 t4 + 1, v[mt][1] of the tokens 8 further
+        auto load_v = [&](int j, uint32_t (&v)[C::kMTiles][2]) {
+            const uint32_t base = smem_u32(vb) + j * C::kPageBytes;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                ldsm_x4_t(base + voff[i], v[2 * i][0], v[2 * i][1], v[2 * i + 1][0], v[2 * i + 1][1]);
+        };
+        // the stage back to the copy engine
+        auto hand_back = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            produce(stage);
+        };
+        // One tile of heads: the unit's V goes into registers and the stage back at once, so that the
+        // next copy overlaps the rest of this unit's arithmetic.  Two tiles: their accumulators leave
+        // no room for that at three CTAs an SM, and the third CTA is worth more.
+        constexpr bool kLateV = NH == 2;
+        uint32_t vw[kLateV ? 1 : U][C::kMTiles][2];
+        if (!kLateV) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) load_v(j, vw[kLateV ? 0 : j]);
+            hand_back();
         }
 
         // scores, hidden keys at -inf (every page but a sequence's last, and a window's first, is whole)
@@ -374,7 +449,7 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
                 s[j][nt][3] *= f;
             }
             if (nv[j] < kPageSize || (kWindow && klo[j] > 0)) {  // warp-uniform
-                const bool ok0 = rk0 < nv[j] && rk0 >= klo[j], ok1 = rk1 < nv[j] && rk1 >= klo[j];
+                const bool ok0 = gr < nv[j] && gr >= klo[j], ok1 = gr + 8 < nv[j] && gr + 8 >= klo[j];
 #pragma unroll
                 for (int nt = 0; nt < NH; ++nt) {
                     s[j][nt][0] = ok0 ? s[j][nt][0] : -INFINITY;
@@ -383,20 +458,23 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
                     s[j][nt][3] = ok1 ? s[j][nt][3] : -INFINITY;
                 }
             }
-#pragma unroll
-            for (int nt = 0; nt < NH; ++nt)
-                raise |= fmaxf(s[j][nt][0], s[j][nt][2]) > mr[nt][0] + kMaxSlack ||
-                         fmaxf(s[j][nt][1], s[j][nt][3]) > mr[nt][1] + kMaxSlack;
         }
+        float cm[NH][2];  // the lane's maximum per column
+#pragma unroll
+        for (int nt = 0; nt < NH; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                cm[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+                for (int j = 1; j < U; ++j) cm[nt][e] = fmax3(cm[nt][e], s[j][nt][e], s[j][nt][2 + e]);
+                raise |= cm[nt][e] > mr[nt][e] + kMaxSlack;
+            }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = s[0][nt][e];
-#pragma unroll
-                    for (int j = 0; j < U; ++j) x = fmax3(x, s[j][nt][e], s[j][nt][2 + e]);
-                    x = col_max(x);
+                    const float x = col_max(cm[nt][e]);
                     const float mn = x > mr[nt][e] + kMaxSlack ? x : mr[nt][e];
                     const float al = mr[nt][e] == -INFINITY ? 0.f : fast_exp2(mr[nt][e] - mn);
                     mr[nt][e] = mn;
@@ -409,7 +487,9 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
                 }
         }
         // a V scale above every one so far: O^T to the next power of two, exactly
-        const float vmx = fmaxf(psc[0].y, psc[1].y);
+        float vmx = psc[0].y;
+#pragma unroll
+        for (int j = 1; j < U; ++j) vmx = fmaxf(vmx, psc[j].y);
         if (vmx > v_top) {  // warp-uniform
             const float top = __uint_as_float((__float_as_uint(vmx) + 0x7FFFFFu) & 0x7F800000u);
             const float inv = 1.0f / top, move = v_top * inv;
@@ -440,35 +520,45 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
             }
         }
 
-        // O^T += V^T P^T, one 16-token k-step per page
+        // O^T += V^T P^T, one 16-token k-step per page; first what the offset codes will add too much
+#pragma unroll
+        for (int nt = 0; nt < NH; ++nt) {
+            float o[4];
+            mma_f16_16816_from(o, 0.f, 0.f, kMinus128, kMinus128, kMinus128, kMinus128, pb[0][nt][0], pb[0][nt][1]);
+#pragma unroll
+            for (int j = 1; j < U; ++j)
+                mma_f16_16816(o, kMinus128, kMinus128, kMinus128, kMinus128, pb[j][nt][0], pb[j][nt][1]);
+            const float2 off = make_float2(o[0], o[1]);
+#pragma unroll
+            for (int mt = 0; mt < C::kMTiles; ++mt) {
+                const float2 x = fadd2(make_float2(acc[mt][nt][0], acc[mt][nt][1]), off);
+                const float2 y = fadd2(make_float2(acc[mt][nt][2], acc[mt][nt][3]), off);
+                acc[mt][nt][0] = x.x;
+                acc[mt][nt][1] = x.y;
+                acc[mt][nt][2] = y.x;
+                acc[mt][nt][3] = y.y;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            // word layout per token row: [half 0 (rows gr): D/64 words][half 1 (rows gr+8)]
+            uint32_t(&v)[C::kMTiles][2] = vw[kLateV ? 0 : j];
+            if (kLateV) load_v(j, v);
+            // rows 0-7 of m-tile mt are head_dim 16mt + 2gr, rows 8-15 the odd ones beside them
 #pragma unroll
-            for (int mp = 0; mp < C::kMTiles / 2; ++mp) {  // m-tiles 2mp, 2mp + 1
-                const int wi = (mp >> 1), sel = (mp & 1) ? 0x7362 : 0x5140;
-                const uint32_t x00 = __byte_perm(vw[j][0][wi], vw[j][1][wi], sel) ^ 0x80808080u;  // half 0, tokens 2t, 2t+1
-                const uint32_t x01 = __byte_perm(vw[j][0][wi + D / 64], vw[j][1][wi + D / 64], sel) ^ 0x80808080u;  // half 1
-                const uint32_t x10 = __byte_perm(vw[j][2][wi], vw[j][3][wi], sel) ^ 0x80808080u;  // half 0, tokens + 8
-                const uint32_t x11 = __byte_perm(vw[j][2][wi + D / 64], vw[j][3][wi + D / 64], sel) ^ 0x80808080u;
+            for (int mt = 0; mt < C::kMTiles; ++mt) {
+                const uint32_t a0 = sub_even(v[mt][0]), a1 = sub_odd(v[mt][0]);
+                const uint32_t a2 = sub_even(v[mt][1]), a3 = sub_odd(v[mt][1]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int mt = 2 * mp + e;
-                    const uint32_t a0 = e ? int8x2_hi_to_f16x2(x00) : int8x2_lo_to_f16x2(x00);
-                    const uint32_t a1 = e ? int8x2_hi_to_f16x2(x01) : int8x2_lo_to_f16x2(x01);
-                    const uint32_t a2 = e ? int8x2_hi_to_f16x2(x10) : int8x2_lo_to_f16x2(x10);
-                    const uint32_t a3 = e ? int8x2_hi_to_f16x2(x11) : int8x2_lo_to_f16x2(x11);
-#pragma unroll
-                    for (int nt = 0; nt < NH; ++nt)
-                        mma_f16_16816(acc[mt][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
-                }
+                for (int nt = 0; nt < NH; ++nt)
+                    mma_f16_16816(acc[mt][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
             }
         }
 
-        const bool seg_end = (cur.p == cur.pb - 1) || (u == n_units - 1);
-        if (seg_end) {
-            const bool whole = seg_p0 == 0 && cur.p == cur.pb - 1;
-            const int64_t slot = (int64_t)wglob + (int64_t)cur.b * a.Hkv + cur.g;
+        if (kLateV) hand_back();
+
+        if (cur.flags & kEnd) {
+            const bool whole = cur.flags & kWhole;
+            const int64_t slot = (int64_t)cur.chunk + (int64_t)cur.b * a.Hkv + cur.g;
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt)
 #pragma unroll
@@ -489,40 +579,24 @@ __global__ void __launch_bounds__(Int8Cfg<D>::kThreads, D == 64 ? (NH == 1 ? 4 :
                             scl = wm / den;
                             lse2 = M + log2f(den);
                         }
-                        // the lane's D/8 outputs of this head are contiguous: half 0 (MMA
-                        // rows gr) then half 1 (rows gr + 8), D/16 each
-                        uint32_t w[D / 16];
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                            for (int j = 0; j < D / 32; ++j)
-                                w[hf * (D / 32) + j] = pack_bf16x2(acc[2 * j][nt][2 * hf + e] * scl * v_top,
-                                                                   acc[2 * j + 1][nt][2 * hf + e] * scl * v_top);
                         __nv_bfloat16 *og = reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                                            ((int64_t)cur.b * a.Hq + h) * D + gr * (D / 8);
+                                            ((int64_t)cur.b * a.Hq + h) * D + 2 * gr;
 #pragma unroll
-                        for (int i = 0; i < D / 64; ++i)
-                            *reinterpret_cast<uint4 *>(og + 8 * i) =
-                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                        for (int mt = 0; mt < C::kMTiles; ++mt)
+                            *reinterpret_cast<uint32_t *>(og + 16 * mt) = pack_bf16x2(
+                                acc[mt][nt][e] * kUp24 * scl * v_top, acc[mt][nt][2 + e] * kUp24 * scl * v_top);
                         if (a.lse && gr == 0) a.lse[(int64_t)cur.b * a.Hq + h] = lse2 * kLn2;
                     } else {
                         const int64_t row = slot * a.G + hc;
-                        float f[D / 8];
+                        float *pa = a.part_acc + row * D + 2 * gr;
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                            for (int mt = 0; mt < D / 16; ++mt) f[hf * (D / 16) + mt] = acc[mt][nt][2 * hf + e] * v_top;
-                        float *pa = a.part_acc + row * D + gr * (D / 8);
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i)
-                            *reinterpret_cast<float4 *>(pa + 4 * i) =
-                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                        for (int mt = 0; mt < C::kMTiles; ++mt)
+                            *reinterpret_cast<float2 *>(pa + 16 * mt) =
+                                make_float2(acc[mt][nt][e] * kUp24 * v_top, acc[mt][nt][2 + e] * kUp24 * v_top);
                         if (gr == 0) *reinterpret_cast<float2 *>(a.part_ml + row * 2) = make_float2(m, L);
                     }
                 }
-            seg_start = true;
         }
-        advance(cur);
     }
 }
 
@@ -537,6 +611,7 @@ __global__ void __launch_bounds__(128) merge_int8_kernel(const DecodeArgs a) {
     __shared__ float4 s_o[kParts][kQuads];
     __shared__ float2 s_ml[kParts];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0;  // for the next call on this workspace
     const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, g = h / a.G, r = h % a.G;
     const int d4 = threadIdx.x % kQuads, part = threadIdx.x / kQuads;
     const int p0 = a.ws_prefix[b], pb = a.ws_prefix[b + 1] - p0;
@@ -606,8 +681,8 @@ __global__ void __launch_bounds__(128) merge_int8_kernel(const DecodeArgs a) {
 
 template <int D, int NH>
 cudaError_t int8_shape_for(int B, int device, int *ctas, int *warps, int *smem) {
-    using C = Int8Cfg<D>;
-    const int bytes = int8_smem_bytes<D>(B);
+    using C = Int8Cfg<D, NH>;
+    const int bytes = int8_smem_bytes<D, NH>(B);
     int optin = 0, sms = 0, occ = 1 << 30;
     cudaError_t e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
     if (e != cudaSuccess) return e;
@@ -636,6 +711,16 @@ cudaError_t int8_shape_for(int B, int device, int *ctas, int *warps, int *smem) 
 }
 
 }  // namespace
+
+int decode_int8_chunks_per_warp() { return kChunks; }
+
+// A chunk's partial state is written and read once, 2 x 4 G D bytes beside the ~8 KB (4 KB with two
+// tiles of heads) of a unit: 3 % of the chunk's bytes at most.
+int decode_int8_min_chunk(int D, int G) {
+    const int unit = G > 8 ? 4096 : 8192;
+    const int n = (33 * 8 * G * D + unit - 1) / unit;
+    return n > 8 ? n : 8;  // and not so short that its start and end show
+}
 
 cudaError_t decode_int8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
                                      int *smem_bytes) {
@@ -678,7 +763,7 @@ cudaError_t launch_decode_int8(int D, const DecodeArgs &a, const CUtensorMap &km
                                int ctas, int smem_bytes, cudaStream_t stream) {
     const bool w = a.window > 0, two = a.G > 8;
 #define SINKATTN_INT8_LAUNCH(DD, NN, WW) \
-    decode_int8_kernel<DD, NN, WW><<<ctas, Int8Cfg<DD>::kThreads, smem_bytes, stream>>>(kmap, vmap, a)
+    decode_int8_kernel<DD, NN, WW><<<ctas, Int8Cfg<DD, NN>::kThreads, smem_bytes, stream>>>(kmap, vmap, a)
     if (D == 64) {
         if (two) {
             if (w) SINKATTN_INT8_LAUNCH(64, 2, true); else SINKATTN_INT8_LAUNCH(64, 2, false);

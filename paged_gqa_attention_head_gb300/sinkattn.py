@@ -79,6 +79,7 @@ SIGNATURES = {
                                               _P]),
     "sinkattn_append_kv_int8": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _P, _DP, _P,
                                                _SZ, _P]),
+    "sinkattn_decode_int8_workspace_size": (ctypes.c_int, [_DP, ctypes.POINTER(_SZ)]),
     "sinkattn_decode_int8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_prefill_int8": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP,
                                              _P, _SZ, _P]),
@@ -725,6 +726,14 @@ def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, k
     return k_pages, v_pages, kv_scales
 
 
+def decode_int8_workspace_size(desc: PagedDesc) -> int:
+    """Bytes of workspace that decode_int8 needs for desc on the current device."""
+    c = _SZ()
+    _check(load().sinkattn_decode_int8_workspace_size(ctypes.byref(desc), ctypes.byref(c)),
+           "decode_int8_workspace_size")
+    return c.value
+
+
 def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=None, scale=None, out=None,
                 lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0, wait_limit_us=0):
     """Split-KV paged decode over an INT8 cache with a scale per page and KV head
@@ -732,19 +741,37 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
     dev = _need_cuda(q, "q")
     _need(q, "q", torch.bfloat16, dev, 3)
     _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
     _need_int8_cache(k_pages, v_pages, kv_scales, dev)
-    if out is not None and out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is not None and lse.shape != q.shape[:2]:
-        raise ValueError("lse must be [B, Hq]")
+    B, Hq, D = q.shape
+    num_pages, Hkv, _, D2 = k_pages.shape
+    if D2 != D:
+        raise ValueError("k_pages / v_pages must be [num_pages, Hkv, 16, D] matching q")
+    if block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table / seq_lens rows must equal the batch")
+    if sinks is not None:
+        _need(sinks, "sinks", torch.float32, dev, 1)
+        if sinks.shape[0] != Hq:
+            raise ValueError("sinks must have one entry per query head")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, dev, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
+    else:
+        _need(lse, "lse", torch.float32, dev, 2)
+        if tuple(lse.shape) != (B, Hq):
+            raise ValueError("lse must be [B, Hq]")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     with torch.cuda.device(dev):
-        if workspace_buf is None:
-            desc = paged_desc(q.shape[0], q.shape[1], k_pages.shape[1], q.shape[2], k_pages.shape[0],
-                              block_table.shape[1], window=window, max_sms=max_sms, wait_limit_us=wait_limit_us)
-            workspace_buf = _stream_workspace(decode_workspace_size(desc), dev, "decode")
-        desc, out, lse, ws, scale = _decode_prep(q, k_pages, v_pages, block_table, seq_lens, sinks, scale, out, lse,
-                                                 workspace_buf, return_lse, window, kv_dtype=torch.int8,
-                                                 max_sms=max_sms, wait_limit_us=wait_limit_us)
+        desc = paged_desc(B, Hq, Hkv, D, num_pages, block_table.shape[1], window=window, max_sms=max_sms,
+                          wait_limit_us=wait_limit_us)
+        ws = workspace_buf
+        if ws is None:
+            ws = _stream_workspace(decode_int8_workspace_size(desc), dev, "decode")
         _check(load().sinkattn_decode_int8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_scales), _ptr(block_table),
                                            _ptr(seq_lens), _ptr(sinks), scale, _ptr(out), _ptr(lse),
                                            ctypes.byref(desc), _ptr(ws), ws.numel(), _stream(dev)),

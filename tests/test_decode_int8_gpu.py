@@ -43,7 +43,7 @@ def _ref(w, window=0):
 def test_shapes(sa, cuda_dev, D, G, sinks):
     lens = [0, 1, 15, 16, 17, 33, 300, 1000, 2049]
     w = inputs.make_decode(lens, len(lens), 2 * G, 2, D, seed=G * 7 + D, sinks=sinks, kv_dtype="int8")
-    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_dev)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=cuda_dev)
     out, lse = sa.decode_int8(*_dev(w, cuda_dev), workspace_buf=ws)
     check(out, lse, _ref(w))
     assert sa.get_status(ws) == 0
@@ -140,7 +140,7 @@ def test_bad_pages_and_lengths_set_the_status(sa, cuda_dev):
     w = inputs.make_decode([100, 40, 60], 3, 16, 2, 64, seed=8, kv_dtype="int8")
     ref = _ref(w)
     a = list(_dev(w, cuda_dev))
-    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_dev)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=cuda_dev)
     a[4] = a[4].clone()
     a[4][1, 1] = w.cache.num_pages
     a[5] = a[5].clone()
@@ -155,7 +155,7 @@ def test_bad_pages_and_lengths_set_the_status(sa, cuda_dev):
 
 def test_waits_that_run_out_report(sa, cuda_dev):
     w = inputs.make_decode([3000, 500], 2, 16, 2, 64, seed=9, kv_dtype="int8")
-    ws = torch.zeros(1 << 24, dtype=torch.uint8, device=cuda_dev)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device=cuda_dev)
     a = _dev(w, cuda_dev)
     flush = torch.empty(512 << 20, dtype=torch.uint8, device=cuda_dev)
     st = 0
@@ -217,5 +217,5 @@ def test_refusals(sa, cuda_dev):
             sa.decode_int8(q, bad.get("k", kp), bad.get("v", vp), bad.get("sc", sc), bt, ln, sk, scale)
     with pytest.raises(ValueError):
         sa.decode_int8(q, kp, vp, sc, bt, ln, sk, scale, out=torch.empty(2, 8, 64, dtype=torch.bfloat16, device=cuda_dev))
-    with pytest.raises(ValueError):
+    with pytest.raises(sa.SinkAttnError, match="workspace"):
         sa.decode_int8(q, kp, vp, sc, bt, ln, sk, scale, workspace_buf=torch.zeros(256, dtype=torch.uint8, device=cuda_dev))
