@@ -81,6 +81,16 @@ int encode_pages_map_fp8(CUtensorMap *m, const void *pages, int num_pages, int H
                                 : (D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B));
 }
 
+// The same pages for the INT8 decode: a (page, head)'s 16 D contiguous bytes as rows of 128, under
+// the 128-byte swizzle.
+int encode_pages_map_int8(CUtensorMap *m, const void *pages, int num_pages, int Hkv, int D) {
+    const int rows = kPageSize * D / 128;
+    const cuuint64_t dims[4] = {128, (cuuint64_t)rows, (cuuint64_t)Hkv, (cuuint64_t)(num_pages > 0 ? num_pages : 1)};
+    const cuuint64_t strides[3] = {128, (cuuint64_t)kPageSize * D, (cuuint64_t)Hkv * kPageSize * D};
+    const cuuint32_t box[4] = {128, (cuuint32_t)rows, 1, 1};
+    return encode_map(m, pages, 4, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
 // Pages [num_pages, Hkv, 16, D]: dims {D, 16, Hkv, num_pages}; a box is one
 // (page, head) row block of 16 tokens x 64 elements.
 int encode_pages_map(CUtensorMap *m, const void *pages, int num_pages, int Hkv, int D) {
@@ -185,8 +195,7 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
     return SINKATTN_OK;
 }
 
-// The INT8 decode's workspace: the same parts for its own grid (ctas8, smem8, total_warps8), with a
-// partial state for each chunk of its plan.
+// The INT8 decode's workspace: the same parts for its own grid (ctas8, smem8, total_warps8).
 int decode_int8_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
     int device = 0, sms = 0;
     int rc = cuda_rc(cudaGetDevice(&device), "cudaGetDevice");
@@ -201,8 +210,7 @@ int decode_int8_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
     if (sms > 0 && d->max_sms > 0 && d->max_sms < sms) L->ctas8 = L->ctas8 / sms * d->max_sms;
     L->total_warps8 = L->ctas8 * L->warps_per_cta8;
     L->ctas = L->smem = L->total_warps = L->warps_per_cta = 0;  // not this kernel's
-    const size_t slots = (size_t)L->total_warps8 * decode_int8_chunks_per_warp() + 1 +
-                         (size_t)d->num_seqs * d->num_kv_heads;
+    const size_t slots = (size_t)L->total_warps8 + (size_t)d->num_seqs * d->num_kv_heads;
     size_t off = kStatusBytes;
     L->prefix = off;
     off += align_up(((size_t)d->num_seqs + 1) * 4);
@@ -262,8 +270,6 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
     a.part_acc = reinterpret_cast<float *>(ws + P->layout.acc);
     a.k_scale = nullptr;
     a.v_scale = nullptr;
-    a.sched = nullptr;
-    a.min_chunk = 0;
     a.kv_scales = nullptr;
     a.k_new = nullptr;
     a.v_new = nullptr;
@@ -641,14 +647,12 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
     if (rc) return rc;
     if ((int64_t)desc->num_seqs * desc->num_qo_heads > (int64_t)INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;  // merge grid
     CUtensorMap kmap, vmap;
-    rc = encode_pages_map_fp8(&kmap, k_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
+    rc = encode_pages_map_int8(&kmap, k_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
     if (rc) return rc;
-    rc = encode_pages_map_fp8(&vmap, v_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
+    rc = encode_pages_map_int8(&vmap, v_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
     if (rc) return rc;
     P.args.kv_scales = kv_scales;
     P.args.total_warps = P.layout.total_warps8;
-    P.args.sched = static_cast<uint32_t *>(workspace) + 32;  // header bytes 128..131
-    P.args.min_chunk = decode_int8_min_chunk(desc->head_dim, P.args.G);
     rc = cuda_rc(launch_decode_int8(desc->head_dim, P.args, kmap, vmap, P.layout.ctas8, P.layout.smem8,
                                     (cudaStream_t)stream),
                  "int8 split-KV decode launch");

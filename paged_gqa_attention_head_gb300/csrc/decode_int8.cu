@@ -24,12 +24,8 @@
 //   * q times a power of two per (sequence, KV head) that puts its largest entry at 2^14 is exact
 //     in f16 whatever its size; the scores take the power back;
 //   * no code is NaN or infinite: slots past a sequence's end need no clearing, P is 0 there.
-// The list of units is cut into chunks of equal length; a warp starts with the chunk of its number
-// and, where there are more chunks than warps, takes further ones from a counter in the workspace
-// header, so that the warps that HBM serves faster do more of the work (equal shares left a tenth
-// of the warps idle on average).  A chunk's partial state has the chunk's number, so no result
-// depends on who took it.  The warp's copy side runs ahead of its arithmetic, over chunk borders
-// too, and leaves what the arithmetic needs to know of a unit beside its pages.
+// A warp's copy side runs ahead of its arithmetic and leaves what that needs to know of a unit
+// beside its pages.
 // The running maximum moves only when a score passes it by more than 8 (log2): P is taken as
 // 2^(s - m + 7), at most 2^15, so a stale maximum costs no precision and the votes, the column
 // maxima and the rescale of O^T drop out of almost every unit.
@@ -50,10 +46,11 @@ template <int D, int NH>
 struct Int8Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
-    // Pages per work unit: 8 KB of K and V for one tile of heads, half of it where the second
-    // tile's accumulators leave few registers; 16 KB a warp in flight.
-    static constexpr int kPPU = (D == 64 ? 4 : 2);
-    static constexpr int kStages = 2;
+    // Pages per work unit: 8 KB of K and V (at head_dim 64 half of that for 16 heads, by registers).
+    // What a unit costs beside its pages' arithmetic is ~300 instructions: with two pages at head_dim
+    // 64 the batch of 1.26 GB ran 9 % longer.
+    static constexpr int kPPU = D == 64 && NH == 1 ? 4 : 2;
+    static constexpr int kStages = D == 64 && NH == 2 ? 4 : 2;
     static constexpr int kPageBytes = kPageSize * D;           // one (page, head) of K or of V codes
     static constexpr int kStageBytes = 2 * kPPU * kPageBytes;  // the unit's K pages, then V pages
     static constexpr int kWarpBytes = kStages * kStageBytes;
@@ -62,7 +59,6 @@ struct Int8Cfg {
     static constexpr int kKWords = D / 16;  // 32-bit words of K a lane reads per token row
 };
 
-constexpr int kChunks = 1;       // chunks per warp, at most
 constexpr float kPShift = 7.f;   // P = 2^(s - m + kPShift)
 constexpr float kMaxSlack = 8.f; // the running maximum moves when a score passes it by more
 
@@ -74,11 +70,19 @@ int int8_smem_bytes(int B) {
            (3 * B + 1) * 4;
 }
 
+// Byte offset of byte c of token t inside a page buffer.  A page's 16 x D contiguous bytes are
+// copied as rows of 128 bytes (at head_dim 64 a row is two tokens: half the rows and requests) under
+// the 128-byte swizzle, which keeps every shared load below free of bank conflicts.
+template <int D>
+__device__ __forceinline__ uint32_t page_off(int t, int c) {
+    const int at = t * D + c;
+    return sw128(at >> 7, (at >> 4) & 7) + (at & 15);
+}
+
 // What the arithmetic needs of a unit: whose it is, and of one of its pages.
 struct __align__(16) UnitMeta {
     int b, g;   // sequence, KV head
     int flags;  // kStart | kEnd | kWhole
-    int chunk;
 };
 constexpr int kStart = 1, kEnd = 2, kWhole = 4;  // first / last unit of a segment; the segment is all of (b, g)
 struct __align__(16) PageMeta {
@@ -134,15 +138,8 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
     scan_pages<U>(a, s_prefix, s_len, s_first);  // contains __syncthreads
 
     const int64_t T = (int64_t)a.Hkv * s_prefix[a.B];
-    // units of a chunk: an equal share of each warp, or of kChunks parts of it where the parts are
-    // still kMinChunk units (whose partial state then is a few percent of the bytes read)
     int64_t per = (T + a.total_warps - 1) / a.total_warps;
     if (per < kMinUnitsPerWarp) per = kMinUnitsPerWarp;
-    if (per >= 2 * a.min_chunk) {
-        const int64_t part = (T + (int64_t)a.total_warps * kChunks - 1) / ((int64_t)a.total_warps * kChunks);
-        per = part > a.min_chunk ? part : a.min_chunk;
-    }
-    const int n_chunks = (int)((T + per - 1) / per);
     if (blockIdx.x == 0) {
         for (int b = tid; b <= a.B; b += blockDim.x) a.ws_prefix[b] = s_prefix[b];
         if (tid == 0) {
@@ -150,40 +147,34 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
             a.ws_plan[1] = per;
         }
     }
-    int p_chunk = blockIdx.x * C::kWarps + wid;  // the copy side's chunk
-    if (p_chunk >= n_chunks) return;  // warp-uniform; no block-wide barrier follows
+    const int wglob = blockIdx.x * C::kWarps + wid;
+    const int64_t u_begin = (int64_t)wglob * per;
+    if (u_begin >= T) return;  // warp-uniform; no block-wide barrier follows
+    const int n_units = (int)min(per, T - u_begin);
 
     uint8_t *wbuf = smem + wid * C::kWarpBytes;
     uint64_t *wbar = bars + wid * S;
     UnitMeta *wunit = s_unit + wid * S;
     PageMeta *wmeta = s_meta + wid * S * U;
 
-    // The copy side: its position, the units left of its chunk, and the chunk after it (asked for
-    // when it began this one).
+    // The copy side's position, the first unit of its segment, and the units copied so far.
     Cursor pc;
-    int p_left = 0, p_seg0 = 0, produced = 0;
-    uint32_t p_next = 0;
-    auto begin_chunk = [&]() {
-        const int64_t u0 = (int64_t)p_chunk * per;
-        p_left = (int)min(per, T - u0);
+    {
         int lo = 0, hi = a.B - 1;
         while (lo < hi) {
             int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)a.Hkv * s_prefix[mid] <= u0)
+            if ((int64_t)a.Hkv * s_prefix[mid] <= u_begin)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         pc.b = lo;
         pc.pb = s_prefix[lo + 1] - s_prefix[lo];
-        const int local = (int)(u0 - (int64_t)a.Hkv * s_prefix[lo]);
+        const int local = (int)(u_begin - (int64_t)a.Hkv * s_prefix[lo]);
         pc.g = local / pc.pb;
         pc.p = local % pc.pb;
-        p_seg0 = pc.p;
-        p_next = (uint32_t)n_chunks;
-        if (n_chunks > a.total_warps && lane == 0) p_next = (uint32_t)a.total_warps + atomicAdd(a.sched, 1u);
-    };
-    begin_chunk();
+    }
+    int p_seg0 = pc.p, produced = 0;
 
     // Block-table window: lane l holds the entry of visible page win_p0 + l of sequence
     // win_b (-1 past its last page) and that page's scales for KV head win_g; the entries of
@@ -202,18 +193,12 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
     const uint64_t policy = l2_policy_evict_first();
     // The next unit, if there is one, into a stage: lanes 0 .. U - 1 take a page each.
     auto produce = [&](int stage) {
-        if (p_left == 0) {
-            const uint32_t next = __shfl_sync(0xffffffffu, p_next, 0);
-            if (next >= (uint32_t)n_chunks) return;
-            p_chunk = (int)next;
-            begin_chunk();
-        }
+        if (produced == n_units) return;
         const Cursor c = pc;
-        --p_left;
         ++produced;
         int flags = 0;
         if (c.p == p_seg0) flags |= kStart;
-        if (c.p == c.pb - 1 || p_left == 0) flags |= kEnd;
+        if (c.p == c.pb - 1 || produced == n_units) flags |= kEnd;
         if (c.p == c.pb - 1 && p_seg0 == 0) flags |= kWhole;
         if (++pc.p == pc.pb) {
             pc.p = p_seg0 = 0;
@@ -264,7 +249,7 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
         __syncwarp();  // the pages' metadata before the arrival
         uint64_t *bar = &wbar[stage];
         if (lane == 0) {
-            wunit[stage] = UnitMeta{c.b, c.g, flags, p_chunk};
+            wunit[stage] = UnitMeta{c.b, c.g, flags};
             if (oks)
                 mbar_arrive_expect_tx(bar, __popc(oks) * 2 * C::kPageBytes);
             else
@@ -286,14 +271,14 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
     uint32_t koff[2][C::kKWords / 4];
 #pragma unroll
     for (int i = 0; i < C::kKWords / 4; ++i) {
-        koff[0][i] = swz<D>(gr, t4 * (D / 4) + 16 * i);
-        koff[1][i] = swz<D>(gr + 8, t4 * (D / 4) + 16 * i);
+        koff[0][i] = page_off<D>(gr, t4 * (D / 4) + 16 * i);
+        koff[1][i] = page_off<D>(gr + 8, t4 * (D / 4) + 16 * i);
     }
     // V: the lane's row address of the transposing loads, 16 bytes of a token each: matrices 0 and 1
     // are tokens 0-7 and 8-15 of one 16-byte column block, 2 and 3 of the next
     uint32_t voff[D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) voff[i] = swz<D>(lane & 15, 16 * (2 * i + (lane >> 4)));
+    for (int i = 0; i < D / 32; ++i) voff[i] = page_off<D>(lane & 15, 16 * (2 * i + (lane >> 4)));
 
     uint32_t qf[C::kKSteps][NH][2];
     float acc[C::kMTiles][NH][4];
@@ -302,7 +287,7 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
     float f0 = 0.f;                   // score factor but for the page's scale and 2^24
     float v_top = 0.f, v_inv = 0.f;   // 2^E and 2^-E
 
-    for (int u = 0; u < produced; ++u) {
+    for (int u = 0; u < n_units; ++u) {
         const int stage = u % S;
         if (!__all_sync(0xffffffffu, mbar_wait_sleep(&wbar[stage], (uint32_t)((u / S) & 1), a.wait_limit_ns))) {
             // give up (all lanes together: the outcome is voted): record it, let the copies
@@ -419,22 +404,14 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
             for (int i = 0; i < D / 32; ++i)
                 ldsm_x4_t(base + voff[i], v[2 * i][0], v[2 * i][1], v[2 * i + 1][0], v[2 * i + 1][1]);
         };
-        // the stage back to the copy engine
-        auto hand_back = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            produce(stage);
-        };
-        // One tile of heads: the unit's V goes into registers and the stage back at once, so that the
-        // next copy overlaps the rest of this unit's arithmetic.  Two tiles: their accumulators leave
-        // no room for that at three CTAs an SM, and the third CTA is worth more.
-        constexpr bool kLateV = NH == 2;
-        uint32_t vw[kLateV ? 1 : U][C::kMTiles][2];
-        if (!kLateV) {
+        // The unit's V goes into registers and the stage back at once, so that the next copy overlaps
+        // the rest of this unit's arithmetic.
+        uint32_t vw[U][C::kMTiles][2];
 #pragma unroll
-            for (int j = 0; j < U; ++j) load_v(j, vw[kLateV ? 0 : j]);
-            hand_back();
-        }
+        for (int j = 0; j < U; ++j) load_v(j, vw[j]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        produce(stage);
 
         // scores, hidden keys at -inf (every page but a sequence's last, and a window's first, is whole)
         bool raise = false;
@@ -541,24 +518,20 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            uint32_t(&v)[C::kMTiles][2] = vw[kLateV ? 0 : j];
-            if (kLateV) load_v(j, v);
             // rows 0-7 of m-tile mt are head_dim 16mt + 2gr, rows 8-15 the odd ones beside them
 #pragma unroll
             for (int mt = 0; mt < C::kMTiles; ++mt) {
-                const uint32_t a0 = sub_even(v[mt][0]), a1 = sub_odd(v[mt][0]);
-                const uint32_t a2 = sub_even(v[mt][1]), a3 = sub_odd(v[mt][1]);
+                const uint32_t a0 = sub_even(vw[j][mt][0]), a1 = sub_odd(vw[j][mt][0]);
+                const uint32_t a2 = sub_even(vw[j][mt][1]), a3 = sub_odd(vw[j][mt][1]);
 #pragma unroll
                 for (int nt = 0; nt < NH; ++nt)
                     mma_f16_16816(acc[mt][nt], a0, a1, a2, a3, pb[j][nt][0], pb[j][nt][1]);
             }
         }
 
-        if (kLateV) hand_back();
-
         if (cur.flags & kEnd) {
             const bool whole = cur.flags & kWhole;
-            const int64_t slot = (int64_t)cur.chunk + (int64_t)cur.b * a.Hkv + cur.g;
+            const int64_t slot = (int64_t)wglob + (int64_t)cur.b * a.Hkv + cur.g;
 #pragma unroll
             for (int nt = 0; nt < NH; ++nt)
 #pragma unroll
@@ -611,7 +584,6 @@ __global__ void __launch_bounds__(128) merge_int8_kernel(const DecodeArgs a) {
     __shared__ float4 s_o[kParts][kQuads];
     __shared__ float2 s_ml[kParts];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0;  // for the next call on this workspace
     const int b = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, g = h / a.G, r = h % a.G;
     const int d4 = threadIdx.x % kQuads, part = threadIdx.x / kQuads;
     const int p0 = a.ws_prefix[b], pb = a.ws_prefix[b + 1] - p0;
@@ -711,16 +683,6 @@ cudaError_t int8_shape_for(int B, int device, int *ctas, int *warps, int *smem) 
 }
 
 }  // namespace
-
-int decode_int8_chunks_per_warp() { return kChunks; }
-
-// A chunk's partial state is written and read once, 2 x 4 G D bytes beside the ~8 KB (4 KB with two
-// tiles of heads) of a unit: 3 % of the chunk's bytes at most.
-int decode_int8_min_chunk(int D, int G) {
-    const int unit = G > 8 ? 4096 : 8192;
-    const int n = (33 * 8 * G * D + unit - 1) / unit;
-    return n > 8 ? n : 8;  // and not so short that its start and end show
-}
 
 cudaError_t decode_int8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
                                      int *smem_bytes) {

@@ -38,8 +38,6 @@ struct DecodeArgs {
     float *part_acc;        // [slots, G, D] partial unnormalised outputs
     const float *k_scale;   // FP8 cache: [Hkv] per-KV-head scales, or nullptr (1)
     const float *v_scale;
-    uint32_t *sched;         // INT8 decode: chunk counter in the workspace header (zero between calls)
-    int min_chunk;           // INT8 decode: units of a chunk taken from the counter, at least
     const float *kv_scales;  // INT8 cache: [num_pages, Hkv, 2] scales (K, V); nullptr: not an INT8 cache
     const void *k_new;      // decode with append: bf16 [B, Hkv, D] new rows, or nullptr
     const void *v_new;
@@ -79,12 +77,8 @@ cudaError_t launch_decode_fp8(int D, const DecodeArgs &a, const CUtensorMap &kma
 
 // The same for the decode over an INT8 cache (a.kv_scales set); its own merge of the partial
 // states, launched so that it is in place when the split-KV kernel ends.
-// max_chunks: partial states of split (sequence, KV head)s the plan makes at most (plus one for
-// each (sequence, KV head)); min_chunk: DecodeArgs.
 cudaError_t decode_int8_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
                                      int *smem_bytes);
-int decode_int8_chunks_per_warp();
-int decode_int8_min_chunk(int D, int G);
 cudaError_t launch_decode_int8(int D, const DecodeArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                int ctas, int smem_bytes, cudaStream_t stream);
 cudaError_t launch_merge_int8(int D, const DecodeArgs &a, cudaStream_t stream);
