@@ -158,31 +158,6 @@ def workspace(nbytes: int, device: torch.device, tag: str = "default") -> torch.
     return ws
 
 
-_stream_workspaces: dict = {}
-_retired_workspaces: list = []  # replaced by larger ones; a captured graph may hold their addresses
-
-
-def _stream_workspace(nbytes: int, device: torch.device, tag: str) -> torch.Tensor:
-    """Default scratch of a call on the current stream: one buffer per (device, stream, tag), so
-    that calls on two streams never share one.  While the stream is captured the call gets a buffer
-    of its own in the graph's memory, whose header the graph clears at each replay; so no two
-    graphs, and no graph and an eager call, share one."""
-    stream = _stream(device)
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _check(load().sinkattn_workspace_init(_ptr(ws), ws.numel(), stream), "sinkattn_workspace_init")
-        return ws
-    key = (device, stream, tag)
-    ws = _stream_workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        if ws is not None:
-            _retired_workspaces.append(ws)
-            nbytes = max(nbytes, 2 * ws.numel())
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _stream_workspaces[key] = ws
-    return ws
-
-
 def paged_desc(num_seqs, num_qo_heads, num_kv_heads, head_dim, num_pages, max_pages_per_seq,
                page_size=PAGE_SIZE, window=0, max_sms=0, wait_limit_us=0, flags=0) -> PagedDesc:
     """window > 0: sliding window (each query sees the keys at its last `window`
@@ -586,42 +561,256 @@ def decode_noalloc(q, k_pages, v_pages, block_table, seq_lens, sinks=None, scale
     return out, lse
 
 
-# ---------------------------------------------------------------- shared checks
-def _status_buffer(device: torch.device) -> Optional[torch.Tensor]:
-    """The status word that calls without scratch share (bits are OR-ed in, so streams may share it):
-    workspace(256, device, "append"), read with get_status.  None while a capture runs before the
-    buffer exists: the calls then report nothing."""
-    if (device, "append") not in _workspaces and torch.cuda.is_current_stream_capturing():
-        return None
-    return workspace(256, device, "append")
+# ---------------------------------------------------------------- INT8 cache, queries and keys
+# The calls below run in steps of a few microseconds on the GPU, so what they cost on the host shows:
+# descriptors and sizes are kept by their values, and a tensor is checked in one expression, its
+# fault named only when there is one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _need_cuda(t: torch.Tensor, name: str) -> torch.device:
+def _fits(t, dtype: torch.dtype, index: int, ndim: int) -> bool:
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == index
+            and t.is_contiguous())
+
+
+def _need_cuda(t: torch.Tensor, name: str) -> int:
+    """The index of the tensor's CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
-    return t.device
+    return t.get_device()
 
 
-def _need_rows(t: torch.Tensor, name: str, device: torch.device) -> int:
+def _need_dense(t: torch.Tensor, name: str, dtype: torch.dtype, index: int, ndim: int) -> None:
+    if not _fits(t, dtype, index, ndim):
+        _need(t, name, dtype, torch.device("cuda", index), ndim)
+
+
+def _need_rows(t: torch.Tensor, name: str, index: int) -> tuple:
     """Checks bf16 rows [T, H, D], each row's [H, D] dense (a part of wider rows will do), and
-    returns the row stride in elements."""
+    returns T, H, D and the row stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {torch.bfloat16}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
     T, H, D = t.shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    row, head, elem = t.stride()
+    if (D > 1 and elem != 1) or (H > 1 and head != D):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return t.stride(0) if T > 1 else H * D
+    return T, H, D, row if T > 1 else H * D
 
 
-# ---------------------------------------------------------------- queries and keys
+_descs: dict = {}
+
+
+def _desc_ref(*key):
+    """A reference to the descriptor of these values (num_seqs, num_qo_heads, num_kv_heads, head_dim,
+    num_pages, max_pages_per_seq, window, max_sms, wait_limit_us); descriptors are only read."""
+    ref = _descs.get(key)
+    if ref is None:
+        if len(_descs) > 4096:
+            _descs.clear()
+        B, Hq, Hkv, D, pages, columns, window, max_sms, wait = key
+        ref = _descs[key] = ctypes.byref(paged_desc(B, Hq, Hkv, D, pages, columns, window=window, max_sms=max_sms,
+                                                    wait_limit_us=wait))
+    return ref
+
+
+def _call(index: int, what: str, *args) -> None:
+    """The library call on the device `index`."""
+    fn = getattr(load(), what)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc != OK:
+        raise SinkAttnError(rc, what)
+
+
+def _status_buffer(index: int) -> Optional[torch.Tensor]:
+    """The status word that calls without scratch share (bits are OR-ed in, so streams may share it):
+    workspace(256, device, "append"), read with get_status.  None while a capture runs before the
+    buffer exists: the calls then report nothing."""
+    device = torch.device("cuda", index)
+    ws = _workspaces.get((device, "append"))
+    if ws is None and not torch.cuda.is_current_stream_capturing():
+        ws = workspace(256, device, "append")
+    return ws
+
+
+_stream_workspaces: dict = {}
+_retired_workspaces: list = []  # replaced by larger ones; a captured graph may hold their addresses
+
+
+def _stream_workspace(nbytes: int, index: int, stream: int, tag: str) -> torch.Tensor:
+    """Default scratch of a call on the current stream: one buffer per (device, stream, tag), so
+    that calls on two streams never share one.  While the stream is captured the call gets a buffer
+    of its own in the graph's memory, whose header the graph clears at each replay; so no two
+    graphs, and no graph and an eager call, share one."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
+        _call(index, "sinkattn_workspace_init", ws.data_ptr(), ws.numel(), stream)
+        return ws
+    key = (index, stream, tag)
+    ws = _stream_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _retired_workspaces.append(ws)
+            nbytes = max(nbytes, 2 * ws.numel())
+        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
+        _stream_workspaces[key] = ws
+    return ws
+
+
+def _need_int8_cache(k_pages, v_pages, kv_scales, index: int) -> tuple:
+    _need_dense(k_pages, "k_pages", torch.int8, index, 4)
+    _need_dense(v_pages, "v_pages", torch.int8, index, 4)
+    _need_dense(kv_scales, "kv_scales", torch.float32, index, 3)
+    shape = k_pages.shape
+    if v_pages.shape != shape or shape[2] != PAGE_SIZE:
+        raise ValueError("k_pages / v_pages must both be [num_pages, Hkv, 16, D]")
+    if kv_scales.shape != (shape[0], shape[1], 2):
+        raise ValueError("kv_scales must be [num_pages, Hkv, 2] (of K and of V)")
+    return shape
+
+
+def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, kv_scales,
+                   workspace_buf=None):
+    """Quantise new bf16 K/V rows into an INT8 cache in place (sinkattn_append_kv_int8): k_pages /
+    v_pages int8 [num_pages, Hkv, 16, D], kv_scales float32 [num_pages, Hkv, 2], all three updated;
+    k, v [T, Hkv, D], each token's heads dense (parts of a fused projection's rows will do)."""
+    dev = _need_cuda(k, "k")
+    T, Hkv, D, ks = _need_rows(k, "k", dev)
+    Tv, Hv, Dv, vs = _need_rows(v, "v", dev)
+    _need_dense(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    _need_dense(block_table, "block_table", torch.int32, dev, 2)
+    _need_dense(start_pos, "start_pos", torch.int32, dev, 1)
+    pages, Hp, _, Dp = _need_int8_cache(k_pages, v_pages, kv_scales, dev)
+    if (Tv, Hv, Dv) != (T, Hkv, D) or (Hp, Dp) != (Hkv, D):
+        raise ValueError("k, v must be [T, Hkv, D] matching the pages")
+    n, columns = block_table.shape
+    if cu_seqlens.shape[0] != n + 1 or start_pos.shape[0] != n:
+        raise ValueError("block_table / start_pos rows must equal the sequences of cu_seqlens")
+    ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
+    _call(dev, "sinkattn_append_kv_int8", k.data_ptr(), ks, v.data_ptr(), vs, cu_seqlens.data_ptr(), T,
+          block_table.data_ptr(), start_pos.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
+          _desc_ref(n, Hkv, Hkv, D, pages, columns, 0, 0, 0), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel(), _raw_stream(dev))
+    return k_pages, v_pages, kv_scales
+
+
+def decode_int8_workspace_size(desc: PagedDesc) -> int:
+    """Bytes of workspace that decode_int8 needs for desc on the current device."""
+    c = _SZ()
+    _check(load().sinkattn_decode_int8_workspace_size(ctypes.byref(desc), ctypes.byref(c)),
+           "decode_int8_workspace_size")
+    return c.value
+
+
+_int8_sizes: dict = {}
+
+
+def _int8_size(index: int, ref, key) -> int:
+    n = _int8_sizes.get((index, key))
+    if n is None:
+        c = _SZ()
+        _call(index, "sinkattn_decode_int8_workspace_size", ref, ctypes.byref(c))
+        n = _int8_sizes[(index, key)] = c.value
+    return n
+
+
+def _attention_outputs(q, out, lse, return_lse, index):
+    """The out and lse of q [T, Hq, D], given or made."""
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need_dense(out, "out", torch.bfloat16, index, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need_dense(lse, "lse", torch.float32, index, 2)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must have one entry per row and head of q")
+    elif return_lse:
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    return out, lse
+
+
+def _need_sinks(sinks, heads: int, index: int) -> Optional[int]:
+    if sinks is None:
+        return None
+    _need_dense(sinks, "sinks", torch.float32, index, 1)
+    if sinks.shape[0] != heads:
+        raise ValueError("sinks must have one entry per query head")
+    return sinks.data_ptr()
+
+
+def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=None, scale=None, out=None,
+                lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0, wait_limit_us=0):
+    """Split-KV paged decode over an INT8 cache with a scale per page and KV head
+    (sinkattn_decode_int8).  Returns (out, lse)."""
+    dev = _need_cuda(q, "q")
+    _need_dense(q, "q", torch.bfloat16, dev, 3)
+    _need_dense(block_table, "block_table", torch.int32, dev, 2)
+    _need_dense(seq_lens, "seq_lens", torch.int32, dev, 1)
+    B, Hq, D = q.shape
+    pages, Hkv, _, Dp = _need_int8_cache(k_pages, v_pages, kv_scales, dev)
+    n, columns = block_table.shape
+    if Dp != D:
+        raise ValueError("k_pages / v_pages must be [num_pages, Hkv, 16, D] matching q")
+    if n != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table / seq_lens rows must equal the batch")
+    sk = _need_sinks(sinks, Hq, dev)
+    out, lse = _attention_outputs(q, out, lse, return_lse, dev)
+    key = (B, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
+    desc, stream, ws = _desc_ref(*key), _raw_stream(dev), workspace_buf
+    if ws is None:
+        ws = _stream_workspace(_int8_size(dev, desc, key), dev, stream, "decode")
+    _call(dev, "sinkattn_decode_int8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
+          block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else scale, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), stream)
+    return out, lse
+
+
+def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_table, prefix_lens, sinks=None,
+                 scale=None, out=None, lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0,
+                 wait_limit_us=0):
+    """Chunked prefill over an INT8 paged prefix with a scale per page and KV head
+    (sinkattn_prefill_int8); the new tokens' q, k, v bf16.  Returns (out, lse)."""
+    dev = _need_cuda(q, "q")
+    _need_dense(q, "q", torch.bfloat16, dev, 3)
+    _need_dense(k, "k", torch.bfloat16, dev, 3)
+    _need_dense(v, "v", torch.bfloat16, dev, 3)
+    _need_dense(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    _need_dense(prefix_block_table, "prefix_block_table", torch.int32, dev, 2)
+    _need_dense(prefix_lens, "prefix_lens", torch.int32, dev, 1)
+    T, Hq, D = q.shape
+    pages, Hkv, _, Dp = _need_int8_cache(k_pages, v_pages, kv_scales, dev)
+    n, columns = prefix_block_table.shape
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or Dp != D:
+        raise ValueError("k / v must be [T, Hkv, D] matching q and the pages")
+    if cu_seqlens.shape[0] != n + 1 or prefix_lens.shape[0] != n:
+        raise ValueError("prefix_block_table / prefix_lens rows must equal the requests of cu_seqlens")
+    sk = _need_sinks(sinks, Hq, dev)
+    out, lse = _attention_outputs(q, out, lse, return_lse, dev)
+    stream, ws = _raw_stream(dev), workspace_buf
+    if ws is None:
+        ws = _stream_workspace(256, dev, stream, "prefill")
+    _call(dev, "sinkattn_prefill_int8", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
+          k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), prefix_block_table.data_ptr(),
+          prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else scale, out.data_ptr(),
+          None if lse is None else lse.data_ptr(),
+          _desc_ref(n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us), ws.data_ptr(), ws.numel(), stream)
+    return out, lse
+
+
 ROTARY_SCALING = {"none": 0, "linear": 1, "yarn": 2, "wavelength": 3}
 
 
@@ -637,6 +826,24 @@ def rotary_desc(base: float, rotary_dim: int, factor: float = 1.0, scaling: str 
                       ROTARY_SCALING[scaling], int(rotary_dim), int(bool(interleaved)))
 
 
+def _need_weight(w, name: str, D: int, index: int) -> Optional[int]:
+    if w is None:
+        return None
+    _need_dense(w, name, torch.float32, index, 1)
+    if w.shape[0] != D:
+        raise ValueError(f"{name} must have head_dim entries")
+    return w.data_ptr()
+
+
+def _rows_output(x, o, name: str, index: int):
+    if o is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    _need_dense(o, name, torch.bfloat16, index, 3)
+    if o.shape != x.shape:
+        raise ValueError(f"{name} must have its input's shape")
+    return o
+
+
 def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_weight=None, k_weight=None,
                  eps: float = 1e-6, q_out=None, k_out=None, workspace_buf=None):
     """Per-head RMS norm and rotary embedding of a step's queries and keys in one pass
@@ -645,184 +852,28 @@ def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_we
     rows are left as they were); q_weight / k_weight float32 [D] or None (no norm); rotary None: no
     rotation.  q_out / k_out dense, or q / k themselves if dense.  Returns (q_out, k_out)."""
     dev = _need_cuda(q, "q")
-    qs = _need_rows(q, "q", dev)
-    T, Hq, D = q.shape
+    T, Hq, D, qs = _need_rows(q, "q", dev)
     ks, Hkv = 0, Hq
     if k is not None:
-        ks, Hkv = _need_rows(k, "k", dev), k.shape[1]
-        if tuple(k.shape) != (T, Hkv, D):
+        Tk, Hkv, Dk, ks = _need_rows(k, "k", dev)
+        if (Tk, Dk) != (T, D):
             raise ValueError("k must be [T, Hkv, D] matching q")
+    elif k_out is not None:
+        raise ValueError("k_out given without its input")
+    pos = rot = None
     if rotary is not None:
         if not isinstance(rotary, RotaryDesc):
             raise TypeError("rotary must be a RotaryDesc (see rotary_desc)")
-        _need(positions, "positions", torch.int32, dev, 1)
+        _need_dense(positions, "positions", torch.int32, dev, 1)
         if positions.shape[0] != T:
             raise ValueError("positions must have one entry per token")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _need(w, name, torch.float32, dev, 1)
-            if w.shape[0] != D:
-                raise ValueError(f"{name} must have head_dim entries")
-    outs = []
-    for name, x, o in (("q_out", q, q_out), ("k_out", k, k_out)):
-        if x is None:
-            if o is not None:
-                raise ValueError(f"{name} given without its input")
-        elif o is None:
-            o = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _need(o, name, torch.bfloat16, dev, 3)
-            if tuple(o.shape) != tuple(x.shape):
-                raise ValueError(f"{name} must have its input's shape")
-        outs.append(o)
-    desc = paged_desc(0, Hq, Hkv, D, 0, 0)
-    with torch.cuda.device(dev):
-        ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
-        _check(load().sinkattn_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                            _ptr(positions) if rotary is not None else None, T,
-                                            None if rotary is None else ctypes.byref(rotary), _ptr(outs[0]),
-                                            _ptr(outs[1]), ctypes.byref(desc), _ptr(ws), 0 if ws is None else ws.numel(),
-                                            _stream(dev)),
-               "sinkattn_qk_norm_rope")
-    return outs[0], outs[1]
-
-
-# ---------------------------------------------------------------- INT8 cache
-def _need_int8_cache(k_pages, v_pages, kv_scales, device):
-    _need(k_pages, "k_pages", torch.int8, device, 4)
-    _need(v_pages, "v_pages", torch.int8, device, 4)
-    _need(kv_scales, "kv_scales", torch.float32, device, 3)
-    if v_pages.shape != k_pages.shape or k_pages.shape[2] != PAGE_SIZE:
-        raise ValueError("k_pages / v_pages must both be [num_pages, Hkv, 16, D]")
-    if tuple(kv_scales.shape) != (k_pages.shape[0], k_pages.shape[1], 2):
-        raise ValueError("kv_scales must be [num_pages, Hkv, 2] (of K and of V)")
-
-
-def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, kv_scales,
-                   workspace_buf=None):
-    """Quantise new bf16 K/V rows into an INT8 cache in place (sinkattn_append_kv_int8): k_pages /
-    v_pages int8 [num_pages, Hkv, 16, D], kv_scales float32 [num_pages, Hkv, 2], all three updated;
-    k, v [T, Hkv, D], each token's heads dense (parts of a fused projection's rows will do)."""
-    dev = _need_cuda(k, "k")
-    ks, vs = _need_rows(k, "k", dev), _need_rows(v, "v", dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
-    _need(block_table, "block_table", torch.int32, dev, 2)
-    _need(start_pos, "start_pos", torch.int32, dev, 1)
-    _need_int8_cache(k_pages, v_pages, kv_scales, dev)
-    T, Hkv, D = k.shape
-    n = cu_seqlens.shape[0] - 1
-    if tuple(v.shape) != (T, Hkv, D) or (k_pages.shape[1], k_pages.shape[3]) != (Hkv, D):
-        raise ValueError("k, v must be [T, Hkv, D] matching the pages")
-    if n < 0 or block_table.shape[0] != n or start_pos.shape[0] != n:
-        raise ValueError("block_table / start_pos rows must equal the sequences of cu_seqlens")
-    desc = paged_desc(n, Hkv, Hkv, D, k_pages.shape[0], block_table.shape[1])
-    with torch.cuda.device(dev):
-        ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
-        _check(load().sinkattn_append_kv_int8(_ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), T, _ptr(block_table),
-                                              _ptr(start_pos), _ptr(k_pages), _ptr(v_pages), _ptr(kv_scales),
-                                              ctypes.byref(desc), _ptr(ws), 0 if ws is None else ws.numel(),
-                                              _stream(dev)),
-               "sinkattn_append_kv_int8")
-    return k_pages, v_pages, kv_scales
-
-
-def decode_int8_workspace_size(desc: PagedDesc) -> int:
-    """Bytes of workspace that decode_int8 needs for desc on the current device."""
-    c = _SZ()
-    _check(load().sinkattn_decode_int8_workspace_size(ctypes.byref(desc), ctypes.byref(c)),
-           "decode_int8_workspace_size")
-    return c.value
-
-
-def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=None, scale=None, out=None,
-                lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0, wait_limit_us=0):
-    """Split-KV paged decode over an INT8 cache with a scale per page and KV head
-    (sinkattn_decode_int8).  Returns (out, lse)."""
-    dev = _need_cuda(q, "q")
-    _need(q, "q", torch.bfloat16, dev, 3)
-    _need(block_table, "block_table", torch.int32, dev, 2)
-    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
-    _need_int8_cache(k_pages, v_pages, kv_scales, dev)
-    B, Hq, D = q.shape
-    num_pages, Hkv, _, D2 = k_pages.shape
-    if D2 != D:
-        raise ValueError("k_pages / v_pages must be [num_pages, Hkv, 16, D] matching q")
-    if block_table.shape[0] != B or seq_lens.shape[0] != B:
-        raise ValueError("block_table / seq_lens rows must equal the batch")
-    if sinks is not None:
-        _need(sinks, "sinks", torch.float32, dev, 1)
-        if sinks.shape[0] != Hq:
-            raise ValueError("sinks must have one entry per query head")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need(out, "out", torch.bfloat16, dev, 3)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev) if return_lse else None
-    else:
-        _need(lse, "lse", torch.float32, dev, 2)
-        if tuple(lse.shape) != (B, Hq):
-            raise ValueError("lse must be [B, Hq]")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        desc = paged_desc(B, Hq, Hkv, D, num_pages, block_table.shape[1], window=window, max_sms=max_sms,
-                          wait_limit_us=wait_limit_us)
-        ws = workspace_buf
-        if ws is None:
-            ws = _stream_workspace(decode_int8_workspace_size(desc), dev, "decode")
-        _check(load().sinkattn_decode_int8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kv_scales), _ptr(block_table),
-                                           _ptr(seq_lens), _ptr(sinks), scale, _ptr(out), _ptr(lse),
-                                           ctypes.byref(desc), _ptr(ws), ws.numel(), _stream(dev)),
-               "sinkattn_decode_int8")
-    return out, lse
-
-
-def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_table, prefix_lens, sinks=None,
-                 scale=None, out=None, lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0,
-                 wait_limit_us=0):
-    """Chunked prefill over an INT8 paged prefix with a scale per page and KV head
-    (sinkattn_prefill_int8); the new tokens' q, k, v bf16.  Returns (out, lse)."""
-    dev = _need_cuda(q, "q")
-    _need(q, "q", torch.bfloat16, dev, 3)
-    _need(k, "k", torch.bfloat16, dev, 3)
-    _need(v, "v", torch.bfloat16, dev, 3)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
-    _need(prefix_block_table, "prefix_block_table", torch.int32, dev, 2)
-    _need(prefix_lens, "prefix_lens", torch.int32, dev, 1)
-    _need_int8_cache(k_pages, v_pages, kv_scales, dev)
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    n = cu_seqlens.shape[0] - 1
-    if tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D) or (k_pages.shape[1], k_pages.shape[3]) != (Hkv, D):
-        raise ValueError("k / v must be [T, Hkv, D] matching q and the pages")
-    if n < 0 or prefix_block_table.shape[0] != n or prefix_lens.shape[0] != n:
-        raise ValueError("prefix_block_table / prefix_lens rows must equal the requests of cu_seqlens")
-    if sinks is not None:
-        _need(sinks, "sinks", torch.float32, dev, 1)
-        if sinks.shape[0] != Hq:
-            raise ValueError("sinks must have one entry per query head")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _need(out, "out", torch.bfloat16, dev, 3)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-    if lse is None and return_lse:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=dev)
-    elif lse is not None:
-        _need(lse, "lse", torch.float32, dev, 2)
-        if tuple(lse.shape) != (T, Hq):
-            raise ValueError("lse must be [T, Hq]")
-    desc = paged_desc(n, Hq, Hkv, D, k_pages.shape[0], prefix_block_table.shape[1], window=window, max_sms=max_sms,
-                      wait_limit_us=wait_limit_us)
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        ws = workspace_buf if workspace_buf is not None else _stream_workspace(256, dev, "prefill")
-        _check(load().sinkattn_prefill_int8(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), T, _ptr(k_pages),
-                                            _ptr(v_pages), _ptr(kv_scales), _ptr(prefix_block_table),
-                                            _ptr(prefix_lens), _ptr(sinks), scale, _ptr(out), _ptr(lse),
-                                            ctypes.byref(desc), _ptr(ws), ws.numel(), _stream(dev)),
-               "sinkattn_prefill_int8")
-    return out, lse
+        pos, rot = positions.data_ptr(), ctypes.byref(rotary)
+    wq, wk = _need_weight(q_weight, "q_weight", D, dev), _need_weight(k_weight, "k_weight", D, dev)
+    q_out = _rows_output(q, q_out, "q_out", dev)
+    if k is not None:
+        k_out = _rows_output(k, k_out, "k_out", dev)
+    ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
+    _call(dev, "sinkattn_qk_norm_rope", q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, wq, wk, eps, pos, T,
+          rot, q_out.data_ptr(), None if k is None else k_out.data_ptr(), _desc_ref(0, Hq, Hkv, D, 0, 0, 0, 0, 0),
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(dev))
+    return q_out, k_out
