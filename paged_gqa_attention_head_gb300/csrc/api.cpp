@@ -205,7 +205,7 @@ int decode_int8_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
                                           &L->smem8),
                  "int8 decode launch shape");
     if (rc) return rc;
-    rc = cuda_rc(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device), "cudaDeviceGetAttribute");
+    rc = cuda_rc(current_sms(&sms), "SM count");
     if (rc) return rc;
     if (sms > 0 && d->max_sms > 0 && d->max_sms < sms) L->ctas8 = L->ctas8 / sms * d->max_sms;
     L->total_warps8 = L->ctas8 * L->warps_per_cta8;
@@ -325,7 +325,7 @@ bool overlap(const void *a, int64_t a_stride, int64_t a_len, const void *b, int6
 
 // The turn per position of each pair of a sinkattn_rotary_desc (its formulas in
 // include/sinkattn.h), in double on the host, as float pairs hi + lo.
-int rotary_table(const sinkattn_rotary_desc *r, int D, RotaryArgs *a) {
+int rotary_rates(const sinkattn_rotary_desc *r, int D, RotaryArgs *a) {
     if (!(r->base > 1.0) || !(r->base < INFINITY)) return SINKATTN_ERR_INVALID_ARG;
     if (r->rotary_dim <= 0 || r->rotary_dim > D || (r->interleaved != 0 && r->interleaved != 1))
         return SINKATTN_ERR_INVALID_ARG;
@@ -362,6 +362,26 @@ int rotary_table(const sinkattn_rotary_desc *r, int D, RotaryArgs *a) {
     a->rotary_dim = R;
     a->interleaved = r->interleaved;
     a->mscale = r->scaling == SINKATTN_ROTARY_YARN ? (float)(1.0 + 0.1 * log(r->factor)) : 1.f;
+    return SINKATTN_OK;
+}
+
+// The same, from the thread's last table where the parameters are equal: a model calls with one
+// set of them, and the powers cost more on the host than the launch's arguments.
+int rotary_table(const sinkattn_rotary_desc *r, int D, RotaryArgs *a) {
+    struct Last {
+        sinkattn_rotary_desc r;
+        RotaryArgs a;
+        int D = 0;  // 0: none yet
+    };
+    thread_local Last last;
+    if (last.D != D || memcmp(&last.r, r, sizeof *r) != 0) {
+        last.D = 0;
+        last.r = *r;
+        const int rc = rotary_rates(r, D, &last.a);
+        if (rc) return rc;
+        last.D = D;
+    }
+    *a = last.a;
     return SINKATTN_OK;
 }
 

@@ -220,10 +220,9 @@ __global__ void __launch_bounds__(32 * kI8Warps) append_int8_kernel(const Append
 
 cudaError_t launch_append_int8(int D, AppendInt8Args a, cudaStream_t stream) {
     if (a.T <= 0 || a.Hkv <= 0) return cudaSuccess;
-    int device = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&device);
+    int sms = 0;
+    const cudaError_t e = current_sms(&sms);
     if (e != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
     // a page's worth of tokens a warp once that still fills the GPU, else one token a warp
     a.group = (int64_t)a.T * a.Hkv > (int64_t)sms * 64 ? kPageSize : 1;
     const int64_t units = ((int64_t)a.T + a.group - 1) / a.group * a.Hkv;

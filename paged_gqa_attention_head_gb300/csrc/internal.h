@@ -11,6 +11,22 @@ namespace sinkattn {
 // produced it (per host thread).
 void record_cuda_error(cudaError_t e, const char *where);
 
+// SMs of the current device (asked of the runtime once per device).
+inline cudaError_t current_sms(int *sms) {
+    constexpr int kKnown = 64;
+    static int known[kKnown];  // 0: not asked yet; every writer writes the same value
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device >= 0 && device < kKnown) {
+        *sms = __atomic_load_n(&known[device], __ATOMIC_RELAXED);
+        if (*sms > 0) return cudaSuccess;
+    }
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess && device >= 0 && device < kKnown) __atomic_store_n(&known[device], *sms, __ATOMIC_RELAXED);
+    return e;
+}
+
 constexpr int kPageSize = 16;
 constexpr uint32_t kStatusBytes = 256;  // workspace header holding the status word
 

@@ -179,10 +179,9 @@ __global__ void __launch_bounds__(32 * kRotWarps) qk_norm_rope_kernel(const Rota
 
 template <int D>
 cudaError_t launch_rotary_d(RotaryArgs a, cudaStream_t stream) {
-    int device = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&device);
+    int sms = 0;
+    const cudaError_t e = current_sms(&sms);
     if (e != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess) return e;
     constexpr int kRows = 32 / (D / 8);
     const int passes = (a.q ? (a.Hq + kRows - 1) / kRows : 0) + (a.k ? (a.Hkv + kRows - 1) / kRows : 0);
     // one warp per token while there are enough tokens to fill the GPU; with fewer, a token's
