@@ -139,7 +139,11 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
 
     const int64_t T = (int64_t)a.Hkv * s_prefix[a.B];
     int64_t per = (T + a.total_warps - 1) / a.total_warps;
-    if (per < kMinUnitsPerWarp) per = kMinUnitsPerWarp;
+    // at least 2 units a warp (16 heads: 4, whose partial states are four times the bytes of a unit's
+    // share): one sequence of 4097 tokens took 10.5 us with 2, 12.6 with 4 and 11.3 with 1 at head_dim
+    // 64, and 16.3 with 2, 15.8 with 4 at head_dim 128 and 16 heads
+    constexpr int kMinUnits = NH == 1 ? 2 : 4;
+    if (per < kMinUnits) per = kMinUnits;
     if (blockIdx.x == 0) {
         for (int b = tid; b <= a.B; b += blockDim.x) a.ws_prefix[b] = s_prefix[b];
         if (tid == 0) {

@@ -78,13 +78,14 @@ constexpr int kItemRing = 16;
 // rest = m * 2^(e - e'), which joins the exponent of P as add = log2(rest) and leaves the row
 // sum by mul = 1 / rest; e' is e where -24 <= e <= 8 (127 * 2^8 < 2^15), else the nearest end.
 // Tiles of new tokens use the same fields: k the score scale, add and mul the V exponents.
+// k and add lie twice each, as the paired arithmetic takes them.
 struct PageScales {
-    float k[8];      // score factor: K scale * softmax scale * log2(e)
-    float add[8];    // V: what the exponent of P gains
+    float2 k[8];     // score factor: K scale * softmax scale * log2(e)
+    float2 add[8];   // V: what the exponent of P gains
     float mul[8];    // V: what a sum of such P is multiplied by
     uint32_t v2[8];  // V: 2^e' as a pair of fp16
 };
-constexpr int kPageScaleBytes = 128;
+constexpr int kPageScaleBytes = 192;
 static_assert(sizeof(PageScales) == kPageScaleBytes, "page scales");
 
 // QB: Q buffers.  Two at head_dim 64 with a sliding window, where items are one or two key
@@ -197,7 +198,8 @@ __device__ __forceinline__ uint32_t f16x2_pow2(uint32_t h, uint32_t p2) {
 }
 
 // Eight INT8 codes (two words) to one 16-byte vector: bf16 codes (kMode 3) or fp16 codes times
-// the power of two p2 (4), both exact.
+// the power of two p2 (4), both exact.  (Fewer instructions - bf16 from bit patterns, the power of
+// two in one FMA with the offset - left the times of both head sizes where they were.)
 template <int kMode>
 __device__ __forceinline__ uint4 int8x8(uint32_t w0, uint32_t w1, uint32_t p2) {
     w0 ^= 0x80808080u;
@@ -572,6 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ItemSlot *s_slot = reinterpret_cast<ItemSlot *>(smem + C::kOffSlot);  // the k-th item in slot k % kItemRing
     PageScales *s_page = reinterpret_cast<PageScales *>(smem + C::kOffPage);  // INT8: [NS]
     constexpr bool kCodes = kFp8 || kInt8;  // the prefix tiles are staged as one-byte codes
+    // INT8: the converters have more to do and are given more registers, at head_dim 64 the softmax's,
+    // whose rows are shorter there (8 chunks of 512 tokens over 16384-token prefixes 1639 -> 1549 us),
+    // at 128 the side warps' (7 ragged chunks 183 -> 175 us)
+    constexpr uint32_t kSideRegs = kInt8 && D == 128 ? 40 : kRegsSide;
+    constexpr uint32_t kConvertRegs = kInt8 ? (D == 64 ? 48 : 40) : kRegsConvert;
+    constexpr uint32_t kSoftmaxRegs = kInt8 && D == 64 ? 208 : kRegsSoftmax;
+    static_assert(128 * kSideRegs + 128 * kConvertRegs + 256 * kSoftmaxRegs <= kThreads * kRegsLaunch, "register split");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -622,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ================================================================ producer
-        reg_dealloc<kRegsSide>();
+        reg_dealloc<kSideRegs>();
         if (lane == 0) {
             tma_prefetch_desc(&qmap);
             tma_prefetch_desc(&kmap);
@@ -688,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = false;
                 break;
             }
+            int ahead = -1;
             for (int j = 0; j < gm.n_kv; ++j, ++kv) {
                 const int s = kv % NS, u = kv / NS;
                 const int tt = kWindow ? gm.t0 + j : j;  // key tile
@@ -699,12 +709,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int page = tt * 8 + lane;
                     nrow = min(kPageSize, max(0, gm.P - page * kPageSize));
                     if (nrow > 0) {
-                        pg = a.prefix_block_table[(int64_t)it.req * a.max_pages + page];
+                        pg = kInt8 && j > 0 ? ahead : a.prefix_block_table[(int64_t)it.req * a.max_pages + page];
                         if (pg < 0 || pg >= a.num_pages) {
                             set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
                             pg = -1;
                         }
                     }
+                    // INT8: the scales hang on the entry, so the next tile's entry is fetched a tile ahead
+                    if (kInt8 && page + 8 < (gm.P + kPageSize - 1) / kPageSize)
+                        ahead = a.prefix_block_table[(int64_t)it.req * a.max_pages + page + 8];
                     if (kInt8 && pg >= 0)
                         psc = __ldg(reinterpret_cast<const float2 *>(a.kv_scales) + (int64_t)pg * a.Hkv + gm.g);
                 }
@@ -726,14 +739,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // 2^e2 in fp16: a normal from 2^-14 up, a subnormal below
                             const uint32_t h = !(psc.y > 0.f) ? 0u : e2 >= -14 ? (uint32_t)(e2 + 15) << 10 : 1u << (e2 + 24);
                             // never 0, so that a hidden key's -inf stays one
-                            ps.k[lane] = fmaxf(a.scale_log2 * psc.x, 1e-37f);
-                            ps.add[lane] = log2f(rest);
+                            const float kf = fmaxf(a.scale_log2 * psc.x, 1e-37f), add = log2f(rest);
+                            ps.k[lane] = make_float2(kf, kf);
+                            ps.add[lane] = make_float2(add, add);
                             ps.mul[lane] = 1.f / rest;
                             ps.v2[lane] = h | h << 16;
                             // P * rest must stay in fp16: P <= 2^8, so rest < 2^7
                             if (!(psc.y < 32768.f)) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
                         } else {
-                            ps.k[lane] = a.scale_log2;  // add and mul come from the converters
+                            ps.k[lane] = make_float2(a.scale_log2, a.scale_log2);  // add and mul: the converters
                         }
                     }
                     __syncwarp();  // before lane 0 arrives on the stage's barriers
@@ -846,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1 || warp == 2) {
         // ================================================================ MMA issuers
-        reg_dealloc<kRegsSide>();
+        reg_dealloc<kSideRegs>();
         // Warp 1 issues the P.V products, warp 2 the S products; each runs its loop warp-
         // uniformly and one elected lane issues each MMA group.  S products are numbered
         // i = 0, 1, ... over the CTA's lifetime (key tile by key tile, query tile x = i %
@@ -946,10 +960,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         (void)ok;
     } else if (warp == 3) {
-        reg_dealloc<kRegsSide>();
+        reg_dealloc<kSideRegs>();
     } else if (warp >= 12) {
         // ================================================================ V converters
-        reg_dealloc<kRegsConvert>();
+        reg_dealloc<kConvertRegs>();
         // Keys 32q..32q+31 of the V tile, bf16 -> fp16 scaled by 2^-k, in place;
         // k = max(0, e - 14) where 2^e <= max|v| < 2^(e+1) over the quarter, so the
         // quarter stays below 2^15 and P * 2^k below 2^15 (k <= 7).  The quarter is
@@ -1068,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) s_vscale[st * 4 + q] = kexp;
                 if (kInt8 && lane < 2) {
-                    s_page[st].add[2 * q + lane] = (float)kexp;
+                    s_page[st].add[2 * q + lane] = make_float2((float)kexp, (float)kexp);
                     s_page[st].mul[2 * q + lane] = sc;
                 }
                 fence_proxy_async_smem();  // the P.V MMA reads these through the async proxy
@@ -1078,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ================================================================ softmax
-        reg_alloc<kRegsSoftmax>();
+        reg_alloc<kSoftmaxRegs>();
         const int x = (warp - 4) >> 2;  // query tile of this warpgroup
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // tile row of this thread
@@ -1167,10 +1181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float mx8[8];
                     float kf[8];
                     if (kInt8) {  // the eight chains are the tile's eight pages (scales are not negative)
-                        const float4 k0 = *reinterpret_cast<const float4 *>(s_page[(tcount - 1) % NS].k);
-                        const float4 k1 = *reinterpret_cast<const float4 *>(s_page[(tcount - 1) % NS].k + 4);
-                        kf[0] = k0.x, kf[1] = k0.y, kf[2] = k0.z, kf[3] = k0.w;
-                        kf[4] = k1.x, kf[5] = k1.y, kf[6] = k1.z, kf[7] = k1.w;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) kf[e] = s_page[(tcount - 1) % NS].k[e].x;
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -1227,12 +1239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float2 pk[2], pn[2], pmul = make_float2(0.f, 0.f);
                         if (kInt8) {
                             const PageScales &ps = s_page[vst];
-                            const float2 k2 = *reinterpret_cast<const float2 *>(ps.k + 2 * ch);
-                            const float2 a2 = *reinterpret_cast<const float2 *>(ps.add + 2 * ch);
+                            const float4 k2 = *reinterpret_cast<const float4 *>(ps.k + 2 * ch);
+                            const float4 a2 = *reinterpret_cast<const float4 *>(ps.add + 2 * ch);
                             pmul = *reinterpret_cast<const float2 *>(ps.mul + 2 * ch);
-                            pk[0] = make_float2(k2.x, k2.x), pk[1] = make_float2(k2.y, k2.y);
-                            pn[0] = make_float2(neg0 + a2.x, neg0 + a2.x);
-                            pn[1] = make_float2(neg0 + a2.y, neg0 + a2.y);
+                            pk[0] = make_float2(k2.x, k2.y), pk[1] = make_float2(k2.z, k2.w);
+                            pn[0] = fadd2(make_float2(neg0, neg0), make_float2(a2.x, a2.y));
+                            pn[1] = fadd2(make_float2(neg0, neg0), make_float2(a2.z, a2.w));
                         }
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {

@@ -739,7 +739,7 @@ def _attention_outputs(q, out, lse, return_lse, index):
         if lse.shape != q.shape[:2]:
             raise ValueError("lse must have one entry per row and head of q")
     elif return_lse:
-        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     return out, lse
 
 
