@@ -43,6 +43,7 @@
 // while the softmax works.  At head_dim 128 (O_A and O_B take 256 columns) P is written
 // over S in two S/P buffers, and S(i) waits for the P.V of product i - 2.
 #include <float.h>
+#include <limits.h>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -66,6 +67,8 @@ static_assert(128 * kRegsSide + 128 * kRegsConvert + 256 * kRegsSoftmax <= kThre
               "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kLocateMax = 1024;  // requests / levels of the shared-memory tile lookup
+constexpr int kSortMax = 256;     // requests that an INT8 prefill orders by their length
+static_assert(kSortMax <= kThreads, "one thread ranks one request");
 // Items reach the CTA's roles through a ring of slots.  Every role is within a few items of
 // the producer (it loads a K/V stage only after the P.V that last read it, which follows that
 // tile's S product, softmax and V conversion; a Q tile only after the last S product of the
@@ -108,7 +111,7 @@ struct PrefillCfg {
     static constexpr int kPBufs = 2;                 // P buffers (64 columns of fp16 pairs)
     static constexpr int kNumBars = 2 * kQBufs + 5 * kStages + 2 * kSBufs + 2 * kPBufs + 2 + 1 + kItemRing;
     static constexpr int kOffLoc = kOffBar + ((kNumBars * 8 + 127) / 128) * 128;
-    static constexpr int kOffMisc = kOffLoc + 4 * kLocateMax * 4;
+    static constexpr int kOffMisc = kOffLoc + (4 * kLocateMax + kSortMax) * 4;
     static constexpr int kOffSlot = kOffMisc + 256;  // [kItemRing] ItemSlot, 64 bytes each
     static constexpr int kOffPage = kOffSlot + kItemRing * 64;  // INT8 prefix: [kStages] PageScales
     static constexpr int kSmemBytes = 1024 + kOffPage + kStages * kPageScaleBytes;
@@ -270,7 +273,9 @@ __device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane,
 
 // Work list, in two parts.  (A) Requests with a paged prefix, request by request (each
 // request's query blocks from the last to the first, then by head pair): the items that
-// read one request's prefix run close together in time and share its pages in L2.
+// read one request's prefix run close together in time and share its pages in L2.  An INT8 prefill
+// takes the requests from the longest to the shortest (up to kSortMax of them), so that a batch of
+// unequal requests does not end with a long one's items (7 ragged chunks at head_dim 128 175 -> 129 us).
 // (B) Requests without a prefix: query blocks ordered by their index inside the request
 // (the number of causal key tiles they see), largest first, then by request, then by head
 // pair.  Without the causal mask every block of a request sees all of its key tiles: the
@@ -283,6 +288,7 @@ __device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane,
 // s_cum[lev] = part-B query blocks at levels above lev.
 struct WorkList {
     const int *nq, *cnt, *cum, *aend;
+    const int *order;  // part A's requests in the order they are taken; nullptr: as they come
     int n, levels, tiles, tiles_a, heads_per_item, groups;  // groups = items per query block
     bool fast;
 };
@@ -296,8 +302,9 @@ __device__ __forceinline__ bool has_prefix(const PrefillArgs &a, int i) {
     return a.prefix_lens != nullptr && a.prefix_lens[i] > 0;
 }
 
+template <bool kSorted>
 __device__ void worklist_setup(const PrefillArgs &a, int *s_nq, int *s_cnt, int *s_cum, int *s_aend,
-                               int *s_misc, WorkList *wl) {
+                               int *s_order, int *s_misc, WorkList *wl) {
     const int tid = threadIdx.x;
     const bool fast = a.n <= kLocateMax;
     if (tid == 0) s_misc[0] = 0;
@@ -316,6 +323,28 @@ __device__ void worklist_setup(const PrefillArgs &a, int *s_nq, int *s_cnt, int 
     __syncthreads();
     const int levels = s_misc[0];
     const bool fast_lv = fast && levels <= kLocateMax;
+    const bool sorted = kSorted && fast_lv && a.prefix_lens != nullptr && a.n <= kSortMax;
+    if (sorted) {
+        // rank of each request of part A by its tokens (equal ones as they come); the keys lie in
+        // s_cum until that is filled
+        for (int i = tid; i < a.n; i += blockDim.x)
+            s_cum[i] = has_prefix(a, i)
+                           ? min(a.prefix_lens[i], a.max_pages * kPageSize) + a.cu_seqlens[i + 1] - a.cu_seqlens[i]
+                           : INT_MIN;
+        __syncthreads();
+        int rank = 0, blocks = 0;
+        if (tid < a.n) {  // kSortMax <= the block's threads
+            const int key = s_cum[tid];
+            blocks = s_aend[tid];
+            for (int k = 0; k < a.n; ++k) rank += s_cum[k] > key || (s_cum[k] == key && k < tid);
+        }
+        __syncthreads();
+        if (tid < a.n) {
+            s_aend[rank] = blocks;  // 0 for the requests of part B, which come last
+            s_order[rank] = tid;
+        }
+        __syncthreads();
+    }
     if (fast && tid < 32) {
         // inclusive prefix sum of s_aend by warp 0: lane l sums a contiguous chunk, the
         // chunk totals are scanned across the warp, then each lane adds its offset
@@ -368,6 +397,7 @@ __device__ void worklist_setup(const PrefillArgs &a, int *s_nq, int *s_cnt, int 
     wl->cnt = s_cnt;
     wl->cum = s_cum;
     wl->aend = s_aend;
+    wl->order = sorted ? s_order : nullptr;
     wl->n = a.n;
     wl->levels = levels;
     wl->tiles = s_misc[1];
@@ -382,6 +412,7 @@ struct Item {
 };
 
 // Item of a given rank (any thread; reads the set-up tables).
+template <bool kSorted>
 __device__ Item item_of(const PrefillArgs &a, const WorkList &wl, int rank) {
     Item it;
     int tr = rank / wl.groups;
@@ -405,6 +436,7 @@ __device__ Item item_of(const PrefillArgs &a, const WorkList &wl, int rank) {
             i = lo;
             before = i > 0 ? wl.aend[i - 1] : 0;
             it.qb = wl.aend[i] - 1 - tr;  // blocks of request i: aend[i] - before
+            if (kSorted && wl.order) i = wl.order[i];
         } else {
             for (i = 0; i < a.n; ++i) {
                 const int q = has_prefix(a, i) ? query_blocks(a, i) : 0;
@@ -585,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     WorkList wl;
-    worklist_setup(a, s_loc, s_loc + kLocateMax, s_loc + 2 * kLocateMax, s_loc + 3 * kLocateMax, misc + 4,
-                   &wl);
+    worklist_setup<kInt8>(a, s_loc, s_loc + kLocateMax, s_loc + 2 * kLocateMax, s_loc + 3 * kLocateMax,
+                          s_loc + 4 * kLocateMax, misc + 4, &wl);
     const int n_items = wl.tiles * wl.groups;
     if ((int)blockIdx.x >= n_items) {  // CTA-uniform, before any allocation
         if (tid == 0) cta_done(a.sched);
@@ -650,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r = min((int)atomicAdd(a.sched, 1u), n_items);
                 sl.rank = r;
                 if (r < n_items) {
-                    sl.it = item_of(a, wl, r);
+                    sl.it = item_of<kInt8>(a, wl, r);
                     sl.gm = geom_of<kWindow, kCausal>(a, sl.it);
                     for (int x = 0; x < 2; ++x)
                         sl.sink2[x] = a.sinks && x < ntiles ? a.sinks[sl.it.h0 + x] * kLog2e : -INFINITY;

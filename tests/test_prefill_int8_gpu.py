@@ -73,6 +73,18 @@ def test_long_prefix_on_few_sms(sa, cuda_dev):
     assert none is None and torch.equal(out, got[0][0])
 
 
+@pytest.mark.parametrize("n", [1, 200, 256, 257, 1030])
+def test_many_requests(sa, cuda_dev, n):
+    """Requests in the order of their length (up to 256 of them) and as they come; equal ones, ones
+    without a prefix, empty ones."""
+    r = np.random.default_rng(n)
+    new, pre = r.integers(0, 4, n).tolist(), (r.integers(0, 40, n) * r.integers(0, 2, n)).tolist()
+    new[0], new[n // 2] = 200, 140
+    p = _make(new, pre, 2, 1, 64, seed=n)
+    out, lse = sa.prefill_int8(*_args(p, cuda_dev))
+    check(out, lse, _ref(p), 300)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_scales_of_every_size(sa, cuda_dev, D):
     """V scales from 2^-30 to 2^14 page by page, zero scales of K and V, K scales far below the rest."""
