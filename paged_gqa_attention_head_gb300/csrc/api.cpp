@@ -460,7 +460,7 @@ const char *sinkattn_error_string(int code) {
     }
 }
 
-int sinkattn_version(void) { return 10200; }
+int sinkattn_version(void) { return 10300; }
 
 int sinkattn_decode_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
     if (!bytes) return SINKATTN_ERR_INVALID_ARG;

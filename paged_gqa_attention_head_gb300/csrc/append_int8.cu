@@ -23,7 +23,7 @@
 namespace sinkattn {
 namespace {
 
-constexpr int kI8Warps = 8;
+constexpr int kI8Warps = 4;
 constexpr int kI8StageReqs = 1024;  // requests whose cu_seqlens / start_pos a block stages
 // Scales below this (values below ~1e-28) are taken as zero: their reciprocals stay finite.
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
@@ -183,8 +183,7 @@ __global__ void __launch_bounds__(32 * kI8Warps) append_int8_kernel(const Append
                 slot0 = (int)(pos % kPageSize);
                 ntok = min(kPageSize - slot0, (int)(c1 - t));
                 pg = a.block_table[(int64_t)lo * a.max_pages + pos / kPageSize];
-                leader = pg >= 0 && pg < a.num_pages;
-                if (!leader) bad = SINKATTN_STATUS_BAD_PAGE;
+                leader = true;
             }
         }
         if (bad && g == 0) set_status(a.status, bad);
@@ -193,7 +192,6 @@ __global__ void __launch_bounds__(32 * kI8Warps) append_int8_kernel(const Append
     for (; leaders; leaders &= leaders - 1) {
         const int src = __ffs(leaders) - 1;
         const int s0 = __shfl_sync(0xffffffffu, slot0, src), nt = __shfl_sync(0xffffffffu, ntok, src);
-        const int64_t page = __shfl_sync(0xffffffffu, pg, src);
         const __nv_bfloat16 *kr = reinterpret_cast<const __nv_bfloat16 *>(a.k) + (first + src) * a.k_stride + (int64_t)g * D;
         const __nv_bfloat16 *vr = reinterpret_cast<const __nv_bfloat16 *>(a.v) + (first + src) * a.v_stride + (int64_t)g * D;
         uint4 kx[N], vx[N];
@@ -205,6 +203,12 @@ __global__ void __launch_bounds__(32 * kI8Warps) append_int8_kernel(const Append
                 kx[e] = *reinterpret_cast<const uint4 *>(kr + row * a.k_stride + c * 8);
                 vx[e] = *reinterpret_cast<const uint4 *>(vr + row * a.v_stride + c * 8);
             }
+        }
+        // the rows are on their way before the page's entry is needed
+        const int64_t page = __shfl_sync(0xffffffffu, pg, src);
+        if (page < 0 || page >= a.num_pages) {  // warp-uniform
+            if (lane == 0 && g == 0) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+            continue;
         }
         float2 *sc = reinterpret_cast<float2 *>(a.kv_scales) + page * a.Hkv + g;
         const float2 old = s0 > 0 ? *sc : make_float2(0.f, 0.f);

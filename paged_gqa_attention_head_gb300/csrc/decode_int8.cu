@@ -116,8 +116,6 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
                        const DecodeArgs a) {
     using C = Int8Cfg<D, NH>;
     constexpr int S = C::kStages, U = C::kPPU;
-    // the merge may take its place on the SMs; it waits for this grid before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -575,6 +573,10 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
                 }
         }
     }
+    // Near the end of the grid the merge may take its place on the SMs; it waits for this grid before
+    // it reads.  (Not earlier: its waiting blocks would hold the threads of the SMs that max_sms
+    // keeps free for others.)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Log-sum-exp merge of the partial states of one (sequence, query head), the sink counted once.

@@ -774,7 +774,7 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
     if ws is None:
         ws = _stream_workspace(_int8_size(dev, desc, key), dev, stream, "decode")
     _call(dev, "sinkattn_decode_int8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
-          block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else scale, out.data_ptr(),
+          block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), stream)
     return out, lse
 
@@ -805,7 +805,7 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
         ws = _stream_workspace(256, dev, stream, "prefill")
     _call(dev, "sinkattn_prefill_int8", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
           k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), prefix_block_table.data_ptr(),
-          prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else scale, out.data_ptr(),
+          prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           None if lse is None else lse.data_ptr(),
           _desc_ref(n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us), ws.data_ptr(), ws.numel(), stream)
     return out, lse
@@ -873,7 +873,7 @@ def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_we
     if k is not None:
         k_out = _rows_output(k, k_out, "k_out", dev)
     ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
-    _call(dev, "sinkattn_qk_norm_rope", q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, wq, wk, eps, pos, T,
+    _call(dev, "sinkattn_qk_norm_rope", q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, wq, wk, float(eps), pos, T,
           rot, q_out.data_ptr(), None if k is None else k_out.data_ptr(), _desc_ref(0, Hq, Hkv, D, 0, 0, 0, 0, 0),
           None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(dev))
     return q_out, k_out

@@ -240,3 +240,19 @@ def test_a_serving_run(sa, cuda_dev, D, Hq, Hkv):
             held = torch.tensor(lens, dtype=torch.int32)
             out, lse = sa.decode_int8(q, *state, bt.to(dev), held.to(dev), sinks.to(dev), scale)
             check(out, lse, plain.attend_int8(q.cpu(), *ref, bt, held, sinks, scale), 100)
+
+
+def test_empty_calls(sa, cuda_dev):
+    """No tokens, no sequences: nothing is written, nothing is refused."""
+    kp = torch.ones(3, 2, 16, 64, dtype=torch.int8, device=cuda_dev)
+    vp, sc = kp.clone(), torch.ones(3, 2, 2, device=cuda_dev)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    rows = lambda t, h: torch.zeros(t, h, 64, dtype=torch.bfloat16, device=cuda_dev)  # noqa: E731
+    out, lse = sa.decode_int8(rows(0, 8), kp, vp, sc, i32(0, 4), i32(0))
+    assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
+    for n in (0, 2):
+        out, lse = sa.prefill_int8(rows(0, 8), rows(0, 2), rows(0, 2), i32(n + 1), kp, vp, sc, i32(n, 4), i32(n))
+        assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
+        sa.append_kv_int8(rows(0, 2), rows(0, 2), i32(n + 1), i32(n, 4), i32(n), kp, vp, sc)
+    torch.cuda.synchronize()
+    assert torch.all(kp == 1) and torch.all(vp == 1) and torch.all(sc == 1)
