@@ -565,13 +565,10 @@ def decode_noalloc(q, k_pages, v_pages, block_table, seq_lens, sinks=None, scale
 # The calls below run in steps of a few microseconds on the GPU, so what they cost on the host shows:
 # descriptors and sizes are kept by their values, and a tensor is checked in one expression, its
 # fault named only when there is one.
+_Tensor = torch.Tensor
+_functions: dict = {}  # the library's entry points by name
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _fits(t, dtype: torch.dtype, index: int, ndim: int) -> bool:
-    return (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == index
-            and t.is_contiguous())
 
 
 def _need_cuda(t: torch.Tensor, name: str) -> int:
@@ -584,7 +581,8 @@ def _need_cuda(t: torch.Tensor, name: str) -> int:
 
 
 def _need_dense(t: torch.Tensor, name: str, dtype: torch.dtype, index: int, ndim: int) -> None:
-    if not _fits(t, dtype, index, ndim):
+    if not (type(t) is _Tensor and t.dtype is dtype and t.dim() == ndim and t.get_device() == index
+            and t.is_contiguous()):
         _need(t, name, dtype, torch.device("cuda", index), ndim)
 
 
@@ -624,7 +622,9 @@ def _desc_ref(*key):
 
 def _call(index: int, what: str, *args) -> None:
     """The library call on the device `index`."""
-    fn = getattr(load(), what)
+    fn = _functions.get(what)
+    if fn is None:
+        fn = _functions[what] = getattr(load(), what)
     if torch.cuda.current_device() == index:
         rc = fn(*args)
     else:
