@@ -375,8 +375,17 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
  * prefix pointers, the scales and the prefix lengths are required; prefix lengths may be 0); the
  * new tokens' k, v stay bf16.  Prefix codes enter the products exactly, each page's scales join
  * the softmax in fp32; V scales of 2^15 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then
- * unspecified), and below 2^-24 the fp16 P loses bits.  Other arguments, workspace and errors as
- * for sinkattn_prefill. */
+ * unspecified), and below 2^-24 the fp16 P loses bits.  Other arguments and errors as for
+ * sinkattn_prefill.
+ * workspace:  at least sinkattn_prefill_workspace_size bytes, as there.  A call with few query
+ *             rows and a wide block table works faster with sinkattn_prefill_int8_workspace_size
+ *             bytes (for its descriptor and total_tokens): each query block's prefix is then
+ *             split over the SMs that would have no work, and a second kernel merges the parts
+ *             (results agree with the unsplit ones within rounding, and do not depend on
+ *             max_sms).  The answer is the header alone where a split would not pay. */
+int sinkattn_prefill_int8_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,
+                                         size_t *bytes);
+
 int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
                           int32_t total_tokens, const void *k_pages, const void *v_pages,
                           const float *kv_scales, const int32_t *prefix_block_table,

@@ -689,6 +689,29 @@ int sinkattn_prefill_workspace_size(const sinkattn_paged_desc *desc, size_t *byt
 }
 
 namespace {
+// Scratch of an INT8 prefill: the header, and where its items are split the parts' states.
+struct PrefillParts {
+    int splits;
+    size_t ml, o, total;
+};
+
+int prefill_int8_parts(const sinkattn_paged_desc *d, int32_t total_tokens, PrefillParts *p) {
+    int sms = 0;
+    const int rc = cuda_rc(current_sms(&sms), "SM count");
+    if (rc) return rc;
+    // (of all SMs, whatever max_sms leaves: the results do not depend on it)
+    p->splits = prefill_int8_splits(total_tokens, d->num_seqs, d->num_qo_heads, d->num_qo_heads / d->num_kv_heads,
+                                    d->max_pages_per_seq, d->window, sms);
+    p->ml = kStatusBytes;
+    p->o = p->total = kStatusBytes;
+    if (p->splits > 1) {
+        const size_t states = (size_t)total_tokens * d->num_qo_heads * p->splits;
+        p->o = align_up(p->ml + states * sizeof(float2));
+        p->total = align_up(p->o + states * d->head_dim * sizeof(float));
+    }
+    return SINKATTN_OK;
+}
+
 int prefill_common(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
                    int32_t total_tokens, const void *k_pages, const void *v_pages,
                    const int32_t *prefix_block_table, const int32_t *prefix_lens, const float *sinks,
@@ -764,8 +787,23 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.kv_scales = kv_scales;
+    a.splits = 1;
+    a.part_o = nullptr;
+    a.part_ml = nullptr;
+    if (kv_scales) {
+        PrefillParts parts;
+        if ((rc = prefill_int8_parts(desc, total_tokens, &parts))) return rc;
+        if (parts.splits > 1 && ws_bytes >= parts.total) {  // less scratch: the items are not split
+            a.splits = parts.splits;
+            a.launch_dependents = false;  // the next kernel is the merge: let in at the end alone, so that it takes no SM
+            a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + parts.ml);
+            a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + parts.o);
+        }
+    }
     cudaError_t e = launch_prefill(a, qmap, kmap, vmap, kpmap, vpmap, (cudaStream_t)stream);
     if (e == cudaErrorNotSupported) return SINKATTN_ERR_UNSUPPORTED;
+    if (e == cudaSuccess && a.splits > 1)
+        return cuda_rc(launch_prefill_merge(a, (cudaStream_t)stream), "prefill merge launch");
     return cuda_rc(e, "prefill launch");
 }
 }  // namespace
@@ -800,6 +838,17 @@ int sinkattn_prefill_fp8(const void *q, const void *k, const void *v, const int3
     return prefill_common(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, prefix_block_table,
                           prefix_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, true, k_scale,
                           v_scale, true, stream);
+}
+
+int sinkattn_prefill_int8_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens, size_t *bytes) {
+    if (!bytes || total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    PrefillParts p;
+    rc = prefill_int8_parts(desc, total_tokens, &p);
+    if (rc) return rc;
+    *bytes = p.total;
+    return SINKATTN_OK;
 }
 
 int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,

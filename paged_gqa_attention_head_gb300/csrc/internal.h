@@ -165,7 +165,13 @@ struct PrefillArgs {
     uint32_t *sched;                   // [2] in the workspace header: next item, CTAs done (zero between calls)
     const float *k_scale, *v_scale;    // FP8 prefix: [Hkv] per-KV-head scales, or nullptr (1)
     const float *kv_scales;            // INT8 prefix: [num_pages, Hkv, 2] scales (K, V); nullptr: not INT8
+    int splits;                        // INT8 prefix: parts an item's key tiles are split into (1: none)
+    float *part_o;                     // splits > 1: [T, Hq, splits, D] unnormalised outputs
+    float2 *part_ml;                   // splits > 1: [T, Hq, splits] running max (log2) and sum
 };
+// Parts that an INT8 prefill splits its items' key tiles into, from what the host knows.
+int prefill_int8_splits(int T, int n, int Hq, int G, int max_pages, int window, int sms);
+cudaError_t launch_prefill_merge(const PrefillArgs &a, cudaStream_t stream);
 // Tensor maps: q [T, Hq, D], k/v [T, Hkv, D] (new tokens), kp/vp prefix pages.
 cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &qmap, const CUtensorMap &kmap,
                            const CUtensorMap &vmap, const CUtensorMap &kpmap,

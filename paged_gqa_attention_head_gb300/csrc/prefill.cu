@@ -411,6 +411,12 @@ struct Item {
     int req, qb, h0;
 };
 
+// INT8 prefill with few items: an item's key tiles are cut into up to `splits` parts of this many tiles
+// (the last may have fewer), each an item of its own that leaves its rows' unnormalised outputs, maxima
+// and sums for the merge, the sink counted in the first.  An item of one tile stays whole.
+constexpr int kMaxSplits = 32;  // one lane of the merge holds one part's maximum and sum
+__device__ __forceinline__ int part_tiles(int n_kv, int splits) { return (n_kv + splits - 1) / splits; }
+
 // Item of a given rank (any thread; reads the set-up tables).
 template <bool kSorted>
 __device__ Item item_of(const PrefillArgs &a, const WorkList &wl, int rank) {
@@ -552,6 +558,7 @@ struct alignas(16) ItemSlot {
     ItemGeom gm;
     float sink2[2];     // per query tile: sink * log2(e), -inf without sinks
     float kscale, vscale;  // FP8 prefix: the KV head's scales (1 if not given)
+    int part;              // INT8 prefix: the part of a split item; -1: the item is whole
 };
 static_assert(sizeof(ItemSlot) == 64, "item slot");
 
@@ -606,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ItemSlot *s_slot = reinterpret_cast<ItemSlot *>(smem + C::kOffSlot);  // the k-th item in slot k % kItemRing
     PageScales *s_page = reinterpret_cast<PageScales *>(smem + C::kOffPage);  // INT8: [NS]
     constexpr bool kCodes = kFp8 || kInt8;  // the prefix tiles are staged as one-byte codes
+    constexpr bool kFrom = kWindow || kInt8;  // an item's key tiles may start behind the first
     // INT8: the converters have more to do and are given more registers, at head_dim 64 the softmax's,
     // whose rows are shorter there (8 chunks of 512 tokens over 16384-token prefixes 1639 -> 1549 us),
     // at 128 the side warps' (7 ragged chunks 183 -> 175 us)
@@ -619,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     WorkList wl;
     worklist_setup<kInt8>(a, s_loc, s_loc + kLocateMax, s_loc + 2 * kLocateMax, s_loc + 3 * kLocateMax,
                           s_loc + 4 * kLocateMax, misc + 4, &wl);
-    const int n_items = wl.tiles * wl.groups;
+    const int splits = kInt8 ? a.splits : 1;
+    const int n_items = wl.tiles * wl.groups * splits;
     if ((int)blockIdx.x >= n_items) {  // CTA-uniform, before any allocation
         if (tid == 0) cta_done(a.sched);
         return;
@@ -679,13 +688,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             int r = 0;
             if (lane == 0) {
                 ItemSlot &sl = s_slot[kk % kItemRing];
-                r = min((int)atomicAdd(a.sched, 1u), n_items);
+                bool empty;  // a part past the item's last one
+                do {
+                    empty = false;
+                    r = min((int)atomicAdd(a.sched, 1u), n_items);
+                    if (kInt8 && splits > 1 && r < n_items) {
+                        const ItemGeom gm = geom_of<kWindow, kCausal>(a, item_of<kInt8>(a, wl, r / splits));
+                        empty = r % splits * part_tiles(gm.n_kv, splits) >= gm.n_kv;
+                    }
+                } while (empty);
                 sl.rank = r;
                 if (r < n_items) {
-                    sl.it = item_of<kInt8>(a, wl, r);
+                    sl.it = item_of<kInt8>(a, wl, r / splits);
                     sl.gm = geom_of<kWindow, kCausal>(a, sl.it);
+                    sl.part = -1;  // whole
+                    const int per = part_tiles(sl.gm.n_kv, splits);
+                    if (kInt8 && splits > 1 && per < sl.gm.n_kv) {
+                        sl.part = r % splits;
+                        const int begin = sl.part * per;
+                        sl.gm.t0 += begin;
+                        sl.gm.n_kv = min(per, sl.gm.n_kv - begin);
+                    }
                     for (int x = 0; x < 2; ++x)
-                        sl.sink2[x] = a.sinks && x < ntiles ? a.sinks[sl.it.h0 + x] * kLog2e : -INFINITY;
+                        sl.sink2[x] = a.sinks && x < ntiles && sl.part <= 0 ? a.sinks[sl.it.h0 + x] * kLog2e : -INFINITY;
                     sl.kscale = kFp8 && a.k_scale ? a.k_scale[sl.gm.g] : 1.f;
                     sl.vscale = kFp8 && a.v_scale ? a.v_scale[sl.gm.g] : 1.f;
                 }
@@ -732,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int ahead = -1;
             for (int j = 0; j < gm.n_kv; ++j, ++kv) {
                 const int s = kv % NS, u = kv / NS;
-                const int tt = kWindow ? gm.t0 + j : j;  // key tile
+                const int tt = kFrom ? gm.t0 + j : j;  // key tile
                 // prefix tile: lane p < 8 looks up page 8tt + p (issued before the wait below so
                 // the load overlaps it); nrow = its valid rows, pg = -1 for a missing page
                 int nrow = 0, pg = -1;
@@ -1032,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float vmul8 = vsc * __uint_as_float((uint32_t)(127 - kexp8) << 23);
             for (int j = 0; j < gm.n_kv; ++j, ++kv) {
                 const int st = kv % NS;
-                const bool fp8_tile = kCodes && (kWindow ? gm.t0 + j : j) < gm.n_pre;
+                const bool fp8_tile = kCodes && (kFrom ? gm.t0 + j : j) < gm.n_pre;
                 if (kCodes) {
                     // K: the FP8 (INT8) prefix tiles to bf16 code values (the S products wait for this)
                     if (!__all_sync(0xffffffffu, wait_or_abort<true>(&bars.k_full[st], (uint32_t)((kv / NS) & 1),
@@ -1167,7 +1192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++tcount;
                 tc::fence_after_sync();
-                const int tt = kWindow ? gm.t0 + j : j;  // key tile
+                const int tt = kFrom ? gm.t0 + j : j;  // key tile
                 // keys lo .. ncols-1 of this tile are the row's to see
                 int ncols;
                 if (!kCausal)
@@ -1360,8 +1385,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc::fence_after_sync();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
             const bool valid = t < gm.L && gm.row0 >= 0 && gm.row0 + t < a.T;
+            const int part = kInt8 ? s_slot[k % kItemRing].part : -1;
+            if (kInt8 && part >= 0) {
+                // a part: the row's sums as they are, for the merge
+                const int64_t pr = ((int64_t)(gm.row0 + t) * a.Hq + h) * splits + part;
+                float *po = a.part_o + pr * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tc::ld_32x32b_x32(tO + c * 32, o);
+                    tc::wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint32_t w[8] = {o[e], o[e + 1], o[e + 2], o[e + 3], o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+                            st_global_v8(po + c * 32 + e, w);
+                        }
+                    }
+                }
+                if (valid) a.part_ml[pr] = make_float2(m_used, l);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.o_free[x]);
+                continue;
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             __nv_bfloat16 *og = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                 ((int64_t)(gm.row0 + t) * a.Hq + h) * D;
 #pragma unroll
@@ -1418,6 +1467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         tc::dealloc(tmem, kTmemCols);
     }
+    if (kInt8 && splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge
     if (tid == 0) cta_done(a.sched);
 }
 
@@ -1439,7 +1489,103 @@ cudaError_t launch_d(const PrefillArgs &a, const CUtensorMap &qmap, const CUtens
     return cudaGetLastError();
 }
 
+// Merge of the parts of each (token, query head) of a split prefill: a warp each, lane s holding part
+// s's maximum and sum, the outputs read part by part:
+//     M = max m_s;  out = sum O_s 2^(m_s - M) / sum l_s 2^(m_s - M);  lse = M + log2 of that sum.
+template <int D, bool kWindow>
+__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillArgs a) {
+    constexpr int kPer = D / 32;  // outputs of a lane
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t idx = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (idx >= (int64_t)a.T * a.Hq) return;
+    const int row = (int)(idx / a.Hq);
+    int lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.cu_seqlens[mid] <= row)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int row0 = a.cu_seqlens[lo];
+    if (row < row0 || row >= a.cu_seqlens[lo + 1]) return;  // behind the last request: left as it was
+    const ItemGeom gm = geom_of<kWindow, true>(a, Item{lo, (row - row0) / kBM, 0});
+    const int per = part_tiles(gm.n_kv, a.splits), parts = (gm.n_kv + per - 1) / per;
+    if (parts <= 1) return;  // whole: its output is there
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < parts) ml = a.part_ml[idx * a.splits + lane];
+    float M = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    float den = ml.y * w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    float acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    const float *po = a.part_o + idx * a.splits * D + lane * kPer;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        float v[kPer];
+        if (kPer == 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(po + (int64_t)s * D);
+            v[0] = x.x, v[1] = x.y;
+        } else {
+            const float4 x = *reinterpret_cast<const float4 *>(po + (int64_t)s * D);
+            v[0] = x.x, v[1] = x.y, v[2 % kPer] = x.z, v[3 % kPer] = x.w;
+        }
+        if (ws == 0.f) continue;  // a part in which the row sees no key
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] = fmaf(v[i], ws, acc[i]);
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    uint32_t *og = reinterpret_cast<uint32_t *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + idx * D + lane * kPer);
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) og[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[idx] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+}
+
 }  // namespace
+
+// An item is (128-row query block, pair of heads of one KV head).  Where they leave half the SMs or more
+// without work each is split over as many SMs as there are for it: one 17-token chunk over prefixes of
+// 1003 / 4000 / 16384 tokens takes 20.5 / 30.5 / 70 us with 64/8 heads of 64 (4 parts; unsplit
+// 26 / 65 / 219) and 18.4 / 24 / 45 us with 16/8 heads of 128 (19 parts; 34 / 96 / 332).  More parts
+// than SMs cost up to a wave (6 parts for 32 items: 85 us of 70), and with more items the SMs are busy and the
+// parts' outputs are extra traffic (128 items: 4 parts 98 us, unsplit 71).  Up to 3 prefix tiles - of
+// the block table's width or the window, all that the host knows - the merge takes what the split
+// gains (250 tokens: 16.4 us, unsplit 15.9).
+int prefill_int8_splits(int T, int n, int Hq, int G, int max_pages, int window, int sms) {
+    const int64_t most = ((int64_t)T + (int64_t)n * (kBM - 1)) / kBM;  // blocks: no more than this, nor rows
+    const int64_t items = (most < T ? most : T) * (G >= 2 ? Hq / 2 : Hq);
+    int64_t tiles = (int64_t)max_pages * kPageSize / kBN;
+    if (window > 0 && tiles > window / kBN + 1) tiles = window / kBN + 1;
+    if (items <= 0 || tiles < 4 || 2 * items > sms) return 1;
+    int64_t splits = sms / items;
+    if (splits > tiles + 1) splits = tiles + 1;
+    return (int)(splits > kMaxSplits ? kMaxSplits : splits);
+}
+
+cudaError_t launch_prefill_merge(const PrefillArgs &a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.T * a.Hq + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool w = a.window > 0;
+    if (a.D == 64)
+        return w ? cudaLaunchKernelEx(&cfg, prefill_merge_kernel<64, true>, a)
+                 : cudaLaunchKernelEx(&cfg, prefill_merge_kernel<64, false>, a);
+    return w ? cudaLaunchKernelEx(&cfg, prefill_merge_kernel<128, true>, a)
+             : cudaLaunchKernelEx(&cfg, prefill_merge_kernel<128, false>, a);
+}
 
 cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &qmap, const CUtensorMap &kmap,
                            const CUtensorMap &vmap, const CUtensorMap &kpmap,

@@ -81,6 +81,7 @@ SIGNATURES = {
                                                _SZ, _P]),
     "sinkattn_decode_int8_workspace_size": (ctypes.c_int, [_DP, ctypes.POINTER(_SZ)]),
     "sinkattn_decode_int8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P]),
+    "sinkattn_prefill_int8_workspace_size": (ctypes.c_int, [_DP, _I32, ctypes.POINTER(_SZ)]),
     "sinkattn_prefill_int8": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP,
                                              _P, _SZ, _P]),
     "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
@@ -714,15 +715,26 @@ def decode_int8_workspace_size(desc: PagedDesc) -> int:
     return c.value
 
 
+def prefill_int8_workspace_size(desc: PagedDesc, total_tokens: int) -> int:
+    """Bytes of workspace with which prefill_int8 works fastest for desc on the current device (256
+    are enough for it to work)."""
+    c = _SZ()
+    _check(load().sinkattn_prefill_int8_workspace_size(ctypes.byref(desc), total_tokens, ctypes.byref(c)),
+           "prefill_int8_workspace_size")
+    return c.value
+
+
 _int8_sizes: dict = {}
 
 
-def _int8_size(index: int, ref, key) -> int:
-    n = _int8_sizes.get((index, key))
+def _int8_size(what: str, index: int, ref, key, *more) -> int:
+    n = _int8_sizes.get((what, index, key, *more))
     if n is None:
+        if len(_int8_sizes) > 4096:
+            _int8_sizes.clear()
         c = _SZ()
-        _call(index, "sinkattn_decode_int8_workspace_size", ref, ctypes.byref(c))
-        n = _int8_sizes[(index, key)] = c.value
+        _call(index, what, ref, *more, ctypes.byref(c))
+        n = _int8_sizes[(what, index, key, *more)] = c.value
     return n
 
 
@@ -772,7 +784,7 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
     key = (B, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
     desc, stream, ws = _desc_ref(*key), _raw_stream(dev), workspace_buf
     if ws is None:
-        ws = _stream_workspace(_int8_size(dev, desc, key), dev, stream, "decode")
+        ws = _stream_workspace(_int8_size("sinkattn_decode_int8_workspace_size", dev, desc, key), dev, stream, "decode")
     _call(dev, "sinkattn_decode_int8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
           block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), stream)
@@ -800,14 +812,15 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
         raise ValueError("prefix_block_table / prefix_lens rows must equal the requests of cu_seqlens")
     sk = _need_sinks(sinks, Hq, dev)
     out, lse = _attention_outputs(q, out, lse, return_lse, dev)
-    stream, ws = _raw_stream(dev), workspace_buf
+    key = (n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
+    desc, stream, ws = _desc_ref(*key), _raw_stream(dev), workspace_buf
     if ws is None:
-        ws = _stream_workspace(256, dev, stream, "prefill")
+        ws = _stream_workspace(_int8_size("sinkattn_prefill_int8_workspace_size", dev, desc, key, T), dev, stream,
+                               "prefill")
     _call(dev, "sinkattn_prefill_int8", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
           k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), prefix_block_table.data_ptr(),
           prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(),
-          _desc_ref(n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us), ws.data_ptr(), ws.numel(), stream)
+          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), stream)
     return out, lse
 
 

@@ -256,3 +256,118 @@ def test_empty_calls(sa, cuda_dev):
         sa.append_kv_int8(rows(0, 2), rows(0, 2), i32(n + 1), i32(n, 4), i32(n), kp, vp, sc)
     torch.cuda.synchronize()
     assert torch.all(kp == 1) and torch.all(vp == 1) and torch.all(sc == 1)
+
+
+# ------------------------------------------------------------ split query blocks
+
+def _parts_ws(sa, p, dev, window=0):
+    """A workspace that lets the call split its query blocks, and into how many parts it does."""
+    T, Hq, D = p.q.shape
+    c = p.prefix
+    desc = sa.paged_desc(len(p.cu_seqlens) - 1, Hq, p.k.shape[1], D, c.k_pages.shape[0], c.block_table.shape[1], window=window)
+    n = sa.prefill_int8_workspace_size(desc, T)
+    return torch.zeros(n, dtype=torch.uint8, device=dev), (n - 256) // (T * Hq * (D + 2) * 4) if T else 0
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 1), (128, 4, 2), (64, 3, 3), (128, 1, 1)])
+@pytest.mark.parametrize("new,pre", [([17], [1003]), ([1], [4096]), ([130], [2000]), ([128], [128 * 31]),
+                                     ([0, 3, 200, 0, 1], [70, 2500, 0, 9, 640])])
+@pytest.mark.parametrize("window", [0, 700])
+def test_split_blocks(sa, cuda_dev, D, Hq, Hkv, new, pre, window):
+    """Few rows over long prefixes, whole and in parts; requests with fewer tiles than parts."""
+    p = _make(new, pre, Hq, Hkv, D, seed=D + Hq, sinks=D == 64)
+    ref = _ref(p, window)
+    ws, parts = _parts_ws(sa, p, cuda_dev, window)
+    assert 2 <= parts <= 32
+    out, lse = sa.prefill_int8(*_args(p, cuda_dev), workspace_buf=ws, window=window)
+    check(out, lse, ref, 4300)
+    small = torch.zeros(ws.numel() - 256, dtype=torch.uint8, device=cuda_dev)  # too small for the parts: whole
+    whole, whole_lse = sa.prefill_int8(*_args(p, cuda_dev), workspace_buf=small, window=window)
+    check(whole, whole_lse, ref, 4300)
+    assert torch.all(small[256:] == 0)
+    # the default workspace splits too, whatever SMs the call may use
+    for kw in ({}, {"max_sms": 2}, {"return_lse": False}):
+        o, m = sa.prefill_int8(*_args(p, cuda_dev), window=window, **kw)
+        assert torch.equal(o, out) and (m is None or torch.equal(m, lse))
+    assert sa.get_status(ws) == 0 and sa.get_status(small) == 0
+
+
+def test_split_blocks_of_padded_steps_and_bad_pages(sa, cuda_dev):
+    """Rows behind the last request stay; a bad page in one part is reported and hurts its request alone;
+    a step in which a page's V scale is out of range is reported."""
+    p = _make([5, 9], [3000, 2000], 8, 1, 64, seed=31)
+    ref = _ref(p)
+    a = list(_args(p, cuda_dev))
+    ws, parts = _parts_ws(sa, p, cuda_dev)
+    assert parts > 2
+    pad = lambda x: torch.cat([x, x[:9]])  # noqa: E731
+    out = torch.full((23, 8, 64), 42.0, dtype=torch.bfloat16, device=cuda_dev)
+    lse = torch.full((23, 8), 42.0, device=cuda_dev)
+    big = torch.zeros(2 * ws.numel(), dtype=torch.uint8, device=cuda_dev)
+    sa.prefill_int8(pad(a[0]), pad(a[1]), pad(a[2]), *a[3:], out=out, lse=lse, workspace_buf=big)
+    check(out[:14], lse[:14], ref, 3100)
+    assert torch.all(out[14:] == 42.0) and torch.all(lse[14:] == 42.0)
+    a[7] = a[7].clone()
+    a[7][1, 100] = -7
+    out, lse = sa.prefill_int8(*a, workspace_buf=ws)
+    assert sa.get_status(ws) == sa.STATUS_BAD_PAGE
+    check(out[:5], lse[:5], tuple(x[:5] for x in ref), 3100)
+
+
+def test_split_blocks_whose_waits_run_out(sa, cuda_dev):
+    p = _make([17], [5000], 8, 1, 64, seed=32)
+    ws, parts = _parts_ws(sa, p, cuda_dev)
+    assert parts > 2
+    st = 0
+    for _ in range(20):
+        sa.prefill_int8(*_args(p, cuda_dev), workspace_buf=ws, wait_limit_us=1)
+        st |= sa.get_status(ws)
+        if st:
+            break
+    assert st == sa.STATUS_WAIT_TIMEOUT
+    out, lse = sa.prefill_int8(*_args(p, cuda_dev), workspace_buf=ws)
+    check(out, lse, _ref(p), 5100)
+    assert sa.get_status(ws) == 0
+
+
+def test_split_blocks_on_streams_and_in_graphs(sa, cuda_dev):
+    ps = [_make([17], [4000], 8, 1, 64, seed=33), _make([100, 3], [2500, 900], 4, 2, 128, seed=34)]
+    args = [_args(p, cuda_dev) for p in ps]
+    alone = [sa.prefill_int8(*a) for a in args]
+    torch.cuda.synchronize()
+    for p, got in zip(ps, alone):
+        check(*got, _ref(p), 4100)
+    streams, graphs, outs = [torch.cuda.Stream() for _ in args], [], []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(2):  # twice on the same stream: the second call's parts wait for the first's merge
+                o = sa.prefill_int8(*a)
+        graphs.append(g)
+        outs.append(o)
+    for use_graph in (False, True):
+        for _ in range(10):
+            got = []
+            torch.cuda.synchronize()
+            for s, g, a, o in zip(streams, graphs, args, outs):
+                with torch.cuda.stream(s):
+                    if use_graph:
+                        g.replay()
+                        got.append(o)
+                    else:
+                        got.append(sa.prefill_int8(*a))
+            torch.cuda.synchronize()
+            for (o, l), (q, m) in zip(got, alone):
+                assert torch.equal(o, q) and torch.equal(l, m)
+
+
+def test_which_calls_split(sa, cuda_dev):
+    """Those that leave half the SMs or more idle over a table of 4 tiles or more."""
+    size = lambda n, Hq, Hkv, D, cols, T, window=0: sa.prefill_int8_workspace_size(  # noqa: E731
+        sa.paged_desc(n, Hq, Hkv, D, 8, cols, window=window), T)
+    assert size(1, 64, 8, 64, 63, 17) > 256
+    assert size(1, 64, 8, 64, 24, 17) == 256  # a short prefix
+    assert size(1, 64, 8, 64, 63, 17, 128) == 256  # a short window
+    assert size(8, 64, 8, 64, 1024, 4096) == 256  # work for all SMs
+    assert size(0, 64, 8, 64, 1024, 0) == 256
+    assert size(1, 1, 1, 128, 100000, 1) < 1 << 20
