@@ -570,6 +570,8 @@ _Tensor = torch.Tensor
 _functions: dict = {}  # the library's entry points by name
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = torch.cuda.is_current_stream_capturing
 
 
 def _need_cuda(t: torch.Tensor, name: str) -> int:
@@ -626,12 +628,12 @@ def _call(index: int, what: str, *args) -> None:
     fn = _functions.get(what)
     if fn is None:
         fn = _functions[what] = getattr(load(), what)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args)
     else:
         with torch.cuda.device(index):
             rc = fn(*args)
-    if rc != OK:
+    if rc:
         raise SinkAttnError(rc, what)
 
 
@@ -639,13 +641,16 @@ def _status_buffer(index: int) -> Optional[torch.Tensor]:
     """The status word that calls without scratch share (bits are OR-ed in, so streams may share it):
     workspace(256, device, "append"), read with get_status.  None while a capture runs before the
     buffer exists: the calls then report nothing."""
-    device = torch.device("cuda", index)
-    ws = _workspaces.get((device, "append"))
-    if ws is None and not torch.cuda.is_current_stream_capturing():
-        ws = workspace(256, device, "append")
+    key = _append_keys.get(index)
+    if key is None:
+        key = _append_keys[index] = (torch.device("cuda", index), "append")
+    ws = _workspaces.get(key)
+    if ws is None and not _capturing():
+        ws = workspace(256, *key)
     return ws
 
 
+_append_keys: dict = {}
 _stream_workspaces: dict = {}
 _retired_workspaces: list = []  # replaced by larger ones; a captured graph may hold their addresses
 
@@ -655,7 +660,7 @@ def _stream_workspace(nbytes: int, index: int, stream: int, tag: str) -> torch.T
     that calls on two streams never share one.  While the stream is captured the call gets a buffer
     of its own in the graph's memory, whose header the graph clears at each replay; so no two
     graphs, and no graph and an eager call, share one."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         _call(index, "sinkattn_workspace_init", ws.data_ptr(), ws.numel(), stream)
         return ws
@@ -751,7 +756,7 @@ def _attention_outputs(q, out, lse, return_lse, index):
         if lse.shape != q.shape[:2]:
             raise ValueError("lse must have one entry per row and head of q")
     elif return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty((q.shape[0], q.shape[1]), dtype=torch.float32, device=q.device)
     return out, lse
 
 
@@ -850,7 +855,7 @@ def _need_weight(w, name: str, D: int, index: int) -> Optional[int]:
 
 def _rows_output(x, o, name: str, index: int):
     if o is None:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
+        return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=torch.contiguous_format)
     _need_dense(o, name, torch.bfloat16, index, 3)
     if o.shape != x.shape:
         raise ValueError(f"{name} must have its input's shape")
