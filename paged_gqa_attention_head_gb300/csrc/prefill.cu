@@ -200,16 +200,27 @@ __device__ __forceinline__ uint32_t f16x2_pow2(uint32_t h, uint32_t p2) {
     return r;
 }
 
+// Two INT8 codes (each under the byte 0x43) to a bf16 pair, exact: 128 + the low seven bits, less
+// 128 or, for a negative code, 256 (0x4300 and 0x4380).
+__device__ __forceinline__ uint32_t int8x2_to_bf16x2(uint32_t w) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w & 0xFF7FFF7Fu), "r"(w & 0xFF80FF80u));
+    return r;
+}
+
 // Eight INT8 codes (two words) to one 16-byte vector: bf16 codes (kMode 3) or fp16 codes times
-// the power of two p2 (4), both exact.  (Fewer instructions - bf16 from bit patterns, the power of
-// two in one FMA with the offset - left the times of both head sizes where they were.)
+// the power of two p2 (4), both exact.
 template <int kMode>
 __device__ __forceinline__ uint4 int8x8(uint32_t w0, uint32_t w1, uint32_t p2) {
+    if (kMode == 3)
+        return make_uint4(int8x2_to_bf16x2(__byte_perm(w0, 0x43434343u, 0x4140)),
+                          int8x2_to_bf16x2(__byte_perm(w0, 0x43434343u, 0x4342)),
+                          int8x2_to_bf16x2(__byte_perm(w1, 0x43434343u, 0x4140)),
+                          int8x2_to_bf16x2(__byte_perm(w1, 0x43434343u, 0x4342)));
     w0 ^= 0x80808080u;
     w1 ^= 0x80808080u;
     const uint32_t h0 = int8x2_lo_to_f16x2(w0), h1 = int8x2_hi_to_f16x2(w0);
     const uint32_t h2 = int8x2_lo_to_f16x2(w1), h3 = int8x2_hi_to_f16x2(w1);
-    if (kMode == 3) return make_uint4(f16x2_to_bf16x2(h0), f16x2_to_bf16x2(h1), f16x2_to_bf16x2(h2), f16x2_to_bf16x2(h3));
     return make_uint4(f16x2_pow2(h0, p2), f16x2_pow2(h1, p2), f16x2_pow2(h2, p2), f16x2_pow2(h3, p2));
 }
 
@@ -217,7 +228,6 @@ __device__ __forceinline__ uint4 int8x8(uint32_t w0, uint32_t w1, uint32_t p2) {
 // values times sc (1), or fp16 code values times the power of two p2 (2).
 template <int kMode>
 __device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, float sc, uint32_t p2) {
-    if (kMode >= 3) return int8x8<kMode>(w0, w1, p2);
     const uint32_t h0 = e4m3x2_lo_to_f16x2(w0), h1 = e4m3x2_hi_to_f16x2(w0);
     const uint32_t h2 = e4m3x2_lo_to_f16x2(w1), h3 = e4m3x2_hi_to_f16x2(w1);
     if (kMode == 0) return make_uint4(f16x2_to_bf16x2(h0), f16x2_to_bf16x2(h1), f16x2_to_bf16x2(h2), f16x2_to_bf16x2(h3));
@@ -225,20 +235,17 @@ __device__ __forceinline__ uint4 codes8(uint32_t w0, uint32_t w1, float sc, uint
     return make_uint4(f16x2_scaled(h0, sc), f16x2_scaled(h1, sc), f16x2_scaled(h2, sc), f16x2_scaled(h3, sc));
 }
 
-// One converter warp's quarter of an FP8 or INT8 prefix tile (keys 32q .. 32q + 31, pages 2q and
+// One converter warp's quarter of an FP8 prefix tile (keys 32q .. 32q + 31, pages 2q and
 // 2q + 1) from its staged codes to 128-byte swizzled rows in place: bf16 code values for K
-// (kMode 0, INT8: 3), fp16 code values times sc (kMode 1) or times the power of two p2 (kMode 2;
-// INT8: 4, one for each page) for V.  Every
+// (kMode 0), fp16 code values times sc (kMode 1) or times the power of two p2 (kMode 2) for V.  Every
 // lane reads its codes of a page (or half page) before any lane writes, since the rows
 // written cover the codes staged.
 template <int D, int kMode>
-__device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane, float sc, uint32_t p2 = 0,
-                                                    const uint32_t *page_p2 = nullptr) {
+__device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane, float sc, uint32_t p2 = 0) {
     using C = PrefillCfg<D>;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const int p = 2 * q + i;
-        if (kMode == 4) p2 = page_p2[p];
         const uint8_t *src = t + C::kOffFp8Page(p);
         if (D == 64) {
             // lane: row r, codes 32h .. 32h + 31 -> 16-byte chunks 4h .. 4h + 3 of row 16p + r
@@ -267,6 +274,38 @@ __device__ __forceinline__ void convert_fp8_quarter(uint8_t *t, int q, int lane,
                 *reinterpret_cast<uint4 *>(blk + sw128(16 * p + r, c0 + 3)) = codes8<kMode>(y.z, y.w, sc, p2);
                 __syncwarp();
             }
+        }
+    }
+}
+
+// One converter warp's quarter of an INT8 prefix tile, in place: bf16 code values for K (kMode 3), fp16
+// code values times the page's power of two for V (4).  A lane takes eight codes of a row at a time, so
+// that D / 8 neighbouring lanes read a row and write its chunks without a bank conflict (32 codes at a
+// time, two lanes a bank: 8 chunks of 512 over 16384 at head_dim 64 1603 us, this way 1536), four such
+// pieces at once.  A batch's rows lie where its own codes were (head_dim 128: row on row; 64: a page on
+// its codes), so each lane has read its batch before any writes.  (The next batch read ahead takes
+// registers that the warps do not have: 1760 us.)
+template <int D, int kMode>
+__device__ __forceinline__ void convert_int8_quarter(uint8_t *t, int q, int lane, const uint32_t *page_p2 = nullptr) {
+    using C = PrefillCfg<D>;
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+    const int r0 = lane / kLanes, c = lane % kLanes;
+    constexpr int NB = 4;
+    uint2 x[NB];
+#pragma unroll 1
+    for (int p = 2 * q; p < 2 * q + 2; ++p) {
+        const uint32_t p2 = kMode == 4 ? page_p2[p] : 0u;
+#pragma unroll 1
+        for (int b = 0; b < kPageSize / (NB * kRows); ++b) {
+            const uint8_t *src = t + C::kOffFp8Page(p) + (b * NB * kRows + r0) * D + c * 8;
+            uint8_t *dst = t + (c >> 3) * 16384;
+            const int row = kPageSize * p + b * NB * kRows + r0;
+#pragma unroll
+            for (int e = 0; e < NB; ++e) x[e] = *reinterpret_cast<const uint2 *>(src + e * kRows * D);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < NB; ++e)
+                *reinterpret_cast<uint4 *>(dst + sw128(row + e * kRows, c & 7)) = int8x8<kMode>(x[e].x, x[e].y, p2);
         }
     }
 }
@@ -616,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kFrom = kWindow || kInt8;  // an item's key tiles may start behind the first
     // INT8: the converters have more to do and are given more registers, at head_dim 64 the softmax's,
     // whose rows are shorter there (8 chunks of 512 tokens over 16384-token prefixes 1639 -> 1549 us),
-    // at 128 the side warps' (7 ragged chunks 183 -> 175 us)
-    constexpr uint32_t kSideRegs = kInt8 && D == 128 ? 40 : kRegsSide;
-    constexpr uint32_t kConvertRegs = kInt8 ? (D == 64 ? 48 : 40) : kRegsConvert;
+    // at 128 the side warps' (7 ragged chunks 183 -> 175 us with 40 for both, 130 -> 128 with 32 and 48)
+    constexpr uint32_t kSideRegs = kInt8 && D == 128 ? 32 : kRegsSide;
+    constexpr uint32_t kConvertRegs = kInt8 ? 48 : kRegsConvert;
     constexpr uint32_t kSoftmaxRegs = kInt8 && D == 64 ? 208 : kRegsSoftmax;
     static_assert(128 * kSideRegs + 128 * kConvertRegs + 256 * kSoftmaxRegs <= kThreads * kRegsLaunch, "register split");
 
@@ -1065,7 +1104,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (fp8_tile) convert_fp8_quarter<D, kInt8 ? 3 : 0>(sK + st * C::kKVBytes, q, lane, 1.f);
+                    if (fp8_tile && kInt8)
+                        convert_int8_quarter<D, 3>(sK + st * C::kKVBytes, q, lane);
+                    else if (fp8_tile)
+                        convert_fp8_quarter<D, 0>(sK + st * C::kKVBytes, q, lane, 1.f);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.k_conv[st]);
@@ -1079,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // V: code * 2^e8 (the softmax takes the rest of the scale), or fp16 of
                     // value * 2^-k, value = scale * e4m3(code), k of the item
                     if (kInt8)
-                        convert_fp8_quarter<D, 4>(sV + st * C::kKVBytes, q, lane, 1.f, 0, s_page[st].v2);
+                        convert_int8_quarter<D, 4>(sV + st * C::kKVBytes, q, lane, s_page[st].v2);
                     else if (fold8)
                         convert_fp8_quarter<D, 2>(sV + st * C::kKVBytes, q, lane, 1.f, p2e8);
                     else
