@@ -156,6 +156,7 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
         if (kSleep) {
             if (mbar_try_wait_sleep(bar, parity, 100000u)) return true;
         } else {
+#pragma unroll 1
             for (int i = 0; i < 128; ++i)
                 if (mbar_try_wait(bar, parity)) return true;
         }
