@@ -382,7 +382,8 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
  *             bytes (for its descriptor and total_tokens): each query block's prefix is then
  *             split over the SMs that would have no work, and a second kernel merges the parts
  *             (results agree with the unsplit ones within rounding, and do not depend on
- *             max_sms).  The answer is the header alone where a split would not pay. */
+ *             max_sms; such a call ignores SINKATTN_FLAG_LAUNCH_NEXT_EARLY).  The answer is the
+ *             header alone where a split would not pay.  It is for the current device. */
 int sinkattn_prefill_int8_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,
                                          size_t *bytes);
 

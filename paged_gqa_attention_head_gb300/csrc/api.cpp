@@ -844,6 +844,8 @@ int sinkattn_prefill_int8_workspace_size(const sinkattn_paged_desc *desc, int32_
     if (!bytes || total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
     int rc = check_heads(desc);
     if (rc) return rc;
+    *bytes = kStatusBytes;
+    if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;
     PrefillParts p;
     rc = prefill_int8_parts(desc, total_tokens, &p);
     if (rc) return rc;

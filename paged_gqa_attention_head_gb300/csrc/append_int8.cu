@@ -10,8 +10,9 @@
 // exact tie or at least 2^-10 away from one: x * (1 / s'), snapped to multiples of 2^-11, then
 // rounds exactly as the quotient does, without a division per element.
 //
-// Bound by HBM for long appends (4 D bytes read and 2 D written per token and head) and by
-// latency for a decode step's single tokens.  A warp holds the new rows of one page and head, K
+// Bound by HBM for long appends (4 D bytes read and 2 D written per token and head; 11708 tokens of 8
+// heads of 64 take 8.5 us, 62 % of the copy rate) and by latency for a decode step's single tokens (64
+// of them 3.4 us: entry, scale, rows, store one after the other).  A warp holds the new rows of one page and head, K
 // and V (at most 2 x 16 x D bf16), in registers: their maxima, then their codes, in one pass
 // over the data.  Which tokens begin a page's rows ("leaders") is found by the warp that owns
 // the token, so no plan of the ragged batch is needed: a warp owns a group of consecutive
@@ -227,7 +228,9 @@ cudaError_t launch_append_int8(int D, AppendInt8Args a, cudaStream_t stream) {
     int sms = 0;
     const cudaError_t e = current_sms(&sms);
     if (e != cudaSuccess) return e;
-    // a page's worth of tokens a warp once that still fills the GPU, else one token a warp
+    // a page's worth of tokens a warp once that still fills the GPU, else one token a warp: 11708
+    // tokens of 8 heads of 64 take 8.5 us so and 33 us with a token a warp, whose lanes find out for
+    // one token what they could for sixteen
     a.group = (int64_t)a.T * a.Hkv > (int64_t)sms * 64 ? kPageSize : 1;
     const int64_t units = ((int64_t)a.T + a.group - 1) / a.group * a.Hkv;
     const int64_t grid = (units + kI8Warps - 1) / kI8Warps;

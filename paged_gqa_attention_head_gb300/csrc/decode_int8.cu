@@ -29,6 +29,9 @@
 // The running maximum moves only when a score passes it by more than 8 (log2): P is taken as
 // 2^(s - m + 7), at most 2^15, so a stale maximum costs no precision and the votes, the column
 // maxima and the rescale of O^T drop out of almost every unit.
+// Measured: 64 sequences up to 131072 tokens, 64/8 heads of 64 (1.26 GB) 200 us, 6.3 TB/s, bound by
+// HBM; 64 sequences up to 16384, 64/4 heads of 128 (0.56 GB) 109 us, 5.1 TB/s, bound by the latencies
+// of the two warps a scheduler that the accumulators of 16 heads leave room for.
 #include <math.h>
 
 #include <mutex>
@@ -583,7 +586,8 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
 // A block of 128 threads: D/4 threads span the head's outputs, the others split the states (8 ways
 // at head_dim 64, 4 at 128), so that the loads of many states are in flight at once; each part
 // keeps its own maximum, and the parts meet in shared memory in a fixed order.  It is launched as
-// a programmatic dependent of the split-KV kernel: its blocks are set up while that one ends.
+// a programmatic dependent of the split-KV kernel: its blocks are set up while that one ends (one
+// sequence of 4097 tokens: 10.5 us for both kernels).
 template <int D>
 __global__ void __launch_bounds__(128) merge_int8_kernel(const DecodeArgs a) {
     constexpr int kQuads = D / 4, kParts = 128 / kQuads;

@@ -82,6 +82,11 @@ def test_prefill_int8_rejects(sa):
     assert pre(d=_desc(sa, head_dim=32)) == 2
     assert pre(T=0, q=None, kp=None) == 0
     assert pre(d=_desc(sa, num_seqs=0), q=None) == 0
+    n = ctypes.c_size_t()
+    size = lambda T=8, d=_desc(sa), out=ctypes.byref(n): lib.sinkattn_prefill_int8_workspace_size(  # noqa: E731
+        None if d is None else ctypes.byref(d), T, out)
+    assert size(T=-1) == 1 and size(d=None) == 1 and size(out=None) == 1 and size(d=_desc(sa, head_dim=32)) == 2
+    assert size(T=0) == 0 and n.value == 256 and size(d=_desc(sa, num_seqs=0)) == 0 and n.value == 256
     x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         sa.prefill_int8(x, x, x, None, None, None, None, None, None)
