@@ -147,7 +147,10 @@ struct Bars {
 // fast path is one blocking probe: measured, a vote inside the wait cost the prefill 18 %,
 // a non-blocking first probe 5-20 %, and any branch ahead of the first probe (such as one
 // for the testing limit) 25-45 %, so the testing setting is handled by the producer instead.
-template <bool kSleep = false>
+// kSmall (the INT8 kernels, whose code is the largest): the loop of probes is not unrolled, so that
+// waiting warps leave the instruction cache to the others (7 ragged chunks at head_dim 128 128 -> 126
+// us, 17 tokens over 1003 25.3 -> 24.5; the bf16 prefix of 8 x 16384 tokens is 3 % slower so).
+template <bool kSleep = false, bool kSmall = false>
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort,
                                               uint32_t *status, uint64_t limit_cycles) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -155,8 +158,11 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     for (;;) {
         if (kSleep) {
             if (mbar_try_wait_sleep(bar, parity, 100000u)) return true;
-        } else {
+        } else if (kSmall) {
 #pragma unroll 1
+            for (int i = 0; i < 128; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+        } else {
             for (int i = 0; i < 128; ++i)
                 if (mbar_try_wait(bar, parity)) return true;
         }
@@ -1202,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int k = 0;
         bool ok = x < ntiles;
         auto take = [&](int kk) {
-            if (!wait_or_abort(&bars.item_full[kk % kItemRing], (uint32_t)((kk / kItemRing) & 1), s_abort, a.status,
+            if (!wait_or_abort<false, kInt8>(&bars.item_full[kk % kItemRing], (uint32_t)((kk / kItemRing) & 1), s_abort, a.status,
                                a.wait_limit_cycles))
                 return n_items;
             return s_slot[kk % kItemRing].rank;
@@ -1229,7 +1235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b = i % NBS, pb = i % NBP;
                 const uint32_t ts = tmem + lane_base + C::kColS(b);
                 const uint32_t tp = tmem + lane_base + C::kColP(pb);
-                if (!wait_or_abort(&bars.s_full[b], (i / NBS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+                if (!wait_or_abort<false, kInt8>(&bars.s_full[b], (i / NBS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                     ok = false;
                     break;
                 }
@@ -1297,7 +1303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  fmaxf(mx8[6], mx8[7]));
                 };
                 if (kInt8 && j == 0 &&  // the page scales are in place once the V tile is
-                    !wait_or_abort(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
+                    !wait_or_abort<false, kInt8>(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
                                    a.wait_limit_cycles)) {
                     ok = false;
                     break;
@@ -1312,7 +1318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (keys 2c, 2c + 1 in column c); 2^-k is the scale of the V quarter holding
                 // keys 32ch..32ch+31
                 const int vst = (tcount - 1) % NS;
-                if (!wait_or_abort(&bars.v_conv[vst], ((tcount - 1) / NS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+                if (!wait_or_abort<false, kInt8>(&bars.v_conv[vst], ((tcount - 1) / NS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                     ok = false;
                     break;
                 }
@@ -1360,7 +1366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (ch == 0 && pwait) {
                             pwait = false;
-                            if (!wait_or_abort(&bars.pv_done[pb], ((i - NBP) / NBP) & 1, s_abort, a.status,
+                            if (!wait_or_abort<false, kInt8>(&bars.pv_done[pb], ((i - NBP) / NBP) & 1, s_abort, a.status,
                                                a.wait_limit_cycles))
                                 pfail = true;
                             tc::fence_after_sync();
@@ -1390,7 +1396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float mt = kInt8 ? row_max() : row_max() * sc;
                         // O_x must hold the P.V of this query tile's previous key tile, product i - ntiles
                         const uint32_t ip = i - ntiles;
-                        if (!wait_or_abort(&bars.pv_done[ip % NBP], (ip / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+                        if (!wait_or_abort<false, kInt8>(&bars.pv_done[ip % NBP], (ip / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                             ok = false;
                             break;
                         }
@@ -1423,7 +1429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // epilogue: O / l for this row, once the item's last P.V has landed
             const uint32_t il = (tcount - 1) * ntiles + x;  // S product of the last key tile
-            if (!wait_or_abort(&bars.pv_done[il % NBP], (il / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+            if (!wait_or_abort<false, kInt8>(&bars.pv_done[il % NBP], (il / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                 ok = false;
                 break;
             }
