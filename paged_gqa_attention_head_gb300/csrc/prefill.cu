@@ -734,29 +734,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             int r = 0;
             if (lane == 0) {
                 ItemSlot &sl = s_slot[kk % kItemRing];
-                bool empty;  // a part past the item's last one
-                do {
-                    empty = false;
-                    r = min((int)atomicAdd(a.sched, 1u), n_items);
-                    if (kInt8 && splits > 1 && r < n_items) {
+                bool first = true;  // the item's part that counts the sink
+                r = min((int)atomicAdd(a.sched, 1u), n_items);
+                if constexpr (kInt8) {
+                    while (splits > 1 && r < n_items) {  // parts past their item's last tile are none
                         const ItemGeom gm = geom_of<kWindow, kCausal>(a, item_of<kInt8>(a, wl, r / splits));
-                        empty = r % splits * part_tiles(gm.n_kv, splits) >= gm.n_kv;
+                        if (r % splits * part_tiles(gm.n_kv, splits) < gm.n_kv) break;
+                        r = min((int)atomicAdd(a.sched, 1u), n_items);
                     }
-                } while (empty);
+                }
                 sl.rank = r;
                 if (r < n_items) {
-                    sl.it = item_of<kInt8>(a, wl, r / splits);
+                    sl.it = item_of<kInt8>(a, wl, kInt8 ? r / splits : r);
                     sl.gm = geom_of<kWindow, kCausal>(a, sl.it);
-                    sl.part = -1;  // whole
-                    const int per = part_tiles(sl.gm.n_kv, splits);
-                    if (kInt8 && splits > 1 && per < sl.gm.n_kv) {
-                        sl.part = r % splits;
-                        const int begin = sl.part * per;
-                        sl.gm.t0 += begin;
-                        sl.gm.n_kv = min(per, sl.gm.n_kv - begin);
+                    if constexpr (kInt8) {
+                        int part = -1;  // whole
+                        const int per = part_tiles(sl.gm.n_kv, splits);
+                        if (splits > 1 && per < sl.gm.n_kv) {
+                            part = r % splits;
+                            const int begin = part * per;
+                            sl.gm.t0 += begin;
+                            sl.gm.n_kv = min(per, sl.gm.n_kv - begin);
+                        }
+                        sl.part = part;
+                        first = part <= 0;
                     }
                     for (int x = 0; x < 2; ++x)
-                        sl.sink2[x] = a.sinks && x < ntiles && sl.part <= 0 ? a.sinks[sl.it.h0 + x] * kLog2e : -INFINITY;
+                        sl.sink2[x] = a.sinks && x < ntiles && first ? a.sinks[sl.it.h0 + x] * kLog2e : -INFINITY;
                     sl.kscale = kFp8 && a.k_scale ? a.k_scale[sl.gm.g] : 1.f;
                     sl.vscale = kFp8 && a.v_scale ? a.v_scale[sl.gm.g] : 1.f;
                 }
@@ -1434,6 +1438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc::fence_after_sync();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             const bool valid = t < gm.L && gm.row0 >= 0 && gm.row0 + t < a.T;
             const int part = kInt8 ? s_slot[k % kItemRing].part : -1;
             if (kInt8 && part >= 0) {
@@ -1459,7 +1464,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&bars.o_free[x]);
                 continue;
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
             __nv_bfloat16 *og = reinterpret_cast<__nv_bfloat16 *>(a.out) +
                                 ((int64_t)(gm.row0 + t) * a.Hq + h) * D;
 #pragma unroll
