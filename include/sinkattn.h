@@ -154,7 +154,9 @@ const char *sinkattn_last_cuda_error(void);
  * must be zero before the first call (sinkattn_workspace_init, or a memset).  The
  * size depends on the descriptor and on the number of SMs of the CURRENT device.
  * Calls that share one workspace must be ordered on the GPU (same stream, or
- * synchronised); overlapping calls on one workspace race.
+ * synchronised); overlapping calls on one workspace race.  A call of several kernels
+ * counts as one: host threads that call on one stream need a workspace each (or a lock
+ * around the call), or one's kernels may come between another's.
  */
 int sinkattn_decode_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
 

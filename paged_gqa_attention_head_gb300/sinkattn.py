@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -651,27 +652,36 @@ def _status_buffer(index: int) -> Optional[torch.Tensor]:
 
 
 _append_keys: dict = {}
-_stream_workspaces: dict = {}
+
+
+class _Scratch(threading.local):
+    def __init__(self):
+        self.buffers = {}
+
+
+_scratch = _Scratch()
 _retired_workspaces: list = []  # replaced by larger ones; a captured graph may hold their addresses
 
 
 def _stream_workspace(nbytes: int, index: int, stream: int, tag: str) -> torch.Tensor:
-    """Default scratch of a call on the current stream: one buffer per (device, stream, tag), so
-    that calls on two streams never share one.  While the stream is captured the call gets a buffer
-    of its own in the graph's memory, whose header the graph clears at each replay; so no two
-    graphs, and no graph and an eager call, share one."""
+    """Default scratch of a call on the current stream: one buffer per (host thread, device, stream,
+    tag).  So calls on two streams never share one, and neither do two threads that call on one
+    stream: a call is a split kernel and its merge, and another thread's split kernel may come
+    between them.  While the stream is captured the call gets a buffer of its own in the graph's
+    memory, whose header the graph clears at each replay; so no two graphs, and no graph and an
+    eager call, share one."""
     if _capturing():
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         _call(index, "sinkattn_workspace_init", ws.data_ptr(), ws.numel(), stream)
         return ws
     key = (index, stream, tag)
-    ws = _stream_workspaces.get(key)
+    ws = _scratch.buffers.get(key)
     if ws is None or ws.numel() < nbytes:
         if ws is not None:
             _retired_workspaces.append(ws)
             nbytes = max(nbytes, 2 * ws.numel())
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
-        _stream_workspaces[key] = ws
+        _scratch.buffers[key] = ws
     return ws
 
 

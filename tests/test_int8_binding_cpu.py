@@ -1,0 +1,35 @@
+"""Host side of the INT8 cache's calls: which scratch and which status word a call gets (no GPU needed)."""
+import threading
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def host_scratch(sa, monkeypatch):
+    """The default scratch as host memory, outside any capture."""
+    real = torch.zeros
+    monkeypatch.setattr(sa.torch, "zeros", lambda *size, dtype=None, device=None: real(*size, dtype=dtype))
+    monkeypatch.setattr(sa, "_capturing", lambda: False)
+    return sa
+
+
+def test_threads_on_one_stream_do_not_share_scratch(host_scratch):
+    """A call is a split kernel and a merge: with one buffer, another thread's split kernel could
+    overwrite the partial states between the two."""
+    sa, got = host_scratch, {}
+
+    def call(name):
+        got[name] = [sa._stream_workspace(n, 0, 0, tag) for n, tag in ((1000, "decode"), (500, "decode"), (500, "prefill"))]
+
+    call("main")
+    threads = [threading.Thread(target=call, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for mine in got.values():
+        assert mine[0] is mine[1]  # a thread keeps its own
+        assert mine[2] is not mine[0]
+    assert len({id(mine[0]) for mine in got.values()}) == 3
+    assert host_scratch._stream_workspace(500, 0, 7, "decode") is not got["main"][0]  # another stream
