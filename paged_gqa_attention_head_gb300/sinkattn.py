@@ -660,7 +660,6 @@ class _Scratch(threading.local):
 
 
 _scratch = _Scratch()
-_retired_workspaces: list = []  # replaced by larger ones; a captured graph may hold their addresses
 
 
 def _stream_workspace(nbytes: int, index: int, stream: int, tag: str) -> torch.Tensor:
@@ -677,8 +676,7 @@ def _stream_workspace(nbytes: int, index: int, stream: int, tag: str) -> torch.T
     key = (index, stream, tag)
     ws = _scratch.buffers.get(key)
     if ws is None or ws.numel() < nbytes:
-        if ws is not None:
-            _retired_workspaces.append(ws)
+        if ws is not None:  # used on this stream alone, so its memory may go back to the allocator
             nbytes = max(nbytes, 2 * ws.numel())
         ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         _scratch.buffers[key] = ws

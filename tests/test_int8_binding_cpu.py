@@ -1,5 +1,6 @@
 """Host side of the INT8 cache's calls: which scratch and which status word a call gets (no GPU needed)."""
 import threading
+import weakref
 
 import pytest
 import torch
@@ -11,6 +12,7 @@ def host_scratch(sa, monkeypatch):
     real = torch.zeros
     monkeypatch.setattr(sa.torch, "zeros", lambda *size, dtype=None, device=None: real(*size, dtype=dtype))
     monkeypatch.setattr(sa, "_capturing", lambda: False)
+    monkeypatch.setattr(sa, "_scratch", sa._Scratch())  # nothing of it stays for tests on a GPU
     return sa
 
 
@@ -33,3 +35,12 @@ def test_threads_on_one_stream_do_not_share_scratch(host_scratch):
         assert mine[2] is not mine[0]
     assert len({id(mine[0]) for mine in got.values()}) == 3
     assert host_scratch._stream_workspace(500, 0, 7, "decode") is not got["main"][0]  # another stream
+
+
+def test_outgrown_scratch_is_let_go(host_scratch):
+    """No captured call uses the eager scratch, so nothing needs the smaller buffer any more."""
+    ws = host_scratch._stream_workspace(1000, 0, 9, "decode")
+    old = weakref.ref(ws)
+    del ws
+    assert host_scratch._stream_workspace(1001, 0, 9, "decode").numel() == 2000
+    assert old() is None
