@@ -396,6 +396,22 @@ int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int
                           const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
                           sinkattn_stream_t stream);
 
+/* The two calls above with the status bits OR-ed into *status (device memory, 4-byte aligned)
+ * instead of the workspace's header; NULL: into the header.  So a scratch that comes and goes, as a
+ * captured call's may, loses no report, and calls on several streams may share one status word.
+ * The decode then leaves the header unread and unwritten; the prefill's must be zero as before. */
+int sinkattn_decode_int8_report(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
+                                const int32_t *block_table, const int32_t *seq_lens, const float *sinks,
+                                float scale, void *out, float *lse, const sinkattn_paged_desc *desc,
+                                void *workspace, size_t ws_bytes, uint32_t *status, sinkattn_stream_t stream);
+
+int sinkattn_prefill_int8_report(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                                 int32_t total_tokens, const void *k_pages, const void *v_pages,
+                                 const float *kv_scales, const int32_t *prefix_block_table,
+                                 const int32_t *prefix_lens, const float *sinks, float scale, void *out,
+                                 float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                                 uint32_t *status, sinkattn_stream_t stream);
+
 /* ------------------------------------------------- queries and keys before attention --
  * Per-head RMS norm and rotary position embedding of a step's queries and keys in one pass, for
  * prefills, decodes and appends alike (sinkattn_decode_append_rope covers gpt-oss decode steps

@@ -460,7 +460,7 @@ const char *sinkattn_error_string(int code) {
     }
 }
 
-int sinkattn_version(void) { return 10300; }
+int sinkattn_version(void) { return 10400; }
 
 int sinkattn_decode_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
     if (!bytes) return SINKATTN_ERR_INVALID_ARG;
@@ -653,14 +653,14 @@ int sinkattn_decode_int8_workspace_size(const sinkattn_paged_desc *desc, size_t 
     return SINKATTN_OK;
 }
 
-int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
-                         const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
-                         void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
-                         sinkattn_stream_t stream) {
+int sinkattn_decode_int8_report(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
+                                const int32_t *block_table, const int32_t *seq_lens, const float *sinks,
+                                float scale, void *out, float *lse, const sinkattn_paged_desc *desc,
+                                void *workspace, size_t ws_bytes, uint32_t *status, sinkattn_stream_t stream) {
     // an empty batch is a no-op (its data pointers may be NULL)
     if (desc && desc->num_seqs == 0) return check_decode_desc(desc);
     if (!k_pages || !v_pages || !kv_scales || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
-        !aligned(kv_scales, 8))
+        !aligned(kv_scales, 8) || !aligned(status, 4))
         return SINKATTN_ERR_INVALID_ARG;
     DecodePrep P;
     int rc = prepare_decode(q, block_table, seq_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, &P, true);
@@ -672,12 +672,21 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
     rc = encode_pages_map_int8(&vmap, v_pages, desc->num_pages, desc->num_kv_heads, desc->head_dim);
     if (rc) return rc;
     P.args.kv_scales = kv_scales;
+    if (status) P.args.status = status;
     P.args.total_warps = P.layout.total_warps8;
     rc = cuda_rc(launch_decode_int8(desc->head_dim, P.args, kmap, vmap, P.layout.ctas8, P.layout.smem8,
                                     (cudaStream_t)stream),
                  "int8 split-KV decode launch");
     if (rc) return rc;
     return cuda_rc(launch_merge_int8(desc->head_dim, P.args, (cudaStream_t)stream), "int8 merge launch");
+}
+
+int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,
+                         const int32_t *block_table, const int32_t *seq_lens, const float *sinks, float scale,
+                         void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                         sinkattn_stream_t stream) {
+    return sinkattn_decode_int8_report(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks, scale, out, lse,
+                                       desc, workspace, ws_bytes, nullptr, stream);
 }
 
 int sinkattn_prefill_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
@@ -717,7 +726,8 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
                    const int32_t *prefix_block_table, const int32_t *prefix_lens, const float *sinks,
                    float scale, void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace,
                    size_t ws_bytes, bool fp8, const float *k_scale, const float *v_scale,
-                   bool causal, sinkattn_stream_t stream, const float *kv_scales = nullptr) {
+                   bool causal, sinkattn_stream_t stream, const float *kv_scales = nullptr,
+                   uint32_t *status = nullptr) {
     int rc = check_heads(desc);
     if (rc) return rc;
     if (!causal && desc->window > 0) return SINKATTN_ERR_INVALID_ARG;
@@ -779,7 +789,7 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
     a.max_sms = desc->max_sms;
     a.wait_limit_ns = wait_limit_ns(desc->wait_limit_us);
     a.wait_limit_cycles = a.wait_limit_ns * 2;  // SM cycles, at least the limit up to 2 GHz
-    a.status = static_cast<uint32_t *>(workspace);
+    a.status = status ? status : static_cast<uint32_t *>(workspace);
     a.fp8_prefix = fp8;
     a.causal = causal;
     a.launch_dependents = (desc->flags & SINKATTN_FLAG_LAUNCH_NEXT_EARLY) != 0;
@@ -853,21 +863,33 @@ int sinkattn_prefill_int8_workspace_size(const sinkattn_paged_desc *desc, int32_
     return SINKATTN_OK;
 }
 
+int sinkattn_prefill_int8_report(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                                 int32_t total_tokens, const void *k_pages, const void *v_pages,
+                                 const float *kv_scales, const int32_t *prefix_block_table,
+                                 const int32_t *prefix_lens, const float *sinks, float scale, void *out,
+                                 float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                                 uint32_t *status, sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
+    if (!k_pages || !v_pages || !kv_scales || !aligned(kv_scales, 8) || !prefix_block_table || !prefix_lens ||
+        !aligned(status, 4))
+        return SINKATTN_ERR_INVALID_ARG;
+    return prefill_common(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, prefix_block_table,
+                          prefix_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, false, nullptr,
+                          nullptr, true, stream, kv_scales, status);
+}
+
 int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
                           int32_t total_tokens, const void *k_pages, const void *v_pages,
                           const float *kv_scales, const int32_t *prefix_block_table,
                           const int32_t *prefix_lens, const float *sinks, float scale, void *out, float *lse,
                           const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
                           sinkattn_stream_t stream) {
-    int rc = check_heads(desc);
-    if (rc) return rc;
-    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
-    if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
-    if (!k_pages || !v_pages || !kv_scales || !aligned(kv_scales, 8) || !prefix_block_table || !prefix_lens)
-        return SINKATTN_ERR_INVALID_ARG;
-    return prefill_common(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, prefix_block_table,
-                          prefix_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, false, nullptr,
-                          nullptr, true, stream, kv_scales);
+    return sinkattn_prefill_int8_report(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, kv_scales,
+                                        prefix_block_table, prefix_lens, sinks, scale, out, lse, desc, workspace,
+                                        ws_bytes, nullptr, stream);
 }
 
 int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,

@@ -12,6 +12,7 @@ import ctypes
 import math
 import os
 import threading
+import warnings
 from typing import Optional
 
 import torch
@@ -82,9 +83,12 @@ SIGNATURES = {
                                                _SZ, _P]),
     "sinkattn_decode_int8_workspace_size": (ctypes.c_int, [_DP, ctypes.POINTER(_SZ)]),
     "sinkattn_decode_int8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P]),
+    "sinkattn_decode_int8_report": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P, _P]),
     "sinkattn_prefill_int8_workspace_size": (ctypes.c_int, [_DP, _I32, ctypes.POINTER(_SZ)]),
     "sinkattn_prefill_int8": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP,
                                              _P, _SZ, _P]),
+    "sinkattn_prefill_int8_report": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP,
+                                                    _P, _SZ, _P, _P]),
     "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
                                              ctypes.POINTER(RotaryDesc), _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
@@ -639,19 +643,36 @@ def _call(index: int, what: str, *args) -> None:
 
 
 def _status_buffer(index: int) -> Optional[torch.Tensor]:
-    """The status word that calls without scratch share (bits are OR-ed in, so streams may share it):
-    workspace(256, device, "append"), read with get_status.  None while a capture runs before the
-    buffer exists: the calls then report nothing."""
+    """The status word that the calls below share when they are given no workspace_buf (bits are OR-ed
+    in, so streams and graphs may share it): workspace(256, device, "append"), read by
+    default_status.  None while a capture runs before the word exists."""
     key = _append_keys.get(index)
     if key is None:
         key = _append_keys[index] = (torch.device("cuda", index), "append")
     ws = _workspaces.get(key)
-    if ws is None and not _capturing():
-        ws = workspace(256, *key)
+    if ws is None:
+        if _capturing():
+            warnings.warn("a captured call will not report its status: call default_status() once before the capture",
+                          RuntimeWarning, stacklevel=3)
+            return None
+        with _status_lock:
+            ws = workspace(256, *key)
+        torch.cuda.current_stream(index).synchronize()  # zero before another stream's call sets a bit
     return ws
 
 
+def default_status(device=None) -> int:
+    """Read and clear the status bits (STATUS_*) of the calls on a CUDA device (default: the current
+    one) that were given no workspace_buf: append_kv, append_kv_fp8, append_kv_int8, qk_norm_rope,
+    decode_int8 and prefill_int8, from any thread or stream, eager or replayed from a graph.  It waits
+    for the current stream; work on others counts once it has run.  Call it once before a first
+    capture, so that the captured calls have a word to report to."""
+    index = torch.device("cuda" if device is None else device).index
+    return get_status(_status_buffer(_current_device() if index is None else index))
+
+
 _append_keys: dict = {}
+_status_lock = threading.Lock()
 
 
 class _Scratch(threading.local):
@@ -662,16 +683,17 @@ class _Scratch(threading.local):
 _scratch = _Scratch()
 
 
-def _stream_workspace(nbytes: int, index: int, stream: int, tag: str) -> torch.Tensor:
+def _stream_workspace(nbytes: int, index: int, stream: int, tag: str, header: bool = True) -> torch.Tensor:
     """Default scratch of a call on the current stream: one buffer per (host thread, device, stream,
     tag).  So calls on two streams never share one, and neither do two threads that call on one
     stream: a call is a split kernel and its merge, and another thread's split kernel may come
     between them.  While the stream is captured the call gets a buffer of its own in the graph's
-    memory, whose header the graph clears at each replay; so no two graphs, and no graph and an
-    eager call, share one."""
+    memory, whose header, if the call reads it, the graph clears at each replay; so no two graphs, and
+    no graph and an eager call, share one."""
     if _capturing():
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
-        _call(index, "sinkattn_workspace_init", ws.data_ptr(), ws.numel(), stream)
+        if header:
+            _call(index, "sinkattn_workspace_init", ws.data_ptr(), ws.numel(), stream)
         return ws
     key = (index, stream, tag)
     ws = _scratch.buffers.get(key)
@@ -780,7 +802,8 @@ def _need_sinks(sinks, heads: int, index: int) -> Optional[int]:
 def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=None, scale=None, out=None,
                 lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0, wait_limit_us=0):
     """Split-KV paged decode over an INT8 cache with a scale per page and KV head
-    (sinkattn_decode_int8).  Returns (out, lse)."""
+    (sinkattn_decode_int8).  Status bits go to workspace_buf's header, without one to
+    default_status.  Returns (out, lse)."""
     dev = _need_cuda(q, "q")
     _need_dense(q, "q", torch.bfloat16, dev, 3)
     _need_dense(block_table, "block_table", torch.int32, dev, 2)
@@ -795,12 +818,14 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
     sk = _need_sinks(sinks, Hq, dev)
     out, lse = _attention_outputs(q, out, lse, return_lse, dev)
     key = (B, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
-    desc, stream, ws = _desc_ref(*key), _raw_stream(dev), workspace_buf
+    desc, stream, ws, status = _desc_ref(*key), _raw_stream(dev), workspace_buf, None
     if ws is None:
-        ws = _stream_workspace(_int8_size("sinkattn_decode_int8_workspace_size", dev, desc, key), dev, stream, "decode")
-    _call(dev, "sinkattn_decode_int8", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
+        ws = _stream_workspace(_int8_size("sinkattn_decode_int8_workspace_size", dev, desc, key), dev, stream, "decode",
+                               header=False)
+        status = _status_buffer(dev)
+    _call(dev, "sinkattn_decode_int8_report", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
           block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), stream)
+          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), _ptr(status), stream)
     return out, lse
 
 
@@ -808,7 +833,8 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
                  scale=None, out=None, lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0,
                  wait_limit_us=0):
     """Chunked prefill over an INT8 paged prefix with a scale per page and KV head
-    (sinkattn_prefill_int8); the new tokens' q, k, v bf16.  Returns (out, lse)."""
+    (sinkattn_prefill_int8); the new tokens' q, k, v bf16.  Status bits go to workspace_buf's header,
+    without one to default_status.  Returns (out, lse)."""
     dev = _need_cuda(q, "q")
     _need_dense(q, "q", torch.bfloat16, dev, 3)
     _need_dense(k, "k", torch.bfloat16, dev, 3)
@@ -826,14 +852,15 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
     sk = _need_sinks(sinks, Hq, dev)
     out, lse = _attention_outputs(q, out, lse, return_lse, dev)
     key = (n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
-    desc, stream, ws = _desc_ref(*key), _raw_stream(dev), workspace_buf
+    desc, stream, ws, status = _desc_ref(*key), _raw_stream(dev), workspace_buf, None
     if ws is None:
         ws = _stream_workspace(_int8_size("sinkattn_prefill_int8_workspace_size", dev, desc, key, T), dev, stream,
                                "prefill")
-    _call(dev, "sinkattn_prefill_int8", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
+        status = _status_buffer(dev)
+    _call(dev, "sinkattn_prefill_int8_report", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
           k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), prefix_block_table.data_ptr(),
           prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), stream)
+          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), _ptr(status), stream)
     return out, lse
 
 

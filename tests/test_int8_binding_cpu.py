@@ -1,4 +1,5 @@
 """Host side of the INT8 cache's calls: which scratch and which status word a call gets (no GPU needed)."""
+import ctypes
 import threading
 import weakref
 
@@ -44,3 +45,31 @@ def test_outgrown_scratch_is_let_go(host_scratch):
     del ws
     assert host_scratch._stream_workspace(1001, 0, 9, "decode").numel() == 2000
     assert old() is None
+
+
+def test_report_entry_points_check_their_arguments(sa):
+    """Before any CUDA work: missing or misaligned pointers, the status word's among them; empty calls."""
+    lib = sa.load()
+    desc = lambda n: ctypes.byref(sa.paged_desc(n, 8, 2, 64, 10, 4))  # noqa: E731
+    buf = (ctypes.c_uint8 * 4096)()
+    p = (ctypes.addressof(buf) + 255) // 256 * 256
+    decode = lambda ptr, status, n=4: lib.sinkattn_decode_int8_report(  # noqa: E731
+        p, ptr, p, p, p, p, None, 0.125, p, None, desc(n), p, 256, status, None)
+    prefill = lambda ptr, status, n=4, tokens=8: lib.sinkattn_prefill_int8_report(  # noqa: E731
+        p, p, p, p, tokens, ptr, p, p, p, p, None, 0.125, p, None, desc(n), p, 256, status, None)
+    for call in (decode, prefill):
+        assert call(None, None) == sa.ERR_INVALID_ARG
+        assert call(p, p + 2) == sa.ERR_INVALID_ARG
+        assert call(None, None, n=0) == sa.OK
+    assert prefill(None, None, tokens=0) == sa.OK
+
+
+def test_the_shared_status_word_during_a_capture(host_scratch, monkeypatch):
+    """Before the word exists a captured call says that it will not report."""
+    sa = host_scratch
+    monkeypatch.setattr(sa, "_workspaces", {})
+    monkeypatch.setattr(sa, "_capturing", lambda: True)
+    with pytest.warns(RuntimeWarning, match="default_status"):
+        assert sa._status_buffer(0) is None
+    word = sa._workspaces[torch.device("cuda", 0), "append"] = torch.zeros(256, dtype=torch.uint8)
+    assert sa._status_buffer(0) is word
