@@ -80,15 +80,25 @@ constexpr int kItemRing = 16;
 // scale m * 2^e (m in [1, 2)) the V tile holds code * 2^e', exact in fp16, and P is taken times
 // rest = m * 2^(e - e'), which joins the exponent of P as add = log2(rest) and leaves the row
 // sum by mul = 1 / rest; e' is e where -24 <= e <= 8 (127 * 2^8 < 2^15), else the nearest end.
+// Scales below 2^-24 would take P's bits with them, so P and O are held times 2^lift while the
+// item has met no larger one: lift = -24 - e of the largest scale so far, 0 once that reaches
+// 2^-24 or a tile of new tokens comes.  It is part of rest.  Where it falls, the tile's row sums are
+// made infinite, which sends every row to the rescale that a growing maximum takes, and there O
+// moves by drop = 2^-fall: the other tiles pay nothing for it.  (A test of drop in every tile: 8 x
+// 512 over 16384 1 % slower, ragged chunks at head_dim 128 2 %.)
 // Tiles of new tokens use the same fields: k the score scale, add and mul the V exponents.
 // k and add lie twice each, as the paired arithmetic takes them.
 struct PageScales {
     float2 k[8];     // score factor: K scale * softmax scale * log2(e)
     float2 add[8];   // V: what the exponent of P gains
-    float mul[8];    // V: what a sum of such P is multiplied by
+    float mul[8];    // V: what a sum of such P is multiplied by; infinite where O has to move first
+    float mul_again[8];  // the same, always finite
     uint32_t v2[8];  // V: 2^e' as a pair of fp16
+    float drop;      // V: what O is multiplied by before this tile's product
+    float pad[3];
 };
-constexpr int kPageScaleBytes = 192;
+constexpr int kPageScaleBytes = 240;
+constexpr int kVScaleMinExp = -100;  // a V scale below 2^-100 (the append writes none) counts as 0
 static_assert(sizeof(PageScales) == kPageScaleBytes, "page scales");
 
 // QB: Q buffers.  Two at head_dim 64 with a sliding window, where items are one or two key
@@ -603,7 +613,11 @@ struct alignas(16) ItemSlot {
     Item it;
     ItemGeom gm;
     float sink2[2];     // per query tile: sink * log2(e), -inf without sinks
-    float kscale, vscale;  // FP8 prefix: the KV head's scales (1 if not given)
+    float kscale;          // FP8 prefix: the KV head's scales (1 if not given)
+    union {
+        float vscale;
+        int lift;          // INT8 prefix: at the item's last tile
+    };
     int part;              // INT8 prefix: the part of a split item; -1: the item is whole
 };
 static_assert(sizeof(ItemSlot) == 64, "item slot");
@@ -762,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 2; ++x)
                         sl.sink2[x] = a.sinks && x < ntiles && first ? a.sinks[sl.it.h0 + x] * kLog2e : -INFINITY;
                     sl.kscale = kFp8 && a.k_scale ? a.k_scale[sl.gm.g] : 1.f;
-                    sl.vscale = kFp8 && a.v_scale ? a.v_scale[sl.gm.g] : 1.f;
+                    if (!kInt8) sl.vscale = kFp8 && a.v_scale ? a.v_scale[sl.gm.g] : 1.f;
                 }
                 mbar_arrive(&bars.item_full[kk % kItemRing]);
             }
@@ -805,13 +819,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             int ahead = -1;
+            int lift = 0;  // INT8: P and O are held times 2^lift
             for (int j = 0; j < gm.n_kv; ++j, ++kv) {
                 const int s = kv % NS, u = kv / NS;
                 const int tt = kFrom ? gm.t0 + j : j;  // key tile
                 // prefix tile: lane p < 8 looks up page 8tt + p (issued before the wait below so
                 // the load overlaps it); nrow = its valid rows, pg = -1 for a missing page
                 int nrow = 0, pg = -1;
-                float2 psc = make_float2(1.f, 1.f);  // INT8: the page's scales (K, V)
+                float2 psc = make_float2(1.f, 0.f);  // INT8: the page's scales (K, V); V 0: its values are 0
                 if (tt < gm.n_pre && lane < 8) {
                     const int page = tt * 8 + lane;
                     nrow = min(kPageSize, max(0, gm.P - page * kPageSize));
@@ -835,28 +850,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint8_t *kt = sK + s * C::kKVBytes;
                 uint8_t *vt = sV + s * C::kKVBytes;
-                if (kInt8) {
-                    if (lane < 8) {
-                        PageScales &ps = s_page[s];
-                        if (tt < gm.n_pre) {
-                            const int e = (int)((__float_as_uint(psc.y) >> 23) & 0xFFu) - 127;
-                            const int e2 = min(max(e, -24), 8);
-                            // V scale / 2^e2 (a scale of 0: any factor, the values are 0 by e' alone)
-                            const float rest = psc.y > 0.f ? psc.y * __uint_as_float((uint32_t)(127 - e2) << 23) : 1.f;
-                            // 2^e2 in fp16: a normal from 2^-14 up, a subnormal below
-                            const uint32_t h = !(psc.y > 0.f) ? 0u : e2 >= -14 ? (uint32_t)(e2 + 15) << 10 : 1u << (e2 + 24);
-                            // never 0, so that a hidden key's -inf stays one
-                            const float kf = fmaxf(a.scale_log2 * psc.x, 1e-37f), add = log2f(rest);
-                            ps.k[lane] = make_float2(kf, kf);
-                            ps.add[lane] = make_float2(add, add);
-                            ps.mul[lane] = 1.f / rest;
-                            ps.v2[lane] = h | h << 16;
-                            // P * rest must stay in fp16: P <= 2^8, so rest < 2^7
-                            if (!(psc.y < 32768.f)) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
-                        } else {
-                            ps.k[lane] = make_float2(a.scale_log2, a.scale_log2);  // add and mul: the converters
-                        }
+                if (kInt8 && tt >= gm.n_pre) {  // new tokens (add and mul: the converters)
+                    PageScales &ps = s_page[s];
+                    if (lane < 8) ps.k[lane] = make_float2(a.scale_log2, a.scale_log2);
+                    if (lane == 0) {
+                        ps.drop = j > 0 ? __uint_as_float((uint32_t)(127 - lift) << 23) : 1.f;
+                        s_slot[k % kItemRing].lift = 0;
                     }
+                    lift = 0;
                     __syncwarp();  // before lane 0 arrives on the stage's barriers
                 }
                 if (kCodes && tt < gm.n_pre) {
@@ -874,6 +875,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (full) {
                         tma_load_4d(kt + C::kOffFp8Page(lane), &kpmap, &bars.k_full[s], 0, 0, gm.g, pg);
                         tma_load_4d(vt + C::kOffFp8Page(lane), &vpmap, &bars.v_full[s], 0, 0, gm.g, pg);
+                    }
+                    if (kInt8) {  // with the copies on their way (8 x 512 over 16384 1524 us before them, 1428 here)
+                        PageScales &ps = s_page[s];
+                        const uint32_t y = __float_as_uint(psc.y);
+                        const int e = (int)((y >> 23) & 0xFFu) - 127, was = lift;  // lanes 8 .. 31: -127
+                        lift = max(0, -24 - max(__reduce_max_sync(0xffffffffu, e), kVScaleMinExp));
+                        if (j > 0) lift = min(lift, was);
+                        const bool falls = j > 0 && lift < was;
+                        if (lane < 8) {
+                            const int e2 = min(max(e, -24), 8);
+                            const bool live = e >= kVScaleMinExp;  // else the values are 0 by 2^e' alone
+                            const float rest = live ? __uint_as_float(y + ((uint32_t)(lift - e2) << 23)) : 1.f;
+                            const float p2 = live ? __uint_as_float((uint32_t)(127 + e2) << 23) : 0.f;
+                            // never 0, so that a hidden key's -inf stays one
+                            const float kf = fmaxf(a.scale_log2 * psc.x, 1e-37f);
+                            // the approximations are off by some 2^-21, where P keeps 2^-11
+                            const float add = __log2f(rest), mul = __fdividef(1.f, rest);
+                            ps.k[lane] = make_float2(kf, kf);
+                            ps.add[lane] = make_float2(add, add);
+                            ps.mul[lane] = falls ? INFINITY : mul;
+                            ps.mul_again[lane] = mul;
+                            ps.v2[lane] = pack_f16x2(p2, p2);
+                            // P * rest must stay in fp16: P <= 2^8, so rest < 2^7
+                            if (!(psc.y < 32768.f)) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
+                        }
+                        if (lane == 0) {
+                            ps.drop = falls ? __uint_as_float((uint32_t)(127 + lift - was) << 23) : 1.f;
+                            if (j == gm.n_kv - 1) s_slot[k % kItemRing].lift = lift;
+                        }
                     }
                     for (uint32_t om = other_mask; om; om &= om - 1) {
                         const int pp = __ffs(om) - 1;
@@ -1193,7 +1223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) s_vscale[st * 4 + q] = kexp;
                 if (kInt8 && lane < 2) {
                     s_page[st].add[2 * q + lane] = make_float2((float)kexp, (float)kexp);
-                    s_page[st].mul[2 * q + lane] = sc;
+                    s_page[st].mul[2 * q + lane] = s_page[st].drop == 1.f ? sc : INFINITY;
+                    s_page[st].mul_again[2 * q + lane] = sc;
                 }
                 fence_proxy_async_smem();  // the P.V MMA reads these through the async proxy
                 __syncwarp();
@@ -1333,7 +1364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 sc2 = make_float2(sc, sc);
                 // writes P against the running max m_used; returns the row's sum of P * 2^-k
                 const bool f8 = kFp8 && fold8 && tt < gm.n_pre;  // warp-uniform
-                auto emit = [&]() {
+                auto emit = [&](bool again) {
                     const float neg0 = m_used == -INFINITY ? 0.f : -m_used;
                     float tl = 0.f;
 #pragma unroll
@@ -1351,7 +1382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const PageScales &ps = s_page[vst];
                             const float4 k2 = *reinterpret_cast<const float4 *>(ps.k + 2 * ch);
                             const float4 a2 = *reinterpret_cast<const float4 *>(ps.add + 2 * ch);
-                            pmul = *reinterpret_cast<const float2 *>(ps.mul + 2 * ch);
+                            pmul = *reinterpret_cast<const float2 *>((again ? ps.mul_again : ps.mul) + 2 * ch);
                             pk[0] = make_float2(k2.x, k2.y), pk[1] = make_float2(k2.z, k2.w);
                             pn[0] = fadd2(make_float2(neg0, neg0), make_float2(a2.x, a2.y));
                             pn[1] = fadd2(make_float2(neg0, neg0), make_float2(a2.z, a2.w));
@@ -1386,7 +1417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return tl;
                 };
-                float tl = emit();
+                float tl = emit(false);
                 if (pfail) {
                     ok = false;
                     break;
@@ -1395,6 +1426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // every P * 2^-k at most 2^8 (so P fits fp16) unless the row's sum passes it
                     const bool need = !(tl <= kPSumLimit) || m_used == -INFINITY;
                     if (__any_sync(0xffffffffu, need)) {
+                        const float drop = kInt8 ? s_page[vst].drop : 1.f;
                         // the row max, a rescale of O and l, and P again (the P written above is
                         // overwritten before p_full; rows that need nothing write the same P)
                         const float mt = kInt8 ? row_max() : row_max() * sc;
@@ -1406,11 +1438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc::fence_after_sync();
                         const float mn = fmaxf(m_used, mt);
-                        const float alpha = need && mn > m_used ? fast_exp2(m_used - mn) : 1.f;
+                        float alpha = need && mn > m_used ? fast_exp2(m_used - mn) : 1.f;
                         if (need && mn > m_used) {
                             l *= alpha;
                             m_used = mn;
                         }
+                        if (kInt8) alpha *= drop;
 #pragma unroll
                         for (int c = 0; c < D / 32; ++c) {
                             uint32_t o[32];
@@ -1421,7 +1454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc::st_32x32b_x32(tO + c * 32, o);
                         }
                         tc::wait_st();  // the first P stores land before the second ones
-                        tl = emit();
+                        tl = emit(true);
                     }
                 }
                 l += tl;
@@ -1458,7 +1491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (valid) a.part_ml[pr] = make_float2(m_used, l);
+                // O is lifted: with the maximum lower and the sum higher by as much, the merge's weights are right
+                const int up = s_slot[k % kItemRing].lift;
+                if (valid) a.part_ml[pr] = make_float2(m_used - (float)up, l * __uint_as_float((uint32_t)(127 + up) << 23));
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.o_free[x]);
