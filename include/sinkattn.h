@@ -331,7 +331,8 @@ int sinkattn_append_kv_fp8(const void *k, const void *v, const float *k_scale,
  *   - k_pages, v_pages: int8 [num_pages, Hkv, 16, D] (the same HND layout), codes in -127 .. 127;
  *   - kv_scales: fp32 [num_pages, Hkv, 2], 8-byte aligned: of K and of V, one pair beside the
  *     other (a page's pair is one read).  Value of an element = scale * code.  Scales must be
- *     finite and not negative; those of a page that holds no tokens are not used.
+ *     finite and not negative (for the attention below 2^100, i.e. values below 2^107); those of a
+ *     page that holds no tokens are not used.
  * An element is off by at most half its page's scale per rounding, i.e. 1/254 of the largest
  * magnitude among the page's 16 x D rows of that head.
  *

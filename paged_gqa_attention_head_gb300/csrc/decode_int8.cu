@@ -64,6 +64,9 @@ struct Int8Cfg {
 
 constexpr float kPShift = 7.f;   // P = 2^(s - m + kPShift)
 constexpr float kMaxSlack = 8.f; // the running maximum moves when a score passes it by more
+// A state leaves a warp with its sums over 2^(kPShift + kMaxSlack), the largest P, so that up to 2^17
+// values of 2^107 (scales of 2^100) stay finite in it and in the merge.
+constexpr float kStateDown = 1.f / 32768.f;
 
 template <int D, int NH>
 int int8_smem_bytes(int B) {
@@ -566,12 +569,15 @@ __global__ void __launch_bounds__(Int8Cfg<D, NH>::kThreads, NH == 2 && D == 128 
                         if (a.lse && gr == 0) a.lse[(int64_t)cur.b * a.Hq + h] = lse2 * kLn2;
                     } else {
                         const int64_t row = slot * a.G + hc;
+                        constexpr float kUp = kUp24 * kStateDown;
                         float *pa = a.part_acc + row * D + 2 * gr;
 #pragma unroll
                         for (int mt = 0; mt < C::kMTiles; ++mt)
                             *reinterpret_cast<float2 *>(pa + 16 * mt) =
-                                make_float2(acc[mt][nt][e] * kUp24 * v_top, acc[mt][nt][2 + e] * kUp24 * v_top);
-                        if (gr == 0) *reinterpret_cast<float2 *>(a.part_ml + row * 2) = make_float2(m, L);
+                                make_float2(acc[mt][nt][e] * kUp * v_top, acc[mt][nt][2 + e] * kUp * v_top);
+                        if (gr == 0)
+                            *reinterpret_cast<float2 *>(a.part_ml + row * 2) =
+                                make_float2(m + kPShift + kMaxSlack, L * kStateDown);
                     }
                 }
         }
