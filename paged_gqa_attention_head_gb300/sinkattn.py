@@ -642,6 +642,14 @@ def _call(index: int, what: str, *args) -> None:
         raise SinkAttnError(rc, what)
 
 
+def _captures(index: int) -> bool:
+    """Whether the current stream of the device `index` is being captured."""
+    if _current_device() == index:
+        return _capturing()
+    with torch.cuda.device(index):
+        return _capturing()
+
+
 def _status_buffer(index: int) -> Optional[torch.Tensor]:
     """The status word that the calls below share when they are given no workspace_buf (bits are OR-ed
     in, so streams and graphs may share it): workspace(256, device, "append"), read by
@@ -651,7 +659,7 @@ def _status_buffer(index: int) -> Optional[torch.Tensor]:
         key = _append_keys[index] = (torch.device("cuda", index), "append")
     ws = _workspaces.get(key)
     if ws is None:
-        if _capturing():
+        if _captures(index):
             warnings.warn("a captured call will not report its status: call default_status() once before the capture",
                           RuntimeWarning, stacklevel=3)
             return None
@@ -690,7 +698,7 @@ def _stream_workspace(nbytes: int, index: int, stream: int, tag: str, header: bo
     between them.  While the stream is captured the call gets a buffer of its own in the graph's
     memory, whose header, if the call reads it, the graph clears at each replay; so no two graphs, and
     no graph and an eager call, share one."""
-    if _capturing():
+    if _captures(index):
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", index))
         if header:
             _call(index, "sinkattn_workspace_init", ws.data_ptr(), ws.numel(), stream)

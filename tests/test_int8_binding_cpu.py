@@ -13,6 +13,7 @@ def host_scratch(sa, monkeypatch):
     real = torch.zeros
     monkeypatch.setattr(sa.torch, "zeros", lambda *size, dtype=None, device=None: real(*size, dtype=dtype))
     monkeypatch.setattr(sa, "_capturing", lambda: False)
+    monkeypatch.setattr(sa, "_current_device", lambda: 0)
     monkeypatch.setattr(sa, "_scratch", sa._Scratch())  # nothing of it stays for tests on a GPU
     return sa
 
@@ -73,3 +74,29 @@ def test_the_shared_status_word_during_a_capture(host_scratch, monkeypatch):
         assert sa._status_buffer(0) is None
     word = sa._workspaces[torch.device("cuda", 0), "append"] = torch.zeros(256, dtype=torch.uint8)
     assert sa._status_buffer(0) is word
+
+
+def test_a_capture_on_another_device_than_the_current_one(host_scratch, monkeypatch):
+    """It is the tensors' device whose stream is asked, not the current one's."""
+    sa, current, calls = host_scratch, [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    real = torch.empty
+    monkeypatch.setattr(sa.torch, "empty", lambda *size, dtype=None, device=None: real(*size, dtype=dtype))
+    monkeypatch.setattr(sa.torch.cuda, "device", Device)
+    monkeypatch.setattr(sa, "_current_device", lambda: current[0])
+    monkeypatch.setattr(sa, "_capturing", lambda: current[0] == 1)
+    monkeypatch.setattr(sa, "_call", lambda index, what, *args: calls.append((index, what)))
+    eager = [sa._stream_workspace(1000, 0, 5, "prefill") for _ in range(2)]
+    captured = [sa._stream_workspace(1000, 1, 5, "prefill") for _ in range(2)]
+    assert eager[0] is eager[1] and captured[0] is not captured[1]
+    assert calls == [(1, "sinkattn_workspace_init")] * 2 and current == [0]
