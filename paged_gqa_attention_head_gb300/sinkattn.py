@@ -713,6 +713,19 @@ def _stream_workspace(nbytes: int, index: int, stream: int, tag: str, header: bo
     return ws
 
 
+def _workspace_args(ws: Optional[torch.Tensor], index: int) -> tuple:
+    """Address and bytes of a workspace; (None, 0) without one."""
+    if ws is None:
+        return None, 0
+    if not isinstance(ws, _Tensor):
+        raise TypeError("workspace_buf must be a tensor")
+    if ws.get_device() != index:
+        raise ValueError(f"workspace_buf is on {ws.device}, expected cuda:{index}")
+    if not ws.is_contiguous():
+        raise ValueError("workspace_buf must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _need_int8_cache(k_pages, v_pages, kv_scales, index: int) -> tuple:
     _need_dense(k_pages, "k_pages", torch.int8, index, 4)
     _need_dense(v_pages, "v_pages", torch.int8, index, 4)
@@ -742,11 +755,10 @@ def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, k
     n, columns = block_table.shape
     if cu_seqlens.shape[0] != n + 1 or start_pos.shape[0] != n:
         raise ValueError("block_table / start_pos rows must equal the sequences of cu_seqlens")
-    ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
+    ws, nbytes = _workspace_args(workspace_buf if workspace_buf is not None else _status_buffer(dev), dev)
     _call(dev, "sinkattn_append_kv_int8", k.data_ptr(), ks, v.data_ptr(), vs, cu_seqlens.data_ptr(), T,
           block_table.data_ptr(), start_pos.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
-          _desc_ref(n, Hkv, Hkv, D, pages, columns, 0, 0, 0), None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel(), _raw_stream(dev))
+          _desc_ref(n, Hkv, Hkv, D, pages, columns, 0, 0, 0), ws, nbytes, _raw_stream(dev))
     return k_pages, v_pages, kv_scales
 
 
@@ -833,7 +845,7 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
         status = _status_buffer(dev)
     _call(dev, "sinkattn_decode_int8_report", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
           block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), _ptr(status), stream)
+          None if lse is None else lse.data_ptr(), desc, *_workspace_args(ws, dev), _ptr(status), stream)
     return out, lse
 
 
@@ -868,7 +880,7 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
     _call(dev, "sinkattn_prefill_int8_report", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
           k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), prefix_block_table.data_ptr(),
           prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), desc, ws.data_ptr(), ws.numel(), _ptr(status), stream)
+          None if lse is None else lse.data_ptr(), desc, *_workspace_args(ws, dev), _ptr(status), stream)
     return out, lse
 
 
@@ -933,8 +945,8 @@ def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_we
     q_out = _rows_output(q, q_out, "q_out", dev)
     if k is not None:
         k_out = _rows_output(k, k_out, "k_out", dev)
-    ws = workspace_buf if workspace_buf is not None else _status_buffer(dev)
+    ws, nbytes = _workspace_args(workspace_buf if workspace_buf is not None else _status_buffer(dev), dev)
     _call(dev, "sinkattn_qk_norm_rope", q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, wq, wk, float(eps), pos, T,
           rot, q_out.data_ptr(), None if k is None else k_out.data_ptr(), _desc_ref(0, Hq, Hkv, D, 0, 0, 0, 0, 0),
-          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(dev))
+          ws, nbytes, _raw_stream(dev))
     return q_out, k_out

@@ -100,3 +100,18 @@ def test_a_capture_on_another_device_than_the_current_one(host_scratch, monkeypa
     captured = [sa._stream_workspace(1000, 1, 5, "prefill") for _ in range(2)]
     assert eager[0] is eager[1] and captured[0] is not captured[1]
     assert calls == [(1, "sinkattn_workspace_init")] * 2 and current == [0]
+
+
+def test_workspaces_that_are_not_the_calls_to_write(sa):
+    """On another device, or with elements that do not lie one after the other."""
+    with pytest.raises(ValueError, match="is on cpu"):
+        sa._workspace_args(torch.zeros(256, dtype=torch.uint8), 0)
+    with pytest.raises(TypeError):
+        sa._workspace_args(4096, 0)
+    here = torch.zeros(256, dtype=torch.int32).get_device()
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(512, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            sa._workspace_args(bad, here)
+    ws = torch.zeros(256, dtype=torch.int32)
+    assert sa._workspace_args(ws, here) == (ws.data_ptr(), 1024)
+    assert sa._workspace_args(None, 0) == (None, 0)

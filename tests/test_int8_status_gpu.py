@@ -68,3 +68,19 @@ def test_a_given_workspace_keeps_its_own_bits(sa, cuda_dev):
     sa.decode_int8(*args, workspace_buf=ws)
     assert sa.get_status(ws) == sa.STATUS_BAD_PAGE
     assert sa.default_status() == 0
+
+
+def test_a_workspace_elsewhere_is_refused(sa, cuda_dev):
+    """By every call of the INT8 cache and by the preparation, before anything is launched."""
+    host = torch.zeros(1 << 24, dtype=torch.uint8)
+    decode, _ = _decode(cuda_dev)
+    prefill, _ = _prefill([17], [40])(cuda_dev)
+    q, k, v, cu, kp, vp, sc, bt, lens = prefill
+    with pytest.raises(ValueError, match="workspace_buf is on cpu"):
+        sa.decode_int8(*decode, workspace_buf=host)
+    with pytest.raises(ValueError, match="workspace_buf is on cpu"):
+        sa.prefill_int8(*prefill, workspace_buf=host)
+    with pytest.raises(ValueError, match="workspace_buf is on cpu"):
+        sa.append_kv_int8(k, v, cu, bt, lens, kp, vp, sc, workspace_buf=host)
+    with pytest.raises(ValueError, match="workspace_buf is on cpu"):
+        sa.qk_norm_rope(q, k, workspace_buf=host)
