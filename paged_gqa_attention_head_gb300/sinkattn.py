@@ -669,6 +669,12 @@ def _status_buffer(index: int) -> Optional[torch.Tensor]:
     return ws
 
 
+def _status_args(index: int) -> tuple:
+    """Address and bytes of the shared status word; (None, 0) without one."""
+    ws = _status_buffer(index)
+    return (None, 0) if ws is None else (ws.data_ptr(), 256)
+
+
 def default_status(device=None) -> int:
     """Read and clear the status bits (STATUS_*) of the calls on a CUDA device (default: the current
     one) that were given no workspace_buf: append_kv, append_kv_fp8, append_kv_int8, qk_norm_rope,
@@ -713,10 +719,8 @@ def _stream_workspace(nbytes: int, index: int, stream: int, tag: str, header: bo
     return ws
 
 
-def _workspace_args(ws: Optional[torch.Tensor], index: int) -> tuple:
-    """Address and bytes of a workspace; (None, 0) without one."""
-    if ws is None:
-        return None, 0
+def _workspace_args(ws: torch.Tensor, index: int) -> tuple:
+    """Address and bytes of a workspace that the caller gave."""
     if not isinstance(ws, _Tensor):
         raise TypeError("workspace_buf must be a tensor")
     if ws.get_device() != index:
@@ -755,7 +759,7 @@ def append_kv_int8(k, v, cu_seqlens, block_table, start_pos, k_pages, v_pages, k
     n, columns = block_table.shape
     if cu_seqlens.shape[0] != n + 1 or start_pos.shape[0] != n:
         raise ValueError("block_table / start_pos rows must equal the sequences of cu_seqlens")
-    ws, nbytes = _workspace_args(workspace_buf if workspace_buf is not None else _status_buffer(dev), dev)
+    ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
     _call(dev, "sinkattn_append_kv_int8", k.data_ptr(), ks, v.data_ptr(), vs, cu_seqlens.data_ptr(), T,
           block_table.data_ptr(), start_pos.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
           _desc_ref(n, Hkv, Hkv, D, pages, columns, 0, 0, 0), ws, nbytes, _raw_stream(dev))
@@ -838,14 +842,16 @@ def decode_int8(q, k_pages, v_pages, kv_scales, block_table, seq_lens, sinks=Non
     sk = _need_sinks(sinks, Hq, dev)
     out, lse = _attention_outputs(q, out, lse, return_lse, dev)
     key = (B, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
-    desc, stream, ws, status = _desc_ref(*key), _raw_stream(dev), workspace_buf, None
-    if ws is None:
+    desc, stream = _desc_ref(*key), _raw_stream(dev)
+    if workspace_buf is None:
         ws = _stream_workspace(_int8_size("sinkattn_decode_int8_workspace_size", dev, desc, key), dev, stream, "decode",
                                header=False)
-        status = _status_buffer(dev)
+        at, nbytes, (status, _) = ws.data_ptr(), ws.numel(), _status_args(dev)
+    else:
+        (at, nbytes), status = _workspace_args(workspace_buf, dev), None
     _call(dev, "sinkattn_decode_int8_report", q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(),
           block_table.data_ptr(), seq_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), desc, *_workspace_args(ws, dev), _ptr(status), stream)
+          None if lse is None else lse.data_ptr(), desc, at, nbytes, status, stream)
     return out, lse
 
 
@@ -872,15 +878,17 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
     sk = _need_sinks(sinks, Hq, dev)
     out, lse = _attention_outputs(q, out, lse, return_lse, dev)
     key = (n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
-    desc, stream, ws, status = _desc_ref(*key), _raw_stream(dev), workspace_buf, None
-    if ws is None:
+    desc, stream = _desc_ref(*key), _raw_stream(dev)
+    if workspace_buf is None:
         ws = _stream_workspace(_int8_size("sinkattn_prefill_int8_workspace_size", dev, desc, key, T), dev, stream,
                                "prefill")
-        status = _status_buffer(dev)
+        at, nbytes, (status, _) = ws.data_ptr(), ws.numel(), _status_args(dev)
+    else:
+        (at, nbytes), status = _workspace_args(workspace_buf, dev), None
     _call(dev, "sinkattn_prefill_int8_report", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
           k_pages.data_ptr(), v_pages.data_ptr(), kv_scales.data_ptr(), prefix_block_table.data_ptr(),
           prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-          None if lse is None else lse.data_ptr(), desc, *_workspace_args(ws, dev), _ptr(status), stream)
+          None if lse is None else lse.data_ptr(), desc, at, nbytes, status, stream)
     return out, lse
 
 
@@ -945,7 +953,7 @@ def qk_norm_rope(q, k, positions=None, rotary: Optional[RotaryDesc] = None, q_we
     q_out = _rows_output(q, q_out, "q_out", dev)
     if k is not None:
         k_out = _rows_output(k, k_out, "k_out", dev)
-    ws, nbytes = _workspace_args(workspace_buf if workspace_buf is not None else _status_buffer(dev), dev)
+    ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
     _call(dev, "sinkattn_qk_norm_rope", q.data_ptr(), qs, None if k is None else k.data_ptr(), ks, wq, wk, float(eps), pos, T,
           rot, q_out.data_ptr(), None if k is None else k_out.data_ptr(), _desc_ref(0, Hq, Hkv, D, 0, 0, 0, 0, 0),
           ws, nbytes, _raw_stream(dev))

@@ -114,4 +114,3 @@ def test_workspaces_that_are_not_the_calls_to_write(sa):
             sa._workspace_args(bad, here)
     ws = torch.zeros(256, dtype=torch.int32)
     assert sa._workspace_args(ws, here) == (ws.data_ptr(), 1024)
-    assert sa._workspace_args(None, 0) == (None, 0)
