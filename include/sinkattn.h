@@ -129,7 +129,7 @@ typedef struct sinkattn_paged_desc {
  * calls run at once on one stream, and the CTAs of each land on SMs of their own.  The decode
  * must read nothing the prefill writes (the prefill writes only its out and lse).  The merge
  * after the split-KV decode, and every later kernel on the stream, still wait for both.
- * The one-launch sliding-window decode and the FP8 decode ignore SINKATTN_FLAG_START_EARLY. */
+ * The one-launch sliding-window decode and the FP8 and INT8 decodes ignore SINKATTN_FLAG_START_EARLY. */
 #define SINKATTN_FLAG_LAUNCH_NEXT_EARLY 0x1
 #define SINKATTN_FLAG_START_EARLY 0x2
 
@@ -333,8 +333,8 @@ int sinkattn_append_kv_fp8(const void *k, const void *v, const float *k_scale,
  *     other (a page's pair is one read).  Value of an element = scale * code.  Scales must be
  *     finite and not negative (for the attention below 2^100, i.e. values below 2^107); those of a
  *     page that holds no tokens are not used.
- * An element is off by at most half its page's scale per rounding, i.e. 1/254 of the largest
- * magnitude among the page's 16 x D rows of that head.
+ * An element is off by at most half its page's scale per rounding, i.e. (1 + 2^-7) / 254 of the
+ * largest magnitude among the page's 16 x D values of that head (the scale is rounded up).
  *
  * sinkattn_append_kv_int8: new bf16 rows into the slots that sinkattn_append_kv would write.
  * For the new rows of one (page, head), with amax their largest finite magnitude:
@@ -362,11 +362,12 @@ int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, 
  * window and status as for sinkattn_decode).  Workspace: sinkattn_decode_int8_workspace_size
  * bytes, 256-byte aligned, its 256-byte header zero before the first call (every call leaves it so
  * but for status bits); calls that share one must be ordered on the GPU.
- * Codes enter the products exactly, scales multiply fp32 sums; q is taken in fp16 times a power
- * of two of its (sequence, KV head): an entry keeps its 8 bits unless it is more than 2^28 times
- * smaller than the largest of its group.  The probabilities are rounded to fp16 (relative
- * 2^-11 each at most), as in sinkattn_decode_fp8.  (With a sliding window it runs the split-KV
- * kernel too, over the visible pages.) */
+ * Codes enter the products exactly; K scales multiply fp32 scores; a probability is taken times its
+ * page's V scale, relative to a power of two of the largest one met, and the product is rounded once
+ * to fp16 (relative 2^-11 at most, as in sinkattn_decode_fp8; from 2^20 below the largest product on,
+ * 2^-31 of that).  q is taken in fp16 times a power of two of its (sequence, KV head): an entry keeps
+ * its 8 bits unless it is more than 2^28 times smaller than the largest of its group.  (With a
+ * sliding window it runs the split-KV kernel too, over the visible pages.) */
 int sinkattn_decode_int8_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
 
 int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages, const float *kv_scales,

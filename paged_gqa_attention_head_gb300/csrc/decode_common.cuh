@@ -1,7 +1,7 @@
 // Pieces of the split-KV decode plan shared by the bf16, FP8 and INT8 decode kernels:
 // the per-sequence page counts and their prefix sum (the list of (sequence, KV head,
 // page) units every warp takes an equal contiguous range of) and the cursor that
-// walks that list; and the shared-memory layout and MMA of the one-byte caches.
+// walks that list; and the MMA of the one-byte caches.
 #pragma once
 
 #include "internal.h"
@@ -79,31 +79,6 @@ __device__ void scan_pages(const DecodeArgs &a, int *s_prefix, int *s_len, int *
 }
 
 // ---------------------------------------------------------------- one-byte caches (FP8, INT8)
-// Byte offset of byte c of token row r inside a page buffer written by TMA with
-// this head_dim's swizzle (64-byte swizzle: 16-byte chunk bits 4-5 XOR address bits
-// 7-8; 128-byte swizzle: bits 4-6 XOR bits 7-9; buffers 1024-byte aligned).
-template <int D>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-    if (D == 64) return (uint32_t)(r * 64 + ((((c >> 4) ^ (r >> 1)) & 3) << 4) + (c & 15));
-    return (uint32_t)(r * 128 + ((((c >> 4) ^ r) & 7) << 4) + (c & 15));
-}
-
-// Physical token row of MMA token index k (0..15).  For head_dim 64 the order
-// 0,3,1,2,4,7,5,6 (and +8) puts the rows one load instruction touches into distinct
-// banks under the 64-byte swizzle; for 128 the identity already does.
-template <int D>
-__device__ __forceinline__ int tok_row(int k) {
-    if (D == 64) return (int)((0x65742130u >> (4 * (k & 7))) & 15u) + (k & 8);
-    return k;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
-    return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2_times(uint32_t v, float mul) {
-    return pack_f16x2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
-}
-
 // D(16x8, f32) += A(16x16, f16, row) * B(16x8, f16, col)
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {

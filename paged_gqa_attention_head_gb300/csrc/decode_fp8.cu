@@ -64,6 +64,28 @@ int fp8_smem_bytes(int B) {
            C::kWarps * C::kStages * (8 + 8 * C::kPPU) + (3 * B + 1) * 4;
 }
 
+// Byte offset of byte c of token row r inside a page buffer written by TMA with
+// this head_dim's swizzle (64-byte swizzle: 16-byte chunk bits 4-5 XOR address bits
+// 7-8; 128-byte swizzle: bits 4-6 XOR bits 7-9; buffers 1024-byte aligned).
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+    if (D == 64) return (uint32_t)(r * 64 + ((((c >> 4) ^ (r >> 1)) & 3) << 4) + (c & 15));
+    return (uint32_t)(r * 128 + ((((c >> 4) ^ r) & 7) << 4) + (c & 15));
+}
+
+// Physical token row of MMA token index k (0..15).  For head_dim 64 the order
+// 0,3,1,2,4,7,5,6 (and +8) puts the rows one load instruction touches into distinct
+// banks under the 64-byte swizzle; for 128 the identity already does.
+template <int D>
+__device__ __forceinline__ int tok_row(int k) {
+    if (D == 64) return (int)((0x65742130u >> (4 * (k & 7))) & 15u) + (k & 8);
+    return k;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
+    return pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
 // NH: 8-head tiles of the query group (1 for G <= 8, 2 for G = 16).  The second bound is the
 // CTAs an SM each variant is built for (its register budget; the occupancy each already had):
 // left to itself the compiler held the two-tile head_dim-128 variant near 210 registers, and

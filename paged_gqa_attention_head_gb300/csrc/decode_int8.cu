@@ -12,7 +12,9 @@
 //     128 comes off in the MMAs' accumulators: the K products start from -128 2^-24 sum(q), and
 //     what the P of a unit add too much is one MMA of a constant -128 2^-24 against them, added to
 //     O^T.  (As values - the offset form under the exponent of 1024, less 1152 - a page cost 27
-//     instructions more at head_dim 64.)  The detour through 128 costs the fp32 sums under 2 bits;
+//     instructions more at head_dim 64.)  The detour through 128 makes the fp32 sums' rounding that of
+//     sums of codes of 128 to 255: it costs a channel of full range a bit, one whose codes are a few
+//     units beside an outlier channel's up to seven of its 24, where P keeps 11;
 //   * K: a page's scale multiplies its 16 scores, together with the softmax scale;
 //   * V: P of a page is taken times s / 2^E, with 2^E the power of two above the largest V scale
 //     the warp has met in this (sequence, head): one rounding to f16, and O^T is summed in the
@@ -20,7 +22,8 @@
 //     an exact power of two.  (Taking each page's product apart and adding it with an FMA per
 //     element rounds no scale at all, and cost 64 FMAs a page at head_dim 128 and 16 heads,
 //     a tenth of the instructions.  Rounding P times the scale is as exact as rounding P for
-//     every page within 2^22 of the largest, and beyond that is off by 2^-33 of the largest.)
+//     products within 2^20 of the largest, and beyond that is off by 2^-31 of it: the largest is
+//     2^6 or more, f16 subnormals end at 2^-24.)
 //   * q times a power of two per (sequence, KV head) that puts its largest entry at 2^14 is exact
 //     in f16 whatever its size; the scores take the power back;
 //   * no code is NaN or infinite: slots past a sequence's end need no clearing, P is 0 there.
@@ -103,6 +106,10 @@ __device__ __forceinline__ uint32_t sub_even(uint32_t w) {
     return r;
 }
 __device__ __forceinline__ uint32_t sub_odd(uint32_t w) { return sub_even(w >> 8); }
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2_times(uint32_t v, float mul) {
+    return pack_f16x2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
+}
+
 // D = A B + C with C's columns c0 and c1 in every row.
 __device__ __forceinline__ void mma_f16_16816_from(float (&d)[4], float c0, float c1, uint32_t a0, uint32_t a1,
                                                    uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
