@@ -516,7 +516,8 @@ int sinkattn_decode_noalloc(const void *q, const void *k_pages, const void *v_pa
  * softmax's running max and denominator start from the sink.  The P.V product takes
  * P and V in fp16 (11-bit significand, fp32 accumulation): each V tile is scaled by a
  * power of two into fp16 range, which covers |v| < 2^22; larger or non-finite values
- * set SINKATTN_STATUS_VALUE_RANGE (their outputs are then unspecified).
+ * set SINKATTN_STATUS_VALUE_RANGE (the outputs of their request are then unspecified).
+ * Rows of q, k and v behind the last request may hold anything.
  *
  * q:          bf16 [T, Hq, D]   (T = total_tokens = cu_seqlens[num_seqs])
  * k, v:       bf16 [T, Hkv, D]  (the new tokens' keys and values)

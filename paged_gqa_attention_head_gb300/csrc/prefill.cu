@@ -1175,6 +1175,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint4 *vt = reinterpret_cast<uint4 *>(sV + st * C::kKVBytes + q * 4096) + lane;
                 // this lane's vectors: 8 per 64-column half, 512 bytes apart
+                // rows past the request's end are another's, or padding: their P is 0, but 0 times what
+                // may stand there (NaN, infinities) is not, so they become zeros; e as in the loops below
+                // (with the rarer one there not unrolled, the code stays small enough that the long bf16
+                // prefix keeps its 1254 us; 1275 with it unrolled by two)
+                const int rows = gm.L - ((kFrom ? gm.t0 + j : j) - gm.n_pre) * kBN - 32 * q;
+#pragma unroll 1
+                for (int e = max(0, rows - (lane >> 3) + 3) >> 2; e < 8; ++e)
+                    for (int hf = 0; hf < C::kHalves; ++hf) vt[hf * 1024 + e * 32] = make_uint4(0, 0, 0, 0);
                 uint32_t mx = 0;  // largest |v| per 16-bit half, as bf16 bits (monotonic in |v|)
 #pragma unroll 1
                 for (int hf = 0; hf < C::kHalves; ++hf) {
@@ -1208,7 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *pw = w;
                         }
                     } else {
-#pragma unroll 2
+#pragma unroll 1
                         for (int e = 0; e < 8; ++e) {
                             uint4 *pw = vt + hf * 1024 + e * 32;
                             uint4 w = *pw;
