@@ -454,7 +454,8 @@ typedef struct sinkattn_rotary_desc {
  *             and a multiple of 8; k alike with Hkv), e.g. parts of a fused projection's rows.
  *             Either may be NULL together with its output.
  * q_weight, k_weight: fp32 [D] or NULL (no norm), 16-byte aligned.  The sum of squares is taken
- *             in fp32: rows with entries of 2^60 or more overflow it.
+ *             in fp32: rows with entries of 2^60 or more overflow it, and with eps = 0 rows whose
+ *             entries all lie below 2^-62 count as zeros.
  * positions:  int32 [total_tokens], each below 2^24; a negative one marks padding: the token's
  *             output rows are left as they were.  Not read without a rotation.
  * rotary:     host pointer, read during the call; NULL: no rotation
