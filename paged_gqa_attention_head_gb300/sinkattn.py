@@ -664,8 +664,11 @@ def _status_buffer(index: int) -> Optional[torch.Tensor]:
                           RuntimeWarning, stacklevel=3)
             return None
         with _status_lock:
-            ws = workspace(256, *key)
-        torch.cuda.current_stream(index).synchronize()  # zero before another stream's call sets a bit
+            ws = _workspaces.get(key)
+            if ws is None:  # zero before a call on another stream can set a bit
+                ws = torch.zeros(256, dtype=torch.uint8, device=key[0])
+                torch.cuda.current_stream(index).synchronize()
+                _workspaces[key] = ws
     return ws
 
 

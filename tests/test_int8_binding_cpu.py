@@ -114,3 +114,25 @@ def test_workspaces_that_are_not_the_calls_to_write(sa):
             sa._workspace_args(bad, here)
     ws = torch.zeros(256, dtype=torch.int32)
     assert sa._workspace_args(ws, here) == (ws.data_ptr(), 1024)
+
+
+def test_the_status_word_is_zero_before_others_see_it(host_scratch, monkeypatch):
+    """Made once, whichever thread comes first, and published after its memory is cleared."""
+    sa, seen, made = host_scratch, [], []
+    words = {}
+
+    class Stream:
+        def synchronize(self):
+            seen.append(dict(words))
+
+    fake = sa.torch.zeros
+    monkeypatch.setattr(sa, "_workspaces", words)
+    monkeypatch.setattr(sa.torch, "zeros", lambda *a, **k: made.append(1) or fake(*a, **k))
+    monkeypatch.setattr(sa.torch.cuda, "current_stream", lambda index: Stream())
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(sa._status_buffer(0))) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert seen == [{}] and len(made) == 1 and all(w is got[0] for w in got) and len(got) == 8
