@@ -1648,12 +1648,12 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillArgs a)
 
 // An item is (128-row query block, pair of heads of one KV head).  Where they leave half the SMs or more
 // without work each is split over as many SMs as there are for it: one 17-token chunk over prefixes of
-// 1003 / 4000 / 16384 tokens takes 20.5 / 30.5 / 70 us with 64/8 heads of 64 (4 parts; unsplit
-// 26 / 65 / 219) and 18.4 / 24 / 45 us with 16/8 heads of 128 (19 parts; 34 / 96 / 332).  More parts
-// than SMs cost up to a wave (6 parts for 32 items: 85 us of 70), and with more items the SMs are busy and the
-// parts' outputs are extra traffic (128 items: 4 parts 98 us, unsplit 71).  Up to 3 prefix tiles - of
-// the block table's width or the window, all that the host knows - the merge takes what the split
-// gains (250 tokens: 16.4 us, unsplit 15.9).
+// 1003 / 4000 / 16384 tokens takes 19.4 / 29 / 66 us with 64/8 heads of 64 (4 parts; unsplit
+// 24 / 61 / 207) and 19.2 / 22 / 35 us with 16/8 heads of 128 (19 parts; 34 / 93 / 325).  More parts
+// than SMs cost up to a wave (6 parts for 32 items: 85 us where 4 took 70), and with more items the SMs
+// are busy and the parts' outputs are extra traffic (128 items: 4 parts 98 us, unsplit 71).  Up to 3
+// prefix tiles - of the block table's width or the window, all that the host knows - the merge takes
+// what the split gains (250 tokens: 16.4 us, unsplit 15.9).
 int prefill_int8_splits(int T, int n, int Hq, int G, int max_pages, int window, int sms) {
     const int64_t most = ((int64_t)T + (int64_t)n * (kBM - 1)) / kBM;  // blocks: no more than this, nor rows
     const int64_t items = (most < T ? most : T) * (G >= 2 ? Hq / 2 : Hq);
