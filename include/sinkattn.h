@@ -379,7 +379,9 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
  * prefix pointers, the scales and the prefix lengths are required; prefix lengths may be 0); the
  * new tokens' k, v stay bf16.  Prefix codes enter the products exactly, each page's scales join
  * the softmax in fp32.  P is taken relative to the largest V scale met so far, so small scales keep
- * its bits; below 2^-100 (the append writes none) they count as 0, and V scales of 2^15 or more set
+ * its bits: an output is off by what the roundings of P make of the largest |v| in the tiles of 128
+ * keys that its block of 128 tokens visits (with a sliding window, hidden keys may be among them).
+ * Scales below 2^-100 (the append writes none) count as 0, and V scales of 2^15 or more set
  * SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified).  Other arguments and errors as for
  * sinkattn_prefill.
  * workspace:  at least sinkattn_prefill_workspace_size bytes, as there.  A call with few query
