@@ -21,8 +21,8 @@
  *     token j of sequence b is slot j % page_size of page block_table[b][j / page_size]
  *     block_table: int32 [num_seqs, max_pages_per_seq], row-major
  *
- * Supported: bf16 data (and FP8 E4M3 and INT8 KV caches for decode, append and the prefix of a
- * chunked prefill, see below),
+ * Supported: bf16 data (and FP8 E4M3, INT8 and 4-bit KV caches for decode, append and the prefix of
+ * a chunked prefill, see below),
  * fp32 sinks, head_dim 64 or 128, page_size 16, num_qo_heads / num_kv_heads in
  * {1, 2, 4, 8, 16}.
  *
@@ -74,7 +74,10 @@ typedef enum sinkattn_error {
 #define SINKATTN_STATUS_WAIT_TIMEOUT 0x8u   /* a pipeline wait hit its iteration limit */
 #define SINKATTN_STATUS_VALUE_RANGE 0x10u   /* prefill: a V value with |v| >= 2^22 or not finite;
                                              * INT8 append: a K or V value not finite;
-                                             * INT8 prefill: a V scale of 2^15 or more */
+                                             * INT8 prefill: a V scale of 2^15 or more;
+                                             * 4-bit append: a K or V value not finite;
+                                             * 4-bit prefill: a V scale of 2^18 or more */
+#define SINKATTN_STATUS_NO_PAGES 0x20u      /* page plan: too few free pages for a request */
 
 /* Shapes of a paged KV cache and of the heads that read it. */
 typedef struct sinkattn_paged_desc {
@@ -129,7 +132,7 @@ typedef struct sinkattn_paged_desc {
  * calls run at once on one stream, and the CTAs of each land on SMs of their own.  The decode
  * must read nothing the prefill writes (the prefill writes only its out and lse).  The merge
  * after the split-KV decode, and every later kernel on the stream, still wait for both.
- * The one-launch sliding-window decode and the FP8 and INT8 decodes ignore SINKATTN_FLAG_START_EARLY. */
+ * The one-launch sliding-window decode and the FP8, INT8 and 4-bit decodes ignore SINKATTN_FLAG_START_EARLY. */
 #define SINKATTN_FLAG_LAUNCH_NEXT_EARLY 0x1
 #define SINKATTN_FLAG_START_EARLY 0x2
 
@@ -416,6 +419,126 @@ int sinkattn_prefill_int8_report(const void *q, const void *k, const void *v, co
                                  const int32_t *prefix_lens, const float *sinks, float scale, void *out,
                                  float *lse, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
                                  uint32_t *status, sinkattn_stream_t stream);
+
+/* ----------------------------------------------------------- 4-bit KV cache --
+ * A KV cache of four bits an element and a 16-bit word for every token and 32 channels (4.5 bits an
+ * element in all), whose tokens do not depend on one another: nothing is ever rounded twice.
+ *   - kv_pages: uint8 [num_pages, Hkv, 2 (K, V), 9, D], 16-byte aligned.  In a (page, head)'s K or V
+ *     the first 8 D bytes are codes [D / 32 groups][16 tokens][16 bytes]; eight channels of a token
+ *     are a little-endian 32-bit word, channel c of them at bit 4 (c / 2) + 16 (c % 2).  The last D
+ *     bytes are words [D / 32][16]: a bf16 scale s with four significant bits (its low four bits
+ *     zero) and in their place the code z of the value 0.
+ *   - value = s * (code - z), codes and z in 0 .. 15.  It is a bf16 number (sinkattn_unpack_kv_int4).
+ * Scales must be finite and not negative, for the attention below 2^100; words of slots that hold no
+ * tokens are not used.
+ *
+ * sinkattn_append_kv_int4: new bf16 rows into the slots given (for example by sinkattn_plan_step).
+ * For a token's group of 32 channels, low = min(0, min x) and high = max(0, max x) of its finite
+ * elements:
+ *     s    = the smallest number of four significant bits with 15 s >= high - low (below 2^-100: 0)
+ *     z    = -low / s rounded,  code = min(15, x / s + z rounded), ties to even (both 0 if s is 0)
+ * so a finite element is off by at most s / 2, and 0 stays 0.  Infinities take the codes 15 and 0 and
+ * NaN the value 0, and both set SINKATTN_STATUS_VALUE_RANGE.
+ * k, v:          bf16, row t at k + t * k_row_stride elements (>= Hkv * D, a multiple of 8):
+ *                [Hkv, D] dense, so K and V may lie inside a fused projection's rows
+ * slots:         int64 [total_tokens], page * 16 + place in the page; a negative one marks padding,
+ *                one past the last page sets SINKATTN_STATUS_BAD_PAGE: nothing is written for either.
+ *                Two rows of one call must not have the same slot.
+ * workspace:     optional, as for sinkattn_append_kv
+ * desc:          num_kv_heads, head_dim, num_pages (the other fields are checked, not used) */
+int sinkattn_append_kv_int4(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                            const int64_t *slots, int32_t total_tokens, void *kv_pages,
+                            const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                            sinkattn_stream_t stream);
+
+/* Pages of such a cache as the bf16 values that they stand for, exactly (scales from 2^-100 to 2^100):
+ * k_out, v_out bf16 [count, Hkv, 16, D], the page layout of the bf16 cache.
+ * pages:         int32 [count], the pages wanted, or NULL: pages 0 .. count - 1.  One outside
+ *                [0, num_pages) sets SINKATTN_STATUS_BAD_PAGE and gives zeros.
+ * workspace:     optional, as for sinkattn_append_kv */
+int sinkattn_unpack_kv_int4(const void *kv_pages, const int32_t *pages, int32_t count, void *k_out, void *v_out,
+                            const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                            sinkattn_stream_t stream);
+
+/* The decode over such a cache (q, block_table, seq_lens, sinks, scale, out, lse, descriptor, window
+ * as for sinkattn_decode).  Workspace: sinkattn_decode_int4_workspace_size bytes, 256-byte aligned, its
+ * 256-byte header zero before the first call; calls that share one must be ordered on the GPU.
+ * status: as in sinkattn_decode_int8_report (NULL: bits go to the workspace's header).
+ * Codes and z enter the products exactly, scales of K multiply fp32 scores.  A probability is taken
+ * times its token's V scale of the group, relative to a power of two of the largest V scale met, and
+ * the product is rounded once to fp16 (relative 2^-11 at most; from 2^20 below the largest product on,
+ * 2^-31 of that).  q is taken in fp16 times a power of two of its (sequence, KV head): an entry keeps
+ * its 8 bits unless it is more than 2^22 times smaller than the largest of its group.  (With a
+ * sliding window it runs the split-KV kernel too, over the visible pages.) */
+int sinkattn_decode_int4_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
+
+int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *block_table, const int32_t *seq_lens,
+                         const float *sinks, float scale, void *out, float *lse, const sinkattn_paged_desc *desc,
+                         void *workspace, size_t ws_bytes, uint32_t *status, sinkattn_stream_t stream);
+
+/* Chunked prefill over such a prefix: sinkattn_prefill with the prefix pages in 4 bits (the pages, the
+ * block table and the prefix lengths are required; prefix lengths may be 0); the new tokens' k, v stay
+ * bf16.  It computes what sinkattn_prefill does over a bf16 prefix of the same values: K exactly, V in
+ * fp16 under a power of two for each 32 keys.  V scales of 2^18 or more set
+ * SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified).  status: as for the decode.  Other arguments
+ * and errors as for sinkattn_prefill, the workspace as for sinkattn_prefill_int8 (with
+ * sinkattn_prefill_int4_workspace_size bytes, calls with few query rows split their prefixes). */
+int sinkattn_prefill_int4_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,
+                                         size_t *bytes);
+
+int sinkattn_prefill_int4(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                          int32_t total_tokens, const void *kv_pages, const int32_t *prefix_block_table,
+                          const int32_t *prefix_lens, const float *sinks, float scale, void *out, float *lse,
+                          const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes, uint32_t *status,
+                          sinkattn_stream_t stream);
+
+/* ---------------------------------------------------------- page plan of a step --
+ * What a serving step's calls take, worked out on the device from the requests' lengths and a list of
+ * free pages, so that neither the lengths nor the list need the host (a captured step replays it).
+ * The list is a stack: free_pages[0 .. *num_free - 1], taken from its top.
+ *
+ * sinkattn_plan_step: request i holds seq_lens[i] tokens and brings new_lens[i] more, packed one
+ * request after the other.  With need_i = ceil((seq_lens[i] + new_lens[i]) / 16) - ceil(seq_lens[i] / 16)
+ * and off_i the sum of the needs before it, its k-th new page is
+ * free_pages[*num_free - 1 - (off_i + k)], entered in its row of the block table behind those it has.
+ * A request is served if it needs no page or off_i + need_i <= *num_free, else nothing is taken for
+ * it and SINKATTN_STATUS_NO_PAGES is set.  Neither is a request served whose length is negative, whose
+ * tokens pass its row of the table or whose rows pass max_tokens (SINKATTN_STATUS_BAD_LENGTH).  The
+ * rows of a request that is not served are passed over: position and slot -1, its length as it was.
+ * new_lens, seq_lens: int32 [num_seqs] (a negative new length counts as 0, with the status bit)
+ * block_table:   int32 [num_seqs, max_pages_per_seq], updated in place
+ * free_pages, num_free: int32 [num_pages] and [1]; the list is read alone (what is taken lies behind
+ *                the new *num_free and may be overwritten by a release)
+ * cu_seqlens:    int32 [num_seqs + 1] (written): prefix sums of the new lengths, at most max_tokens
+ * start_pos:     int32 [num_seqs] (written), a copy of seq_lens; or NULL
+ * seq_lens_out, num_free_out: int32 [num_seqs] and [1] (written): the values after the step.  They may
+ *                be seq_lens and num_free themselves
+ * positions, slots: int32 and int64 [max_tokens] (written), 16-byte aligned: each row's position in
+ *                its request and its slot in the cache (page * 16 + position % 16); -1 for rows behind the
+ *                last request.  A page outside [0, num_pages) sets SINKATTN_STATUS_BAD_PAGE, its slots are -1
+ * workspace:     optional (may be NULL): if given (>= 256 bytes), its status word takes the bits
+ * desc:          num_seqs (at most 8192), num_pages, max_pages_per_seq (the other fields are checked,
+ *                not used) */
+int sinkattn_plan_step(const int32_t *new_lens, const int32_t *seq_lens, int32_t *block_table,
+                       const int32_t *free_pages, const int32_t *num_free, int32_t max_tokens, int32_t *cu_seqlens,
+                       int32_t *start_pos, int32_t *seq_lens_out, int32_t *num_free_out, int32_t *positions,
+                       int64_t *slots, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                       sinkattn_stream_t stream);
+
+/* The pages of the requests with done[i] != 0 back to the list, in the opposite order of their taking
+ * (a release of all that one plan took leaves the list as it was), and their lengths to 0:
+ * with n_i = ceil(seq_lens[i] / 16), off_i the sum before it over the requests released and R their sum,
+ * page k of request i goes to free_pages[*num_free + R - 1 - (off_i + k)].
+ * done:          uint8 [num_seqs]
+ * seq_lens_out, num_free_out: as above, possibly seq_lens and num_free themselves
+ * A length that is negative or passes the table sets SINKATTN_STATUS_BAD_LENGTH (no page of it is
+ * released), and so does a list that would pass num_pages entries (the pages past it are dropped); an
+ * entry outside [0, num_pages) is pushed as it is and sets SINKATTN_STATUS_BAD_PAGE.
+ * Other arguments as for sinkattn_plan_step. */
+int sinkattn_release_pages(const uint8_t *done, const int32_t *seq_lens, const int32_t *block_table,
+                           int32_t *free_pages, const int32_t *num_free, int32_t *seq_lens_out, int32_t *num_free_out,
+                           const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                           sinkattn_stream_t stream);
 
 /* ------------------------------------------------- queries and keys before attention --
  * Per-head RMS norm and rotary position embedding of a step's queries and keys in one pass, for

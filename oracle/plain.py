@@ -1,5 +1,5 @@
-"""Plain fp64 forms of the operators around the INT8 KV cache and of the query/key preparation,
-straight from their definitions in include/sinkattn.h: sequence by sequence, page by page, head by
+"""Plain fp64 forms of the operators around the INT8 and the 4-bit KV cache, of the page plan and of
+the query/key preparation, straight from their definitions in include/sinkattn.h: sequence by sequence, page by page, head by
 head, in numpy doubles.  Inputs are torch tensors or numpy arrays; outputs numpy.
 """
 from __future__ import annotations
@@ -111,6 +111,125 @@ def attend_int8(q, k_pages, v_pages, kv_scales, block_table, lens, sinks, scale:
                     lse[t0:t1, h] = np.where(live, m0[:, 0] + np.log(den), -np.inf)
                 vmax[t0:t1, h] = top
     return out, lse, vmax
+
+
+def coded_int4(x):
+    """Codes [..., D], z and s [..., D / 32] of rows x [..., D] in a 4-bit cache."""
+    x = _np(x)
+    x = x.reshape(*x.shape[:-1], -1, 32)
+    fin = np.where(np.isfinite(x), x, 0.0)
+    low, high = np.minimum(fin.min(axis=-1), 0.0), np.maximum(fin.max(axis=-1), 0.0)
+    part, power = np.frexp((high - low) / 15.0)
+    s = np.ldexp(np.ceil(part * 16.0) / 16.0, power)
+    s = np.where(s < 2.0 ** -100, 0.0, s)
+    by = np.where(s > 0, s, 1.0)
+    z = np.where(s > 0, np.rint(-low / by), 0.0)
+    with np.errstate(invalid="ignore"):
+        codes = np.clip(np.rint(x / by[..., None] + z[..., None]), 0, 15)
+    codes = np.where(np.isnan(x), z[..., None], codes)
+    codes = np.where(s[..., None] > 0, codes, 0.0)
+    return codes.reshape(*codes.shape[:-2], -1).astype(np.int64), z.astype(np.int64), s
+
+
+def _word_int4(s, z):
+    """The 16-bit word of a group: the upper half of s as a float, z in its low bits."""
+    return (np.asarray(s, dtype=np.float32).view(np.uint32) >> 16).astype(np.int64) | z
+
+
+def put_int4(rec, tok: int, x) -> None:
+    """Row x [D] into place tok of one (page, head)'s K or V, bytes rec [9, D], in place."""
+    flat, dim = rec.reshape(-1), rec.shape[-1]
+    codes, z, s = coded_int4(x)
+    for c in range(dim):
+        i, e = c % 32 // 8, c % 8
+        bit = 4 * (e // 2) + 16 * (e % 2)
+        at = (c // 32 * PAGE + tok) * 16 + 4 * i + bit // 8
+        flat[at] = (flat[at] & ~(15 << bit % 8)) | (int(codes[c]) << bit % 8)
+    for g, w in enumerate(_word_int4(s, z)):
+        at = 8 * dim + (g * PAGE + tok) * 2
+        flat[at], flat[at + 1] = w & 255, w >> 8
+
+
+def append_kv_int4(k, v, slots, kv_pages) -> np.ndarray:
+    """The bytes of the cache after the append."""
+    out = _np(kv_pages, np.int64).copy()
+    rows = [_np(k), _np(v)]
+    for t, slot in enumerate(_np(slots, np.int64)):
+        if 0 <= slot < out.shape[0] * PAGE:
+            for h in range(out.shape[1]):
+                for i in range(2):
+                    put_int4(out[slot // PAGE, h, i], int(slot % PAGE), rows[i][t, h])
+    return out.astype(np.uint8)
+
+
+def values_int4(kv_pages) -> list:
+    """A 4-bit cache's K and V as numbers, each [num_pages, Hkv, 16, D]."""
+    raw = _np(kv_pages, np.int64)
+    n, h, _, _, dim = raw.shape
+    flat = raw.reshape(n, h, 2, 9 * dim)
+    tok = np.arange(PAGE)
+    out = np.empty((2, n, h, PAGE, dim))
+    for c in range(dim):
+        i, e = c % 32 // 8, c % 8
+        bit = 4 * (e // 2) + 16 * (e % 2)
+        row = c // 32 * PAGE + tok
+        code = (flat[..., row * 16 + 4 * i + bit // 8] >> bit % 8) & 15
+        word = flat[..., 8 * dim + 2 * row] | flat[..., 8 * dim + 2 * row + 1] << 8
+        s = ((word & 0xFFF0) << 16).astype(np.uint32).view(np.float32).astype(np.float64)
+        out[..., c] = np.moveaxis((code - (word & 15)) * s, 2, 0)
+    return [out[0], out[1]]
+
+
+def attend_int4(q, kv_pages, block_table, lens, sinks, scale: float, window: int = 0, new: Optional[tuple] = None):
+    """attend_int8 over the pages of a 4-bit cache."""
+    k, v = values_int4(kv_pages)
+    return attend_int8(q, k, v, np.ones((*k.shape[:2], 2)), block_table, lens, sinks, scale, window, new)
+
+
+def plan_step(new_lens, seq_lens, block_table, free_pages, num_free: int, max_tokens: int) -> dict:
+    """A step's plan, request by request: the list of free pages is a stack, taken from its top."""
+    new, lens, table = _np(new_lens, np.int64), _np(seq_lens, np.int64), _np(block_table, np.int64).copy()
+    free, num_pages = _np(free_pages, np.int64), len(free_pages)
+    room = table.shape[1] * PAGE
+    pos, slots = np.full(max_tokens, -1), np.full(max_tokens, -1)
+    cu, after, t, short, long, bad = [0], [], 0, False, False, False
+    left, wanted = num_free, 0
+    for b, (n, have) in enumerate(zip(new, lens)):
+        long |= n < 0
+        n = max(int(n), 0)
+        fits, rows = have >= 0 and have + n <= room, n == 0 or t + n <= max_tokens
+        long |= not (fits and rows)
+        first, last = -(-have // PAGE), -(-(have + n) // PAGE)
+        need = int(last - first) if fits else 0
+        wanted += need
+        served = bool(fits and rows and (need == 0 or wanted <= num_free))
+        short |= bool(fits and rows and not served)
+        if served:
+            for c in range(first, last):
+                left -= 1
+                table[b, c] = free[left]
+            for i in range(n):
+                p = have + i
+                pg = table[b, p // PAGE]
+                pos[t + i] = p
+                if 0 <= pg < num_pages:
+                    slots[t + i] = pg * PAGE + p % PAGE
+                else:
+                    bad = True
+        after.append(have + n if served else have)
+        t += n
+        cu.append(min(t, max_tokens))
+    return dict(cu_seqlens=np.array(cu), start_pos=lens, seq_lens=np.array(after), positions=pos, slots=slots,
+                num_free=left, block_table=table, short=short, long=long, bad=bad)
+
+
+def release_pages(done, seq_lens, block_table, free_pages, num_free: int):
+    """Lengths, list and its size once the requests that are done have given their pages back."""
+    lens, table, free = _np(seq_lens, np.int64).copy(), _np(block_table, np.int64), _np(free_pages, np.int64).copy()
+    back = [table[b, c] for b in range(len(lens)) if done[b] for c in range(-(-lens[b] // PAGE))]
+    free[num_free:num_free + len(back)] = back[::-1]
+    lens[np.asarray(done, dtype=bool)] = 0
+    return lens, free, num_free + len(back)
 
 
 def rotary_rates(base: float, rotary_dim: int, factor: float = 1.0, scaling: str = "none",

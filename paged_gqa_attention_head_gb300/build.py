@@ -15,8 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsinkattn.so")
-SOURCES = ["api.cpp", "decode.cu", "decode_fp8.cu", "decode_int8.cu", "append.cu", "append_int8.cu", "prefill.cu",
-           "decode_noalloc.cu", "rotary.cu"]
+SOURCES = ["api.cpp", "decode.cu", "decode_fp8.cu", "decode_int8.cu", "decode_int4.cu", "append.cu",
+           "append_int8.cu", "append_int4.cu", "plan.cu", "prefill.cu", "decode_noalloc.cu", "rotary.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 

@@ -195,15 +195,19 @@ int decode_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
     return SINKATTN_OK;
 }
 
-// The INT8 decode's workspace: the same parts for its own grid (ctas8, smem8, total_warps8).
-int decode_int8_layout(const sinkattn_paged_desc *d, DecodeLayout *L) {
+// Which cache a decode reads.
+enum class Cache { kBf16OrFp8, kInt8, kInt4 };
+
+// The INT8 and the 4-bit decode's workspace: the same parts for the kernel's own grid (ctas8, smem8,
+// total_warps8).
+int decode_own_layout(const sinkattn_paged_desc *d, Cache cache, DecodeLayout *L) {
     int device = 0, sms = 0;
     int rc = cuda_rc(cudaGetDevice(&device), "cudaGetDevice");
     if (rc) return rc;
     const int G = d->num_qo_heads / d->num_kv_heads;
-    rc = cuda_rc(decode_int8_launch_shape(d->head_dim, G, d->num_seqs, device, &L->ctas8, &L->warps_per_cta8,
-                                          &L->smem8),
-                 "int8 decode launch shape");
+    rc = cuda_rc((cache == Cache::kInt4 ? decode_int4_launch_shape : decode_int8_launch_shape)(
+                     d->head_dim, G, d->num_seqs, device, &L->ctas8, &L->warps_per_cta8, &L->smem8),
+                 cache == Cache::kInt4 ? "int4 decode launch shape" : "int8 decode launch shape");
     if (rc) return rc;
     rc = cuda_rc(current_sms(&sms), "SM count");
     if (rc) return rc;
@@ -233,7 +237,7 @@ struct DecodePrep {
 int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq_lens,
                    const float *sinks, float scale, void *out, float *lse,
                    const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
-                   DecodePrep *P, bool int8 = false) {
+                   DecodePrep *P, Cache cache = Cache::kBf16OrFp8) {
     int rc = check_decode_desc(desc);
     if (rc) return rc;
     if (!q || !block_table || !seq_lens || !out || !workspace) return SINKATTN_ERR_INVALID_ARG;
@@ -241,7 +245,7 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
         !aligned(block_table, 4) || !aligned(seq_lens, 4) || (sinks && !aligned(sinks, 4)) ||
         (lse && !aligned(lse, 4)))
         return SINKATTN_ERR_INVALID_ARG;
-    rc = int8 ? decode_int8_layout(desc, &P->layout) : decode_layout(desc, &P->layout);
+    rc = cache == Cache::kBf16OrFp8 ? decode_layout(desc, &P->layout) : decode_own_layout(desc, cache, &P->layout);
     if (rc) return rc;
     if (ws_bytes < P->layout.total) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
     DecodeArgs &a = P->args;
@@ -271,6 +275,7 @@ int prepare_decode(const void *q, const int32_t *block_table, const int32_t *seq
     a.k_scale = nullptr;
     a.v_scale = nullptr;
     a.kv_scales = nullptr;
+    a.kv_int4 = nullptr;
     a.k_new = nullptr;
     a.v_new = nullptr;
     a.k_pages_w = nullptr;
@@ -460,7 +465,7 @@ const char *sinkattn_error_string(int code) {
     }
 }
 
-int sinkattn_version(void) { return 10400; }
+int sinkattn_version(void) { return 10500; }
 
 int sinkattn_decode_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
     if (!bytes) return SINKATTN_ERR_INVALID_ARG;
@@ -647,7 +652,7 @@ int sinkattn_decode_int8_workspace_size(const sinkattn_paged_desc *desc, size_t 
     int rc = check_decode_desc(desc);
     if (rc) return rc;
     DecodeLayout L;
-    rc = decode_int8_layout(desc, &L);
+    rc = decode_own_layout(desc, Cache::kInt8, &L);
     if (rc) return rc;
     *bytes = L.total;
     return SINKATTN_OK;
@@ -663,7 +668,7 @@ int sinkattn_decode_int8_report(const void *q, const void *k_pages, const void *
         !aligned(kv_scales, 8) || !aligned(status, 4))
         return SINKATTN_ERR_INVALID_ARG;
     DecodePrep P;
-    int rc = prepare_decode(q, block_table, seq_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, &P, true);
+    int rc = prepare_decode(q, block_table, seq_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, &P, Cache::kInt8);
     if (rc) return rc;
     if ((int64_t)desc->num_seqs * desc->num_qo_heads > (int64_t)INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;  // merge grid
     CUtensorMap kmap, vmap;
@@ -689,6 +694,36 @@ int sinkattn_decode_int8(const void *q, const void *k_pages, const void *v_pages
                                        desc, workspace, ws_bytes, nullptr, stream);
 }
 
+int sinkattn_decode_int4_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
+    if (!bytes) return SINKATTN_ERR_INVALID_ARG;
+    int rc = check_decode_desc(desc);
+    if (rc) return rc;
+    DecodeLayout L;
+    rc = decode_own_layout(desc, Cache::kInt4, &L);
+    if (rc) return rc;
+    *bytes = L.total;
+    return SINKATTN_OK;
+}
+
+int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *block_table, const int32_t *seq_lens,
+                         const float *sinks, float scale, void *out, float *lse, const sinkattn_paged_desc *desc,
+                         void *workspace, size_t ws_bytes, uint32_t *status, sinkattn_stream_t stream) {
+    // an empty batch is a no-op (its data pointers may be NULL)
+    if (desc && desc->num_seqs == 0) return check_decode_desc(desc);
+    if (!kv_pages || !aligned(kv_pages, 16) || !aligned(status, 4)) return SINKATTN_ERR_INVALID_ARG;
+    DecodePrep P;
+    int rc = prepare_decode(q, block_table, seq_lens, sinks, scale, out, lse, desc, workspace, ws_bytes, &P, Cache::kInt4);
+    if (rc) return rc;
+    if ((int64_t)desc->num_seqs * desc->num_qo_heads > (int64_t)INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;  // merge grid
+    P.args.kv_int4 = kv_pages;
+    if (status) P.args.status = status;
+    P.args.total_warps = P.layout.total_warps8;
+    rc = cuda_rc(launch_decode_int4(desc->head_dim, P.args, P.layout.ctas8, P.layout.smem8, (cudaStream_t)stream),
+                 "int4 split-KV decode launch");
+    if (rc) return rc;
+    return cuda_rc(launch_merge_int8(desc->head_dim, P.args, (cudaStream_t)stream), "int4 merge launch");
+}
+
 int sinkattn_prefill_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes) {
     if (!bytes) return SINKATTN_ERR_INVALID_ARG;
     int rc = check_heads(desc);
@@ -698,7 +733,7 @@ int sinkattn_prefill_workspace_size(const sinkattn_paged_desc *desc, size_t *byt
 }
 
 namespace {
-// Scratch of an INT8 prefill: the header, and where its items are split the parts' states.
+// Scratch of an INT8 or 4-bit prefill: the header, and where its items are split the parts' states.
 struct PrefillParts {
     int splits;
     size_t ml, o, total;
@@ -727,7 +762,7 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
                    float scale, void *out, float *lse, const sinkattn_paged_desc *desc, void *workspace,
                    size_t ws_bytes, bool fp8, const float *k_scale, const float *v_scale,
                    bool causal, sinkattn_stream_t stream, const float *kv_scales = nullptr,
-                   uint32_t *status = nullptr) {
+                   uint32_t *status = nullptr, bool int4 = false) {
     int rc = check_heads(desc);
     if (rc) return rc;
     if (!causal && desc->window > 0) return SINKATTN_ERR_INVALID_ARG;
@@ -757,7 +792,10 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
     if ((rc = encode_rows_map(&vmap, v, total_tokens, Hkv, D, 128))) return rc;
     if (fp8 && !has_prefix) return SINKATTN_ERR_INVALID_ARG;
     if ((k_scale && !aligned(k_scale, 4)) || (v_scale && !aligned(v_scale, 4))) return SINKATTN_ERR_INVALID_ARG;
-    if (has_prefix && (fp8 || kv_scales)) {  // one-byte codes
+    if (int4) {  // untiled copies of whole records
+        kpmap = kmap;
+        vpmap = vmap;
+    } else if (has_prefix && (fp8 || kv_scales)) {  // one-byte codes
         if ((rc = encode_pages_map_fp8(&kpmap, k_pages, desc->num_pages, Hkv, D, false))) return rc;
         if ((rc = encode_pages_map_fp8(&vpmap, v_pages, desc->num_pages, Hkv, D, false))) return rc;
     } else if (has_prefix) {
@@ -797,10 +835,11 @@ int prefill_common(const void *q, const void *k, const void *v, const int32_t *c
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.kv_scales = kv_scales;
+    a.kv_int4 = int4 ? k_pages : nullptr;
     a.splits = 1;
     a.part_o = nullptr;
     a.part_ml = nullptr;
-    if (kv_scales) {
+    if (kv_scales || int4) {
         PrefillParts parts;
         if ((rc = prefill_int8_parts(desc, total_tokens, &parts))) return rc;
         if (parts.splits > 1 && ws_bytes >= parts.total) {  // less scratch: the items are not split
@@ -890,6 +929,154 @@ int sinkattn_prefill_int8(const void *q, const void *k, const void *v, const int
     return sinkattn_prefill_int8_report(q, k, v, cu_seqlens, total_tokens, k_pages, v_pages, kv_scales,
                                         prefix_block_table, prefix_lens, sinks, scale, out, lse, desc, workspace,
                                         ws_bytes, nullptr, stream);
+}
+
+int sinkattn_prefill_int4_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens, size_t *bytes) {
+    return sinkattn_prefill_int8_workspace_size(desc, total_tokens, bytes);
+}
+
+int sinkattn_prefill_int4(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                          int32_t total_tokens, const void *kv_pages, const int32_t *prefix_block_table,
+                          const int32_t *prefix_lens, const float *sinks, float scale, void *out, float *lse,
+                          const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes, uint32_t *status,
+                          sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
+    if (!kv_pages || !prefix_block_table || !prefix_lens || !aligned(status, 4)) return SINKATTN_ERR_INVALID_ARG;
+    return prefill_common(q, k, v, cu_seqlens, total_tokens, kv_pages, kv_pages, prefix_block_table, prefix_lens, sinks,
+                          scale, out, lse, desc, workspace, ws_bytes, false, nullptr, nullptr, true, stream, nullptr,
+                          status, true);
+}
+
+int sinkattn_append_kv_int4(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                            const int64_t *slots, int32_t total_tokens, void *kv_pages,
+                            const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                            sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
+    if (total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
+    if (!k || !v || !slots || !kv_pages) return SINKATTN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8) || !aligned(kv_pages, 16)) return SINKATTN_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)desc->num_kv_heads * desc->head_dim;
+    if (k_row_stride < row || v_row_stride < row || k_row_stride % 8 || v_row_stride % 8)
+        return SINKATTN_ERR_INVALID_ARG;
+    if (workspace && (ws_bytes < kStatusBytes || !aligned(workspace, kAlign))) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_pages < 1) return SINKATTN_ERR_INVALID_ARG;
+    AppendInt4Args a;
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_row_stride;
+    a.v_stride = v_row_stride;
+    a.slots = slots;
+    a.kv_pages = kv_pages;
+    a.T = total_tokens;
+    a.Hkv = desc->num_kv_heads;
+    a.num_pages = desc->num_pages;
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_rc(launch_append_int4(desc->head_dim, a, (cudaStream_t)stream), "int4 append launch");
+}
+
+int sinkattn_unpack_kv_int4(const void *kv_pages, const int32_t *pages, int32_t count, void *k_out, void *v_out,
+                            const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes, sinkattn_stream_t stream) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (count < 0) return SINKATTN_ERR_INVALID_ARG;
+    if (count == 0) return SINKATTN_OK;
+    if (!kv_pages || !k_out || !v_out || !aligned(kv_pages, 16) || !aligned(pages, 4) || !aligned(k_out, 16) ||
+        !aligned(v_out, 16))
+        return SINKATTN_ERR_INVALID_ARG;
+    if (workspace && (ws_bytes < kStatusBytes || !aligned(workspace, kAlign))) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_pages < 1 || (!pages && count > desc->num_pages)) return SINKATTN_ERR_INVALID_ARG;
+    if ((int64_t)count * desc->num_kv_heads > (int64_t)INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;
+    UnpackInt4Args a;
+    a.kv_pages = kv_pages;
+    a.pages = pages;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.n = count;
+    a.Hkv = desc->num_kv_heads;
+    a.num_pages = desc->num_pages;
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_rc(launch_unpack_int4(desc->head_dim, a, (cudaStream_t)stream), "int4 unpack launch");
+}
+
+namespace {
+// What the page plan and the release check alike.
+int check_plan(const sinkattn_paged_desc *desc, const int32_t *seq_lens, const int32_t *block_table,
+               const int32_t *free_pages, const int32_t *num_free, const int32_t *seq_lens_out,
+               const int32_t *num_free_out, const void *workspace, size_t ws_bytes) {
+    int rc = check_heads(desc);
+    if (rc) return rc;
+    if (desc->num_pages < 1 || desc->max_pages_per_seq < 1) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_seqs > kPlanMaxSeqs ||
+        (int64_t)desc->num_seqs * desc->max_pages_per_seq >= (int64_t)INT32_MAX)
+        return SINKATTN_ERR_UNSUPPORTED;
+    if (!free_pages || !num_free || !num_free_out) return SINKATTN_ERR_INVALID_ARG;
+    if (desc->num_seqs > 0 && (!seq_lens || !block_table || !seq_lens_out)) return SINKATTN_ERR_INVALID_ARG;
+    if (!aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(num_free, 4) ||
+        !aligned(seq_lens_out, 4) || !aligned(num_free_out, 4))
+        return SINKATTN_ERR_INVALID_ARG;
+    if (workspace && (ws_bytes < kStatusBytes || !aligned(workspace, kAlign))) return SINKATTN_ERR_INVALID_ARG;
+    return SINKATTN_OK;
+}
+}  // namespace
+
+int sinkattn_plan_step(const int32_t *new_lens, const int32_t *seq_lens, int32_t *block_table,
+                       const int32_t *free_pages, const int32_t *num_free, int32_t max_tokens, int32_t *cu_seqlens,
+                       int32_t *start_pos, int32_t *seq_lens_out, int32_t *num_free_out, int32_t *positions,
+                       int64_t *slots, const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                       sinkattn_stream_t stream) {
+    int rc = check_plan(desc, seq_lens, block_table, free_pages, num_free, seq_lens_out, num_free_out, workspace, ws_bytes);
+    if (rc) return rc;
+    if (max_tokens < 0 || !cu_seqlens || (desc->num_seqs > 0 && !new_lens) || (max_tokens > 0 && (!positions || !slots)))
+        return SINKATTN_ERR_INVALID_ARG;
+    if (!aligned(new_lens, 4) || !aligned(cu_seqlens, 4) || !aligned(start_pos, 4) || !aligned(positions, 16) ||
+        !aligned(slots, 16))
+        return SINKATTN_ERR_INVALID_ARG;
+    if (start_pos && (start_pos == seq_lens || start_pos == seq_lens_out)) return SINKATTN_ERR_INVALID_ARG;
+    PlanArgs a = {};
+    a.new_lens = new_lens;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.free_pages = free_pages;
+    a.num_free = num_free;
+    a.num_free_out = num_free_out;
+    a.seq_lens_out = seq_lens_out;
+    a.cu_seqlens = cu_seqlens;
+    a.start_pos = start_pos;
+    a.positions = positions;
+    a.slots = slots;
+    a.B = desc->num_seqs;
+    a.max_tokens = max_tokens;
+    a.num_pages = desc->num_pages;
+    a.max_pages = desc->max_pages_per_seq;
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_rc(launch_plan_step(a, (cudaStream_t)stream), "page plan launch");
+}
+
+int sinkattn_release_pages(const uint8_t *done, const int32_t *seq_lens, const int32_t *block_table,
+                           int32_t *free_pages, const int32_t *num_free, int32_t *seq_lens_out, int32_t *num_free_out,
+                           const sinkattn_paged_desc *desc, void *workspace, size_t ws_bytes,
+                           sinkattn_stream_t stream) {
+    int rc = check_plan(desc, seq_lens, block_table, free_pages, num_free, seq_lens_out, num_free_out, workspace, ws_bytes);
+    if (rc) return rc;
+    if (desc->num_seqs > 0 && !done) return SINKATTN_ERR_INVALID_ARG;
+    PlanArgs a = {};
+    a.done = done;
+    a.seq_lens = seq_lens;
+    a.block_table = const_cast<int32_t *>(block_table);
+    a.free_pages_w = free_pages;
+    a.num_free = num_free;
+    a.num_free_out = num_free_out;
+    a.seq_lens_out = seq_lens_out;
+    a.B = desc->num_seqs;
+    a.num_pages = desc->num_pages;
+    a.max_pages = desc->max_pages_per_seq;
+    a.status = static_cast<uint32_t *>(workspace);
+    return cuda_rc(launch_release_pages(a, (cudaStream_t)stream), "page release launch");
 }
 
 int sinkattn_append_kv_int8(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,

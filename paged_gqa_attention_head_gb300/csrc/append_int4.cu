@@ -1,0 +1,231 @@
+// The 4-bit paged cache: new bf16 K/V rows quantised into their slots, and pages back as the bf16
+// values that they stand for.
+//
+// A group is 32 channels of one token, so an appended row touches no other token's codes, and a
+// row's slot is all that the kernel has to know of the batch.  For a group with low = min(0, min x)
+// and high = max(0, max x):
+//     s    = the smallest number of four significant bits with 15 s >= high - low
+//     z    = rint(-low / s),   code = min(15, rint(x / s + z)),   value = s (code - z)
+// A scale and a code difference of four bits each make every value a bf16 number.  Quotients of
+// bf16 values by such a scale are exact ties or at least 2^-11 away from one: x * (1 / s) + z,
+// snapped to multiples of 2^-11, then rounds exactly as the quotient does.
+//
+// Record of a (page, KV head, K or V), 9 D bytes: codes [D / 32 groups][16 tokens][16 bytes], then
+// [D / 32][16] 16-bit words, the bf16 scale with z in its low four bits.  The codes lie so that
+// 8x8 loads of a group's rows meet no bank conflict, and eight channels of a token in one 32-bit
+// word, channel c at bit 4 (c / 2) + 16 (c % 2): masking a word with 0x000f000f leaves a pair of
+// neighbouring channels, or, after a transposing load, one channel of two neighbouring tokens.
+//
+// Bound by HBM for long appends and for unpacking, by latency for a decode step.  A warp holds eight
+// tokens of one head, four lanes to a group, all groups of K and V at once: reads of 64 bytes and,
+// where the tokens' slots follow each other, writes of 128.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace sinkattn {
+namespace {
+
+constexpr int kI4Warps = 4;
+constexpr float kScaleFloor4 = 7.888609052210118e-31f;  // 2^-100: smaller scales are taken as zero
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t min_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Scale of a group from its low <= 0 <= high.  The range is halved, so that it cannot overflow, and
+// rounded upwards: it passes 7.5 s (eight bits) if and only if the exact one does.
+__device__ __forceinline__ float scale4(float low, float high) {
+    const float half = __fsub_ru(0.5f * high, 0.5f * low);
+    const float s = __uint_as_float((__float_as_uint(__fdiv_ru(half, 7.5f)) + 0xFFFFFu) & 0xFFF00000u);
+    return s >= kScaleFloor4 ? s : 0.f;
+}
+
+// rint(x r + z) in the low bits; the sum snapped to multiples of 2^-11 first (6144 = 1.5 * 2^12).  It is
+// -0.5 or more but for an infinity, whose low bits are those of the code 0.
+__device__ __forceinline__ uint32_t code4(float x, float r, float z6144) {
+    const float q = fminf(fmaf(x, r, z6144) - 6144.f, 15.f);
+    return __float_as_uint(q + 12582912.f);
+}
+
+// Eight channels of one lane and their group's word; the four lanes of a group call it together.
+__device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t &word, bool &bad) {
+    const uint32_t mag = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    bad = (mag & 0xFFFFu) >= 0x7F80u || (mag >> 16) >= 0x7F80u;
+    uint32_t lo2 = min_bf2(min_bf2(x.x, x.y), min_bf2(x.z, x.w));
+    uint32_t hi2 = max_bf2(max_bf2(x.x, x.y), max_bf2(x.z, x.w));
+    if (bad) {  // of the finite values alone; NaN becomes 0, infinities stay and take the last codes
+        uint32_t *u = &x.x;
+        lo2 = hi2 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t fin = 0, keep = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t v = (u[i] >> (16 * h)) & 0xFFFFu, m = v & 0x7FFFu;
+                if (m < 0x7F80u) fin |= v << (16 * h);
+                if (m <= 0x7F80u) keep |= v << (16 * h);
+            }
+            lo2 = min_bf2(lo2, fin);
+            hi2 = max_bf2(hi2, fin);
+            u[i] = keep;
+        }
+    }
+    float low = fminf(fminf(bf_lo(lo2), bf_hi(lo2)), 0.f), high = fmaxf(fmaxf(bf_lo(hi2), bf_hi(hi2)), 0.f);
+    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, 1));
+    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
+    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, 2));
+    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
+    const float s = scale4(low, high);
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    const uint32_t z = __float_as_uint(fmaf(-low, r, 6144.f) - 6144.f + 12582912.f) & 15u;
+    word = (__float_as_uint(s) >> 16) | z;
+    if (s == 0.f) x = make_uint4(0, 0, 0, 0);  // infinities among zeros: times 0 they would be NaN
+    const float zf = (float)z + 6144.f;
+    uint32_t w = 0;
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = code4(bf_lo(u[i]), r, zf), b = code4(bf_hi(u[i]), r, zf);
+        w |= __byte_perm(a, b, 0x5410) << (4 * i);
+    }
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kI4Warps) append_int4_kernel(const AppendInt4Args a) {
+    constexpr int NG = D / 32;
+    const int lane = threadIdx.x & 31, t4 = lane & 3;
+    const int64_t unit = (int64_t)blockIdx.x * kI4Warps + (threadIdx.x >> 5);
+    const int g = (int)(unit % a.Hkv);
+    const int64_t t = unit / a.Hkv * 8 + (lane >> 2);
+    if (unit / a.Hkv * 8 >= a.T) return;
+    const bool in = t < a.T;
+    uint4 x[2][NG];
+    const __nv_bfloat16 *kr = reinterpret_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride + (int64_t)g * D + 8 * t4;
+    const __nv_bfloat16 *vr = reinterpret_cast<const __nv_bfloat16 *>(a.v) + t * a.v_stride + (int64_t)g * D + 8 * t4;
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+        if (in) {
+            x[0][i] = __ldg(reinterpret_cast<const uint4 *>(kr + 32 * i));
+            x[1][i] = __ldg(reinterpret_cast<const uint4 *>(vr + 32 * i));
+        }
+    }
+    int64_t slot = in ? a.slots[t] : -1;
+    const int64_t page = slot / kPageSize;
+    if (slot >= 0 && page >= a.num_pages) {
+        if (g == 0 && t4 == 0) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+        slot = -1;
+    }
+    const int tok = (int)(slot % kPageSize);
+    uint8_t *rec = static_cast<uint8_t *>(a.kv_pages) + (page * a.Hkv + g) * (18 * D);
+    bool any_bad = false;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            uint32_t word;
+            bool bad;
+            const uint32_t codes = quantise8(x[kv][i], word, bad);
+            any_bad |= bad;
+            if (slot >= 0) {
+                uint8_t *r = rec + kv * 9 * D;
+                *reinterpret_cast<uint32_t *>(r + (i * kPageSize + tok) * 16 + 4 * t4) = codes;
+                if (t4 == 0) *reinterpret_cast<uint16_t *>(r + 8 * D + (i * kPageSize + tok) * 2) = (uint16_t)word;
+            }
+        }
+    if (any_bad && slot >= 0) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
+}
+
+__device__ __forceinline__ uint32_t sub_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A thread takes a run of eight channels of a token, D / 8 neighbouring threads a row: 16-byte stores
+// side by side, and 64 bytes of codes of each group to a warp.
+template <int D>
+__global__ void __launch_bounds__(256) unpack_int4_kernel(const UnpackInt4Args a) {
+    constexpr int kRuns = D / 8, kPer = 2 * kPageSize * kRuns;  // runs of a row; of a (page, head)
+    const uint32_t pairs = (uint32_t)a.n * a.Hkv;  // (page, head) pairs, below 2^31
+    constexpr int N = 4;
+    uint32_t w[N], p[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const uint32_t i = e * 256 + threadIdx.x, ph = blockIdx.x * (256 * N / kPer) + i / kPer;
+        w[e] = p[e] = 0;
+        if (ph >= pairs) continue;
+        const int at = (int)(i % kPer), kv = at / (kPageSize * kRuns), tok = at / kRuns % kPageSize, c = at % kRuns;
+        const uint32_t head = ph % (uint32_t)a.Hkv;
+        int64_t page = ph / (uint32_t)a.Hkv;
+        if (a.pages) page = a.pages[page];
+        if (page < 0 || page >= a.num_pages) {
+            if (at == 0 && head == 0) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+            continue;  // its values are zeros
+        }
+        const uint8_t *r = static_cast<const uint8_t *>(a.kv_pages) + ((page * a.Hkv + head) * 2 + kv) * (9 * D);
+        const int row = c / 4 * kPageSize + tok;
+        w[e] = __ldg(reinterpret_cast<const uint32_t *>(r + row * 16 + 4 * (c % 4)));
+        p[e] = __ldg(reinterpret_cast<const uint16_t *>(r + 8 * D + 2 * row));
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const uint32_t i = e * 256 + threadIdx.x, ph = blockIdx.x * (256 * N / kPer) + i / kPer;
+        if (ph >= pairs) continue;
+        const int at = (int)(i % kPer), kv = at / (kPageSize * kRuns), rest = at % (kPageSize * kRuns);
+        // 128 + code and 128 + z are bf16 numbers, and so is all that follows
+        const uint32_t s = (p[e] & 0xFFF0u) * 0x10001u, z = (p[e] & 15u) * 0x10001u + 0x43004300u;
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = mul_bf2(sub_bf2(((w[e] >> (4 * j)) & 0x000F000Fu) | 0x43004300u, z), s);
+        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(kv ? a.v_out : a.k_out);
+        *reinterpret_cast<uint4 *>(out + ((int64_t)ph * (kPageSize * kRuns) + rest) * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_int4(int D, const AppendInt4Args &a, cudaStream_t stream) {
+    if (a.T <= 0 || a.Hkv <= 0) return cudaSuccess;
+    const int64_t units = ((int64_t)a.T + 7) / 8 * a.Hkv, grid = (units + kI4Warps - 1) / kI4Warps;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (D == 64)
+        append_int4_kernel<64><<<(unsigned)grid, 32 * kI4Warps, 0, stream>>>(a);
+    else if (D == 128)
+        append_int4_kernel<128><<<(unsigned)grid, 32 * kI4Warps, 0, stream>>>(a);
+    else
+        return cudaErrorInvalidValue;
+    return cudaGetLastError();
+}
+
+cudaError_t launch_unpack_int4(int D, const UnpackInt4Args &a, cudaStream_t stream) {
+    const int64_t pairs = (int64_t)a.n * a.Hkv, per = 1024 / (4 * D), grid = (pairs + per - 1) / per;
+    if (grid <= 0) return cudaSuccess;
+    if (pairs > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (D == 64)
+        unpack_int4_kernel<64><<<(unsigned)grid, 256, 0, stream>>>(a);
+    else if (D == 128)
+        unpack_int4_kernel<128><<<(unsigned)grid, 256, 0, stream>>>(a);
+    else
+        return cudaErrorInvalidValue;
+    return cudaGetLastError();
+}
+
+}  // namespace sinkattn

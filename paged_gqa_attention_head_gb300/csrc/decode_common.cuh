@@ -1,7 +1,7 @@
 // Pieces of the split-KV decode plan shared by the bf16, FP8 and INT8 decode kernels:
 // the per-sequence page counts and their prefix sum (the list of (sequence, KV head,
 // page) units every warp takes an equal contiguous range of) and the cursor that
-// walks that list; and the MMA of the one-byte caches.
+// walks that list; and the MMA of the narrow caches.
 #pragma once
 
 #include "internal.h"
@@ -78,7 +78,7 @@ __device__ void scan_pages(const DecodeArgs &a, int *s_prefix, int *s_len, int *
     __syncthreads();
 }
 
-// ---------------------------------------------------------------- one-byte caches (FP8, INT8)
+// ---------------------------------------------------------------- narrow caches (FP8, INT8, 4 bits)
 // D(16x8, f32) += A(16x16, f16, row) * B(16x8, f16, col)
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -87,6 +87,16 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A B + C with C's columns c0 and c1 in every row.
+__device__ __forceinline__ void mma_f16_16816_from(float (&d)[4], float c0, float c1, uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 // Position in the unit list: sequence b, KV head g, unit p of the sequence.

@@ -110,15 +110,6 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2_times(uint32_t v, float mul)
     return pack_f16x2(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xFFFF0000u) * mul);
 }
 
-// D = A B + C with C's columns c0 and c1 in every row.
-__device__ __forceinline__ void mma_f16_16816_from(float (&d)[4], float c0, float c1, uint32_t a0, uint32_t a1,
-                                                   uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %11, %10, %11};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
-}
 constexpr uint32_t kMinus128 = 0x80808080u;  // an f16 pair of -128 * 2^-24
 constexpr float kUp24 = 16777216.f;          // 2^24
 

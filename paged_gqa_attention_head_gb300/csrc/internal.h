@@ -55,6 +55,7 @@ struct DecodeArgs {
     const float *k_scale;   // FP8 cache: [Hkv] per-KV-head scales, or nullptr (1)
     const float *v_scale;
     const float *kv_scales;  // INT8 cache: [num_pages, Hkv, 2] scales (K, V); nullptr: not an INT8 cache
+    const void *kv_int4;     // 4-bit cache: uint8 [num_pages, Hkv, 2, 9 D]; nullptr: not one
     const void *k_new;      // decode with append: bf16 [B, Hkv, D] new rows, or nullptr
     const void *v_new;
     void *k_pages_w;        // the cache the new rows are written into (decode with append)
@@ -99,6 +100,11 @@ cudaError_t launch_decode_int8(int D, const DecodeArgs &a, const CUtensorMap &km
                                int ctas, int smem_bytes, cudaStream_t stream);
 cudaError_t launch_merge_int8(int D, const DecodeArgs &a, cudaStream_t stream);
 
+// The same for the decode over a 4-bit cache (a.kv_int4 set); the INT8 decode's merge completes it.
+cudaError_t decode_int4_launch_shape(int D, int G, int B, int device, int *ctas, int *warps_per_cta,
+                                     int *smem_bytes);
+cudaError_t launch_decode_int4(int D, const DecodeArgs &a, int ctas, int smem_bytes, cudaStream_t stream);
+
 struct AppendArgs {
     const void *k, *v;  // bf16 [T, Hkv, D]
     const int32_t *cu_seqlens;
@@ -125,6 +131,46 @@ struct AppendInt8Args {
     uint32_t *status;            // or nullptr
 };
 cudaError_t launch_append_int8(int D, AppendInt8Args a, cudaStream_t stream);
+
+struct AppendInt4Args {
+    const void *k, *v;           // bf16 [T] rows of [Hkv, D], `stride` elements apart
+    int64_t k_stride, v_stride;
+    const int64_t *slots;        // [T] slot of each row (page * 16 + place), negative: none
+    void *kv_pages;              // uint8 [num_pages, Hkv, 2, 9 D]
+    int T, Hkv, num_pages;
+    uint32_t *status;            // or nullptr
+};
+cudaError_t launch_append_int4(int D, const AppendInt4Args &a, cudaStream_t stream);
+
+struct UnpackInt4Args {
+    const void *kv_pages;        // uint8 [num_pages, Hkv, 2, 9 D]
+    const int32_t *pages;        // [n] or nullptr: 0 .. n - 1
+    void *k_out, *v_out;         // bf16 [n, Hkv, 16, D]
+    int n, Hkv, num_pages;
+    uint32_t *status;            // or nullptr
+};
+cudaError_t launch_unpack_int4(int D, const UnpackInt4Args &a, cudaStream_t stream);
+
+// Page plan of a step, and release of finished requests' pages.
+constexpr int kPlanMaxSeqs = 8192;  // their lengths lie in shared memory
+struct PlanArgs {
+    const int32_t *new_lens;     // plan: [B]
+    const uint8_t *done;         // release: [B]
+    const int32_t *seq_lens;     // [B]
+    int32_t *block_table;        // [B, max_pages] (release: read alone)
+    const int32_t *free_pages;   // plan: the list
+    int32_t *free_pages_w;       // release: the list
+    const int32_t *num_free;
+    int32_t *num_free_out, *seq_lens_out;  // may be num_free and seq_lens
+    int32_t *cu_seqlens;         // [B + 1]
+    int32_t *start_pos;          // [B] or nullptr
+    int32_t *positions;          // [max_tokens]
+    int64_t *slots;              // [max_tokens]
+    int B, max_tokens, num_pages, max_pages;
+    uint32_t *status;            // or nullptr
+};
+cudaError_t launch_plan_step(const PlanArgs &a, cudaStream_t stream);
+cudaError_t launch_release_pages(const PlanArgs &a, cudaStream_t stream);
 
 constexpr int kRotaryMaxPos = 1 << 24;  // positions stay exact floats below this
 struct RotaryArgs {
@@ -165,11 +211,12 @@ struct PrefillArgs {
     uint32_t *sched;                   // [2] in the workspace header: next item, CTAs done (zero between calls)
     const float *k_scale, *v_scale;    // FP8 prefix: [Hkv] per-KV-head scales, or nullptr (1)
     const float *kv_scales;            // INT8 prefix: [num_pages, Hkv, 2] scales (K, V); nullptr: not INT8
-    int splits;                        // INT8 prefix: parts an item's key tiles are split into (1: none)
+    const void *kv_int4;               // 4-bit prefix: uint8 [num_pages, Hkv, 2, 9 D]; nullptr: not one
+    int splits;                        // INT8 and 4-bit prefix: parts an item's key tiles are split into (1: none)
     float *part_o;                     // splits > 1: [T, Hq, splits, D] unnormalised outputs
     float2 *part_ml;                   // splits > 1: [T, Hq, splits] running max (log2) and sum
 };
-// Parts that an INT8 prefill splits its items' key tiles into, from what the host knows.
+// Parts that an INT8 or 4-bit prefill splits its items' key tiles into, from what the host knows.
 int prefill_int8_splits(int T, int n, int Hq, int G, int max_pages, int window, int sms);
 cudaError_t launch_prefill_merge(const PrefillArgs &a, cudaStream_t stream);
 // Tensor maps: q [T, Hq, D], k/v [T, Hkv, D] (new tokens), kp/vp prefix pages.

@@ -140,6 +140,10 @@ struct PrefillCfg {
     __host__ __device__ static constexpr uint32_t kOffFp8Page(int p) {
         return D == 64 ? 2048u * p + 1024u : 16384u + 2048u * p;
     }
+    // 4-bit pages (9 D bytes: codes, then words) end where their own converted rows end.
+    __host__ __device__ static constexpr uint32_t kOffInt4Page(int p) {
+        return (D == 64 ? 2048u * p : 16384u + 2048u * p) + 2048u - 9u * D;
+    }
     static_assert(kColO(2) <= 512, "TMEM columns");
 };
 
@@ -327,6 +331,97 @@ __device__ __forceinline__ void convert_int8_quarter(uint8_t *t, int q, int lane
     }
 }
 
+// Eight 4-bit codes (a word) less z, times their group's scale, as one 16-byte vector.  kV false: bf16
+// for K: 128 + code and 128 + z are bf16 numbers, and so are the difference (four bits) and its product
+// with a scale of four bits.  kV true: fp16 for V: 1024 + code, or 1024 + 16 code for every other pair,
+// which one multiplication and addition brings down to the difference.  zz and zo: pairs of what comes
+// off; ss: a pair of the scale.
+template <bool kV>
+__device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t zz, uint32_t zo, uint32_t ss) {
+    uint32_t o[4];
+    if (!kV) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}"
+                : "=r"(o[j])
+                : "r"(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u), "r"(zz), "r"(ss));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const uint32_t h = w >> (4 * j);
+            asm("{\n\t.reg .b32 d;\n\tsub.rn.f16x2 d, %1, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
+                : "=r"(o[j])
+                : "r"((h & 0x000F000Fu) | 0x64006400u), "r"(zz), "r"(ss));
+            asm("{\n\t.reg .b32 d;\n\tfma.rn.f16x2 d, %1, %4, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
+                : "=r"(o[j + 1])
+                : "r"((h & 0x00F000F0u) | 0x64006400u), "r"(zo), "r"(ss), "r"(0x2C002C00u));  // 1/16
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One converter warp's quarter of a 4-bit prefix tile, in place: a lane takes the 32 channels of a token's
+// group at a time, 16 bytes of codes to four chunks of its row (neighbouring lanes: neighbouring tokens,
+// whose swizzled chunks meet no bank conflict).  Tokens from `rows` on (of the quarter) become zeros,
+// whatever lies there.  K: bf16 values, exactly.  V: fp16 values times 2^-k, |value| 2^-k < 2^15, k from
+// the quarter's largest scale; returns k (8 or more: out of range).
+template <int D, bool kV>
+__device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane, int rows) {
+    using C = PrefillCfg<D>;
+    constexpr int N = D / 64;  // token groups of a lane and page
+    const int tok = lane & 15;
+    int kexp = 0;
+    if (kV) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const uint32_t w = *reinterpret_cast<const uint16_t *>(t + C::kOffInt4Page(2 * q + i) + 8 * D + 2 * (lane + 32 * e));
+                if (16 * i + tok < rows) mx = max(mx, w);
+            }
+        kexp = max(0, (int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127 - 10);  // |code - z| <= 15
+    }
+    const float down = __uint_as_float((uint32_t)(127 - min(kexp, 7)) << 23);
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int p = 2 * q + i;
+        const uint8_t *src = t + C::kOffInt4Page(p);
+        uint4 x[N];
+        uint32_t w[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            x[e] = *reinterpret_cast<const uint4 *>(src + 16 * (lane + 32 * e));
+            w[e] = *reinterpret_cast<const uint16_t *>(src + 8 * D + 2 * (lane + 32 * e));
+        }
+        __syncwarp();  // a page's rows cover its codes
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int g = 2 * e + (lane >> 4);
+            if (16 * i + tok >= rows) w[e] = 0;
+            const uint32_t z = (w[e] & 15u) * 0x10001u;
+            uint32_t zz, zo = 0, ss;
+            if (kV) {
+                zz = z | 0x64006400u;                                                          // 1024 + z
+                asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(zo) : "r"(0x63806380u), "r"(zz));  // 960 - (1024 + z)
+                const float s = __uint_as_float((w[e] & 0xFFF0u) << 16) * down;
+                ss = pack_f16x2(s, s);
+            } else {
+                zz = z | 0x43004300u;  // 128 + z
+                ss = (w[e] & 0xFFF0u) * 0x10001u;
+            }
+            uint8_t *dst = t + (g >> 1) * 16384;
+            const int row = kPageSize * p + tok, c0 = 4 * (g & 1);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 0)) = int4x8<kV>(x[e].x, zz, zo, ss);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 1)) = int4x8<kV>(x[e].y, zz, zo, ss);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 2)) = int4x8<kV>(x[e].z, zz, zo, ss);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 3)) = int4x8<kV>(x[e].w, zz, zo, ss);
+        }
+        __syncwarp();
+    }
+    return kexp;
+}
+
 // Work list, in two parts.  (A) Requests with a paged prefix, request by request (each
 // request's query blocks from the last to the first, then by head pair): the items that
 // read one request's prefix run close together in time and share its pages in L2.  An INT8 prefill
@@ -467,7 +562,7 @@ struct Item {
     int req, qb, h0;
 };
 
-// INT8 prefill with few items: an item's key tiles are cut into up to `splits` parts of this many tiles
+// INT8 or 4-bit prefill with few items: an item's key tiles are cut into up to `splits` parts of this many tiles
 // (the last may have fewer), each an item of its own that leaves its rows' unnormalised outputs, maxima
 // and sums for the merge, the sink counted in the first.  An item of one tile stays whole.
 constexpr int kMaxSplits = 32;  // one lane of the merge holds one part's maximum and sum
@@ -630,8 +725,10 @@ static_assert(sizeof(ItemSlot) == 64, "item slot");
 // those tiles), V to fp16 value * 2^-k like the bf16 V tiles.  kInt8: it is an INT8 cache with a
 // scale per page and head: the same staging and conversion, the scales of a tile's eight pages
 // looked up by the producer with the pages and applied by the softmax page by page (16 columns
-// of S), so that no code or scale is rounded.
-template <int D, bool kWindow, bool kFp8, bool kCausal, bool kInt8>
+// of S), so that no code or scale is rounded.  kInt4: it is a 4-bit cache (append_int4.cu): the
+// converters make its values, K in bf16 exactly, V in fp16 like the bf16 V tiles, so that the softmax
+// has nothing to do for it.
+template <int D, bool kWindow, bool kFp8, bool kCausal, bool kInt8, bool kInt4>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kpmap,
@@ -672,22 +769,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *s_vscale = misc + 32;  // [NS][4] exponent k of each 32-key quarter of each V tile
     ItemSlot *s_slot = reinterpret_cast<ItemSlot *>(smem + C::kOffSlot);  // the k-th item in slot k % kItemRing
     PageScales *s_page = reinterpret_cast<PageScales *>(smem + C::kOffPage);  // INT8: [NS]
-    constexpr bool kCodes = kFp8 || kInt8;  // the prefix tiles are staged as one-byte codes
-    constexpr bool kFrom = kWindow || kInt8;  // an item's key tiles may start behind the first
+    constexpr bool kCodes = kFp8 || kInt8 || kInt4;  // the prefix tiles are staged as codes
+    constexpr bool kSplit = kInt8 || kInt4;          // requests by their length, and items in parts
+    constexpr bool kFrom = kWindow || kSplit;  // an item's key tiles may start behind the first
     // INT8: the converters have more to do and are given more registers, at head_dim 64 the softmax's,
     // whose rows are shorter there (8 chunks of 512 tokens over 16384-token prefixes 1639 -> 1549 us),
     // at 128 the side warps' (7 ragged chunks 183 -> 175 us with 40 for both, 130 -> 128 with 32 and 48)
-    constexpr uint32_t kSideRegs = kInt8 && D == 128 ? 32 : kRegsSide;
-    constexpr uint32_t kConvertRegs = kInt8 ? 48 : kRegsConvert;
-    constexpr uint32_t kSoftmaxRegs = kInt8 && D == 64 ? 208 : kRegsSoftmax;
+    constexpr uint32_t kSideRegs = kSplit && D == 128 ? 32 : kRegsSide;
+    constexpr uint32_t kConvertRegs = kSplit ? 48 : kRegsConvert;
+    constexpr uint32_t kSoftmaxRegs = kSplit && D == 64 ? 208 : kRegsSoftmax;
     static_assert(128 * kSideRegs + 128 * kConvertRegs + 256 * kSoftmaxRegs <= kThreads * kRegsLaunch, "register split");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     WorkList wl;
-    worklist_setup<kInt8>(a, s_loc, s_loc + kLocateMax, s_loc + 2 * kLocateMax, s_loc + 3 * kLocateMax,
+    worklist_setup<kSplit>(a, s_loc, s_loc + kLocateMax, s_loc + 2 * kLocateMax, s_loc + 3 * kLocateMax,
                           s_loc + 4 * kLocateMax, misc + 4, &wl);
-    const int splits = kInt8 ? a.splits : 1;
+    const int splits = kSplit ? a.splits : 1;
     const int n_items = wl.tiles * wl.groups * splits;
     if ((int)blockIdx.x >= n_items) {  // CTA-uniform, before any allocation
         if (tid == 0) cta_done(a.sched);
@@ -750,18 +848,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ItemSlot &sl = s_slot[kk % kItemRing];
                 bool first = true;  // the item's part that counts the sink
                 r = min((int)atomicAdd(a.sched, 1u), n_items);
-                if constexpr (kInt8) {
+                if constexpr (kSplit) {
                     while (splits > 1 && r < n_items) {  // parts past their item's last tile are none
-                        const ItemGeom gm = geom_of<kWindow, kCausal>(a, item_of<kInt8>(a, wl, r / splits));
+                        const ItemGeom gm = geom_of<kWindow, kCausal>(a, item_of<kSplit>(a, wl, r / splits));
                         if (r % splits * part_tiles(gm.n_kv, splits) < gm.n_kv) break;
                         r = min((int)atomicAdd(a.sched, 1u), n_items);
                     }
                 }
                 sl.rank = r;
                 if (r < n_items) {
-                    sl.it = item_of<kInt8>(a, wl, kInt8 ? r / splits : r);
+                    sl.it = item_of<kSplit>(a, wl, kSplit ? r / splits : r);
                     sl.gm = geom_of<kWindow, kCausal>(a, sl.it);
-                    if constexpr (kInt8) {
+                    if constexpr (kSplit) {
                         int part = -1;  // whole
                         const int per = part_tiles(sl.gm.n_kv, splits);
                         if (splits > 1 && per < sl.gm.n_kv) {
@@ -860,7 +958,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lift = 0;
                     __syncwarp();  // before lane 0 arrives on the stage's barriers
                 }
-                if (kCodes && tt < gm.n_pre) {
+                if (kInt4 && tt < gm.n_pre) {
+                    // eight pages as they lie, K and V of the head apart, ragged ones whole (the converters
+                    // leave out what is past the prefix); a page that is not there: words of zero, which
+                    // make every value zero
+                    const bool have = nrow > 0 && pg >= 0;
+                    const uint32_t have_mask = __ballot_sync(0xffffffffu, have);
+                    if (lane == 0) {
+                        const uint32_t bytes = (uint32_t)__popc(have_mask) * 9 * D;
+                        mbar_expect_tx(&bars.k_full[s], bytes);
+                        mbar_expect_tx(&bars.v_full[s], bytes);
+                    }
+                    if (have) {
+                        const uint8_t *rec = static_cast<const uint8_t *>(a.kv_int4) + ((int64_t)pg * a.Hkv + gm.g) * (18 * D);
+                        bulk_load(kt + C::kOffInt4Page(lane), rec, 9 * D, &bars.k_full[s]);
+                        bulk_load(vt + C::kOffInt4Page(lane), rec + 9 * D, 9 * D, &bars.v_full[s]);
+                    } else if (lane < 8) {
+                        for (int e = 0; e < D; e += 16) {
+                            *reinterpret_cast<uint4 *>(kt + C::kOffInt4Page(lane) + 8 * D + e) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(vt + C::kOffInt4Page(lane) + 8 * D + e) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars.k_full[s]);
+                        mbar_arrive(&bars.v_full[s]);
+                    }
+                } else if (kCodes && tt < gm.n_pre) {
                     // eight FP8 or INT8 pages of 16 tokens, as codes into their staging places: each
                     // whole valid page by a TMA issued from its own lane (one box of 16 rows x D
                     // bytes), the others by the warp (valid rows copied, the rest code 0 = 0.0)
@@ -1145,7 +1270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (fp8_tile && kInt8)
+                    if (fp8_tile && kInt4)
+                        convert_int4_quarter<D, false>(sK + st * C::kKVBytes, q, lane, gm.P - (gm.t0 + j) * kBN - 32 * q);
+                    else if (fp8_tile && kInt8)
                         convert_int8_quarter<D, 3>(sK + st * C::kKVBytes, q, lane);
                     else if (fp8_tile)
                         convert_fp8_quarter<D, 0>(sK + st * C::kKVBytes, q, lane, 1.f);
@@ -1161,13 +1288,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (fp8_tile) {
                     // V: code * 2^e8 (the softmax takes the rest of the scale), or fp16 of
                     // value * 2^-k, value = scale * e4m3(code), k of the item
-                    if (kInt8)
+                    int kexp4 = 0;
+                    if (kInt4) {
+                        kexp4 = convert_int4_quarter<D, true>(sV + st * C::kKVBytes, q, lane, gm.P - (gm.t0 + j) * kBN - 32 * q);
+                        if (kexp4 > 7) {
+                            if (lane == 0) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
+                            kexp4 = 7;
+                        }
+                    } else if (kInt8)
                         convert_int8_quarter<D, 4>(sV + st * C::kKVBytes, q, lane, s_page[st].v2);
                     else if (fold8)
                         convert_fp8_quarter<D, 2>(sV + st * C::kKVBytes, q, lane, 1.f, p2e8);
                     else
                         convert_fp8_quarter<D, 1>(sV + st * C::kKVBytes, q, lane, vmul8);
-                    if (lane == 0) s_vscale[st * 4 + q] = fold8 ? 0 : kexp8;
+                    if (lane == 0) s_vscale[st * 4 + q] = kInt4 ? kexp4 : fold8 ? 0 : kexp8;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.v_conv[st]);
@@ -1251,7 +1385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int k = 0;
         bool ok = x < ntiles;
         auto take = [&](int kk) {
-            if (!wait_or_abort<false, kInt8>(&bars.item_full[kk % kItemRing], (uint32_t)((kk / kItemRing) & 1), s_abort, a.status,
+            if (!wait_or_abort<false, kSplit>(&bars.item_full[kk % kItemRing], (uint32_t)((kk / kItemRing) & 1), s_abort, a.status,
                                a.wait_limit_cycles))
                 return n_items;
             return s_slot[kk % kItemRing].rank;
@@ -1278,7 +1412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b = i % NBS, pb = i % NBP;
                 const uint32_t ts = tmem + lane_base + C::kColS(b);
                 const uint32_t tp = tmem + lane_base + C::kColP(pb);
-                if (!wait_or_abort<false, kInt8>(&bars.s_full[b], (i / NBS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+                if (!wait_or_abort<false, kSplit>(&bars.s_full[b], (i / NBS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                     ok = false;
                     break;
                 }
@@ -1346,7 +1480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  fmaxf(mx8[6], mx8[7]));
                 };
                 if (kInt8 && j == 0 &&  // the page scales are in place once the V tile is
-                    !wait_or_abort<false, kInt8>(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
+                    !wait_or_abort<false, kSplit>(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
                                    a.wait_limit_cycles)) {
                     ok = false;
                     break;
@@ -1361,7 +1495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (keys 2c, 2c + 1 in column c); 2^-k is the scale of the V quarter holding
                 // keys 32ch..32ch+31
                 const int vst = (tcount - 1) % NS;
-                if (!wait_or_abort<false, kInt8>(&bars.v_conv[vst], ((tcount - 1) / NS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+                if (!wait_or_abort<false, kSplit>(&bars.v_conv[vst], ((tcount - 1) / NS) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                     ok = false;
                     break;
                 }
@@ -1409,7 +1543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (ch == 0 && pwait) {
                             pwait = false;
-                            if (!wait_or_abort<false, kInt8>(&bars.pv_done[pb], ((i - NBP) / NBP) & 1, s_abort, a.status,
+                            if (!wait_or_abort<false, kSplit>(&bars.pv_done[pb], ((i - NBP) / NBP) & 1, s_abort, a.status,
                                                a.wait_limit_cycles))
                                 pfail = true;
                             tc::fence_after_sync();
@@ -1440,7 +1574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float mt = kInt8 ? row_max() : row_max() * sc;
                         // O_x must hold the P.V of this query tile's previous key tile, product i - ntiles
                         const uint32_t ip = i - ntiles;
-                        if (!wait_or_abort<false, kInt8>(&bars.pv_done[ip % NBP], (ip / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+                        if (!wait_or_abort<false, kSplit>(&bars.pv_done[ip % NBP], (ip / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                             ok = false;
                             break;
                         }
@@ -1474,15 +1608,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             // epilogue: O / l for this row, once the item's last P.V has landed
             const uint32_t il = (tcount - 1) * ntiles + x;  // S product of the last key tile
-            if (!wait_or_abort<false, kInt8>(&bars.pv_done[il % NBP], (il / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
+            if (!wait_or_abort<false, kSplit>(&bars.pv_done[il % NBP], (il / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const bool valid = t < gm.L && gm.row0 >= 0 && gm.row0 + t < a.T;
-            const int part = kInt8 ? s_slot[k % kItemRing].part : -1;
-            if (kInt8 && part >= 0) {
+            const int part = kSplit ? s_slot[k % kItemRing].part : -1;
+            if (kSplit && part >= 0) {
                 // a part: the row's sums as they are, for the merge
                 const int64_t pr = ((int64_t)(gm.row0 + t) * a.Hq + h) * splits + part;
                 float *po = a.part_o + pr * D;
@@ -1500,7 +1634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // O is lifted: with the maximum lower and the sum higher by as much, the merge's weights are right
-                const int up = s_slot[k % kItemRing].lift;
+                const int up = kInt8 ? s_slot[k % kItemRing].lift : 0;
                 if (valid) a.part_ml[pr] = make_float2(m_used - (float)up, l * __uint_as_float((uint32_t)(127 + up) << 23));
                 tc::fence_before_sync();
                 __syncwarp();
@@ -1563,16 +1697,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         tc::dealloc(tmem, kTmemCols);
     }
-    if (kInt8 && splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge
+    if (kSplit && splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge
     if (tid == 0) cta_done(a.sched);
 }
 
-template <int D, bool kWindow, bool kFp8, bool kCausal = true, bool kInt8 = false>
+template <int D, bool kWindow, bool kFp8, bool kCausal = true, bool kInt8 = false, bool kInt4 = false>
 cudaError_t launch_d(const PrefillArgs &a, const CUtensorMap &qmap, const CUtensorMap &kmap,
                      const CUtensorMap &vmap, const CUtensorMap &kpmap, const CUtensorMap &vpmap,
                      cudaStream_t stream) {
     using C = PrefillCfg<D, (D == 64 && kWindow) ? 2 : 1>;
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, kWindow, kFp8, kCausal, kInt8>,
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, kWindow, kFp8, kCausal, kInt8, kInt4>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
     int device = 0, sms = 0;
@@ -1581,7 +1715,7 @@ cudaError_t launch_d(const PrefillArgs &a, const CUtensorMap &qmap, const CUtens
     // persistent: one CTA per SM (shared memory and the 512 TMEM columns allow no more),
     // on at most max_sms SMs when the caller keeps the others for concurrent work
     if (a.max_sms > 0 && a.max_sms < sms) sms = a.max_sms;
-    prefill_kernel<D, kWindow, kFp8, kCausal, kInt8><<<sms, kThreads, C::kSmemBytes, stream>>>(qmap, kmap, vmap, kpmap, vpmap, a);
+    prefill_kernel<D, kWindow, kFp8, kCausal, kInt8, kInt4><<<sms, kThreads, C::kSmemBytes, stream>>>(qmap, kmap, vmap, kpmap, vpmap, a);
     return cudaGetLastError();
 }
 
@@ -1691,6 +1825,15 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &qmap, const 
         if (a.fp8_prefix || w || a.prefix_lens) return cudaErrorInvalidValue;
         if (a.D == 64) return launch_d<64, false, false, false>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
         if (a.D == 128) return launch_d<128, false, false, false>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
+        return cudaErrorNotSupported;
+    }
+    if (a.kv_int4) {
+        if (a.D == 64)
+            return w ? launch_d<64, true, false, true, false, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream)
+                     : launch_d<64, false, false, true, false, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
+        if (a.D == 128)
+            return w ? launch_d<128, true, false, true, false, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream)
+                     : launch_d<128, false, false, true, false, true>(a, qmap, kmap, vmap, kpmap, vpmap, stream);
         return cudaErrorNotSupported;
     }
     if (a.kv_scales) {

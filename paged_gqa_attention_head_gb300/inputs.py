@@ -150,6 +150,33 @@ def normal_int8(shape, seed: int, stream: int):
     return codes, scales
 
 
+def pack_int4(k_pages: torch.Tensor, v_pages: torch.Tensor) -> torch.Tensor:
+    """A 4-bit cache uint8 [num_pages, Hkv, 2, 9, D] of bf16 pages [num_pages, Hkv, 16, D]: each group of
+    32 channels by its range (0 counted in), the scale rounded up to four significant bits.  Groups
+    with a NaN (poisoned slots) take NaN words and the code 15 throughout."""
+    out = []
+    for x in (k_pages, v_pages):
+        n, h, _, dim = x.shape
+        x = x.double().reshape(n, h, PAGE_SIZE, dim // 32, 32)
+        lost = x.isnan().any(-1)
+        x = x.nan_to_num(0.0)
+        low, high = x.amin(-1).clamp(max=0), x.amax(-1).clamp(min=0)
+        part, power = np.frexp(((high - low) / 15).numpy())
+        s = torch.from_numpy(np.ldexp(np.ceil(part * 16) / 16, power))
+        by = torch.where(s > 0, s, torch.ones_like(s))
+        z = torch.round(-low / by)
+        codes = torch.round(x / by[..., None] + z[..., None]).clamp(max=15).to(torch.int64)
+        word = (s.float().view(torch.int32).to(torch.int64) >> 16) | z.to(torch.int64)
+        codes[lost], word[lost] = 15, 0x7FCF
+        c = codes.view(n, h, PAGE_SIZE, dim // 32, 4, 8).permute(0, 1, 3, 2, 4, 5)  # [.., group, token, run, channel]
+        nibbles = torch.stack([c[..., [0, 4, 1, 5]], c[..., [2, 6, 3, 7]]])          # low and high ones of the four bytes
+        codes8 = (nibbles[0] | nibbles[1] << 4).reshape(n, h, 8, dim)
+        w = word.permute(0, 1, 3, 2).reshape(n, h, 1, dim // 2, 1)
+        words8 = torch.cat([w & 255, w >> 8], dim=-1).reshape(n, h, 1, dim)
+        out.append(torch.cat([codes8, words8], dim=2).to(torch.uint8))
+    return torch.stack(out, dim=2).contiguous()
+
+
 def poison_rows_(t: torch.Tensor) -> None:
     """Fill a bf16 tensor (view) with NaN; a uint8 (E4M3 code) tensor with the NaN code; an int8
     tensor with the code -128."""

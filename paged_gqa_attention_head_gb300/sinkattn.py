@@ -13,7 +13,7 @@ import math
 import os
 import threading
 import warnings
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libsinkattn.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA = range(5)
 STATUS_BAD_PAGE, STATUS_BAD_LENGTH, STATUS_BAD_CU_SEQLENS, STATUS_WAIT_TIMEOUT = 1, 2, 4, 8
-STATUS_VALUE_RANGE = 16
+STATUS_VALUE_RANGE, STATUS_NO_PAGES = 16, 32
 FLAG_LAUNCH_NEXT_EARLY, FLAG_START_EARLY = 1, 2
 PAGE_SIZE = 16
 
@@ -89,6 +89,14 @@ SIGNATURES = {
                                              _P, _SZ, _P]),
     "sinkattn_prefill_int8_report": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _F, _P, _P, _DP,
                                                     _P, _SZ, _P, _P]),
+    "sinkattn_append_kv_int4": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _P, _DP, _P, _SZ, _P]),
+    "sinkattn_unpack_kv_int4": (ctypes.c_int, [_P, _P, _I32, _P, _P, _DP, _P, _SZ, _P]),
+    "sinkattn_decode_int4_workspace_size": (ctypes.c_int, [_DP, ctypes.POINTER(_SZ)]),
+    "sinkattn_decode_int4": (ctypes.c_int, [_P, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P, _P]),
+    "sinkattn_prefill_int4_workspace_size": (ctypes.c_int, [_DP, _I32, ctypes.POINTER(_SZ)]),
+    "sinkattn_prefill_int4": (ctypes.c_int, [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _F, _P, _P, _DP, _P, _SZ, _P, _P]),
+    "sinkattn_plan_step": (ctypes.c_int, [_P, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _DP, _P, _SZ, _P]),
+    "sinkattn_release_pages": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _F, _P, _I32,
                                              ctypes.POINTER(RotaryDesc), _P, _P, _DP, _P, _SZ, _P]),
     "sinkattn_get_status": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_uint32), _P]),
@@ -681,7 +689,7 @@ def _status_args(index: int) -> tuple:
 def default_status(device=None) -> int:
     """Read and clear the status bits (STATUS_*) of the calls on a CUDA device (default: the current
     one) that were given no workspace_buf: append_kv, append_kv_fp8, append_kv_int8, qk_norm_rope,
-    decode_int8 and prefill_int8, from any thread or stream, eager or replayed from a graph.  It waits
+    decode_int8, prefill_int8, the 4-bit cache's calls and the page plan, from any thread or stream, eager or replayed from a graph.  It waits
     for the current stream; work on others counts once it has run.  Call it once before a first
     capture, so that the captured calls have a word to report to."""
     index = torch.device("cuda" if device is None else device).index
@@ -893,6 +901,215 @@ def prefill_int8(q, k, v, cu_seqlens, k_pages, v_pages, kv_scales, prefix_block_
           prefix_lens.data_ptr(), sk, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
           None if lse is None else lse.data_ptr(), desc, at, nbytes, status, stream)
     return out, lse
+
+
+# ---------------------------------------------------------------- 4-bit cache, page plan
+def _need_int4_cache(kv_pages, index: int) -> tuple:
+    """Pages, KV heads and head_dim of a 4-bit cache."""
+    _need_dense(kv_pages, "kv_pages", torch.uint8, index, 5)
+    pages, heads, two, rows, dim = kv_pages.shape
+    if two != 2 or rows != 9:
+        raise ValueError("kv_pages must be [num_pages, Hkv, 2, 9, D]")
+    return pages, heads, dim
+
+
+def append_kv_int4(k, v, slots, kv_pages, workspace_buf=None):
+    """Quantise new bf16 K/V rows into the slots of a 4-bit cache, in place (sinkattn_append_kv_int4):
+    kv_pages uint8 [num_pages, Hkv, 2, 9, D]; slots int64 [T] (page * 16 + place; negative: padding), for
+    example a StepPlan's; k, v [T, Hkv, D], each token's heads dense (parts of a fused projection's rows
+    will do)."""
+    dev = _need_cuda(k, "k")
+    T, Hkv, D, ks = _need_rows(k, "k", dev)
+    Tv, Hv, Dv, vs = _need_rows(v, "v", dev)
+    _need_dense(slots, "slots", torch.int64, dev, 1)
+    pages, Hp, Dp = _need_int4_cache(kv_pages, dev)
+    if (Tv, Hv, Dv) != (T, Hkv, D) or (Hp, Dp) != (Hkv, D):
+        raise ValueError("k, v must be [T, Hkv, D] matching the pages")
+    if slots.shape[0] != T:
+        raise ValueError("slots must have one entry per token")
+    ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
+    _call(dev, "sinkattn_append_kv_int4", k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, kv_pages.data_ptr(),
+          _desc_ref(0, Hkv, Hkv, D, pages, 0, 0, 0, 0), ws, nbytes, _raw_stream(dev))
+    return kv_pages
+
+
+def unpack_kv_int4(kv_pages, pages=None, k_out=None, v_out=None, workspace_buf=None):
+    """Pages of a 4-bit cache as bf16 pages [n, Hkv, 16, D], exactly (sinkattn_unpack_kv_int4): those
+    that pages (int32 [n]) names, or all.  Returns (k_pages, v_pages)."""
+    dev = _need_cuda(kv_pages, "kv_pages")
+    num_pages, Hkv, D = _need_int4_cache(kv_pages, dev)
+    n, wanted = num_pages, None
+    if pages is not None:
+        _need_dense(pages, "pages", torch.int32, dev, 1)
+        n, wanted = pages.shape[0], pages.data_ptr()
+    shape = (n, Hkv, PAGE_SIZE, D)
+    outs = []
+    for name, o in (("k_out", k_out), ("v_out", v_out)):
+        if o is None:
+            o = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
+        else:
+            _need_dense(o, name, torch.bfloat16, dev, 4)
+            if o.shape != shape:
+                raise ValueError(f"{name} must be [n, Hkv, 16, D] = {shape}")
+        outs.append(o)
+    ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
+    _call(dev, "sinkattn_unpack_kv_int4", kv_pages.data_ptr(), wanted, n, outs[0].data_ptr(), outs[1].data_ptr(),
+          _desc_ref(0, Hkv, Hkv, D, num_pages, 0, 0, 0, 0), ws, nbytes, _raw_stream(dev))
+    return outs[0], outs[1]
+
+
+def decode_int4_workspace_size(desc: PagedDesc) -> int:
+    """Bytes of workspace that decode_int4 needs for desc on the current device."""
+    c = _SZ()
+    _check(load().sinkattn_decode_int4_workspace_size(ctypes.byref(desc), ctypes.byref(c)),
+           "decode_int4_workspace_size")
+    return c.value
+
+
+def prefill_int4_workspace_size(desc: PagedDesc, total_tokens: int) -> int:
+    """Bytes of workspace with which prefill_int4 works fastest for desc on the current device (256
+    are enough for it to work)."""
+    c = _SZ()
+    _check(load().sinkattn_prefill_int4_workspace_size(ctypes.byref(desc), total_tokens, ctypes.byref(c)),
+           "prefill_int4_workspace_size")
+    return c.value
+
+
+def decode_int4(q, kv_pages, block_table, seq_lens, sinks=None, scale=None, out=None, lse=None, workspace_buf=None,
+                return_lse=True, window=0, max_sms=0, wait_limit_us=0):
+    """Split-KV paged decode over a 4-bit cache, uint8 [num_pages, Hkv, 2, 9, D] (sinkattn_decode_int4).
+    Status bits go to workspace_buf's header, without one to default_status.  Returns (out, lse)."""
+    dev = _need_cuda(q, "q")
+    _need_dense(q, "q", torch.bfloat16, dev, 3)
+    _need_dense(block_table, "block_table", torch.int32, dev, 2)
+    _need_dense(seq_lens, "seq_lens", torch.int32, dev, 1)
+    B, Hq, D = q.shape
+    pages, Hkv, Dp = _need_int4_cache(kv_pages, dev)
+    n, columns = block_table.shape
+    if Dp != D:
+        raise ValueError("kv_pages must be [num_pages, Hkv, 2, 9, D] matching q")
+    if n != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table / seq_lens rows must equal the batch")
+    sk = _need_sinks(sinks, Hq, dev)
+    out, lse = _attention_outputs(q, out, lse, return_lse, dev)
+    key = (B, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
+    desc, stream = _desc_ref(*key), _raw_stream(dev)
+    if workspace_buf is None:
+        ws = _stream_workspace(_int8_size("sinkattn_decode_int4_workspace_size", dev, desc, key), dev, stream, "decode",
+                               header=False)
+        at, nbytes, (status, _) = ws.data_ptr(), ws.numel(), _status_args(dev)
+    else:
+        (at, nbytes), status = _workspace_args(workspace_buf, dev), None
+    _call(dev, "sinkattn_decode_int4", q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), sk,
+          D ** -0.5 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), desc, at,
+          nbytes, status, stream)
+    return out, lse
+
+
+def prefill_int4(q, k, v, cu_seqlens, kv_pages, prefix_block_table, prefix_lens, sinks=None, scale=None, out=None,
+                 lse=None, workspace_buf=None, return_lse=True, window=0, max_sms=0, wait_limit_us=0):
+    """Chunked prefill over a 4-bit paged prefix (sinkattn_prefill_int4); the new tokens' q, k, v bf16.
+    Status bits go to workspace_buf's header, without one to default_status.  Returns (out, lse)."""
+    dev = _need_cuda(q, "q")
+    _need_dense(q, "q", torch.bfloat16, dev, 3)
+    _need_dense(k, "k", torch.bfloat16, dev, 3)
+    _need_dense(v, "v", torch.bfloat16, dev, 3)
+    _need_dense(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    _need_dense(prefix_block_table, "prefix_block_table", torch.int32, dev, 2)
+    _need_dense(prefix_lens, "prefix_lens", torch.int32, dev, 1)
+    T, Hq, D = q.shape
+    pages, Hkv, Dp = _need_int4_cache(kv_pages, dev)
+    n, columns = prefix_block_table.shape
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or Dp != D:
+        raise ValueError("k / v must be [T, Hkv, D] matching q and the pages")
+    if cu_seqlens.shape[0] != n + 1 or prefix_lens.shape[0] != n:
+        raise ValueError("prefix_block_table / prefix_lens rows must equal the requests of cu_seqlens")
+    sk = _need_sinks(sinks, Hq, dev)
+    out, lse = _attention_outputs(q, out, lse, return_lse, dev)
+    key = (n, Hq, Hkv, D, pages, columns, window, max_sms, wait_limit_us)
+    desc, stream = _desc_ref(*key), _raw_stream(dev)
+    if workspace_buf is None:
+        ws = _stream_workspace(_int8_size("sinkattn_prefill_int4_workspace_size", dev, desc, key, T), dev, stream,
+                               "prefill")
+        at, nbytes, (status, _) = ws.data_ptr(), ws.numel(), _status_args(dev)
+    else:
+        (at, nbytes), status = _workspace_args(workspace_buf, dev), None
+    _call(dev, "sinkattn_prefill_int4", q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), T,
+          kv_pages.data_ptr(), prefix_block_table.data_ptr(), prefix_lens.data_ptr(), sk,
+          D ** -0.5 if scale is None else float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), desc, at,
+          nbytes, status, stream)
+    return out, lse
+
+
+class StepPlan(NamedTuple):
+    """What a serving step's calls take (plan_step), all on the device."""
+    cu_seqlens: torch.Tensor  # int32 [B + 1]
+    start_pos: torch.Tensor   # int32 [B] tokens held before the step (prefix lengths, append positions)
+    seq_lens: torch.Tensor    # int32 [B] and after it (what a decode attends)
+    positions: torch.Tensor   # int32 [max_tokens] of the packed rows; -1: padding, or a request not served
+    slots: torch.Tensor       # int64 [max_tokens] in the cache; -1 likewise
+    num_free: torch.Tensor    # int32 [1] pages left
+
+
+def _need_page_list(seq_lens, block_table, free_pages, num_free, index: int) -> tuple:
+    """Requests, columns of the table and pages of the pool."""
+    _need_dense(seq_lens, "seq_lens", torch.int32, index, 1)
+    _need_dense(block_table, "block_table", torch.int32, index, 2)
+    _need_dense(free_pages, "free_pages", torch.int32, index, 1)
+    _need_dense(num_free, "num_free", torch.int32, index, 1)
+    B, columns = block_table.shape
+    if seq_lens.shape[0] != B:
+        raise ValueError("block_table / seq_lens rows must equal the batch")
+    if num_free.shape[0] != 1:
+        raise ValueError("num_free must have one entry")
+    return B, columns, free_pages.shape[0]
+
+
+def plan_step(new_lens, seq_lens, block_table, free_pages, num_free, max_tokens, update=False,
+              workspace_buf=None) -> StepPlan:
+    """Block-table entries, slots, positions and lengths of a serving step, on the device
+    (sinkattn_plan_step).  new_lens, seq_lens int32 [B]: tokens that each request brings and holds;
+    block_table int32 [B, columns] is updated in place; free_pages int32 [num_pages], num_free int32 [1]:
+    the free pages, a stack; max_tokens: rows of the packed step (those behind the last request are
+    padding).  update: seq_lens and num_free take their new values in place, as a captured step needs;
+    else they stay, and the plan holds the new ones.  STATUS_NO_PAGES in workspace_buf's header, without one in
+    default_status, tells that some request was not served."""
+    dev = _need_cuda(new_lens, "new_lens")
+    _need_dense(new_lens, "new_lens", torch.int32, dev, 1)
+    B, columns, pages = _need_page_list(seq_lens, block_table, free_pages, num_free, dev)
+    if new_lens.shape[0] != B:
+        raise ValueError("new_lens must have one entry per request")
+    at = new_lens.device
+    cu = torch.empty(B + 1, dtype=torch.int32, device=at)
+    positions = torch.empty(max_tokens, dtype=torch.int32, device=at)
+    slots = torch.empty(max_tokens, dtype=torch.int64, device=at)
+    if update:
+        start, lens, left = torch.empty_like(seq_lens), seq_lens, num_free
+    else:
+        start, lens, left = seq_lens, torch.empty_like(seq_lens), torch.empty_like(num_free)
+    ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
+    _call(dev, "sinkattn_plan_step", new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+          num_free.data_ptr(), max_tokens, cu.data_ptr(), start.data_ptr() if update else None, lens.data_ptr(),
+          left.data_ptr(), positions.data_ptr(), slots.data_ptr(), _desc_ref(B, 1, 1, 64, pages, columns, 0, 0, 0), ws,
+          nbytes, _raw_stream(dev))
+    return StepPlan(cu, start, lens, positions, slots, left)
+
+
+def release_pages(done, seq_lens, block_table, free_pages, num_free, update=False, workspace_buf=None):
+    """The pages of the requests with done (bool [B]) back to the list of free pages, which is updated in
+    place, and their lengths to 0 (sinkattn_release_pages).  update as for plan_step.  Returns
+    (seq_lens, num_free)."""
+    dev = _need_cuda(done, "done")
+    _need_dense(done, "done", torch.bool, dev, 1)
+    B, columns, pages = _need_page_list(seq_lens, block_table, free_pages, num_free, dev)
+    if done.shape[0] != B:
+        raise ValueError("done must have one entry per request")
+    lens, left = (seq_lens, num_free) if update else (torch.empty_like(seq_lens), torch.empty_like(num_free))
+    ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
+    _call(dev, "sinkattn_release_pages", done.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+          num_free.data_ptr(), lens.data_ptr(), left.data_ptr(), _desc_ref(B, 1, 1, 64, pages, columns, 0, 0, 0), ws, nbytes,
+          _raw_stream(dev))
+    return lens, left
 
 
 ROTARY_SCALING = {"none": 0, "linear": 1, "yarn": 2, "wavelength": 3}
