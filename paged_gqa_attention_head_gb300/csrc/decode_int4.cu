@@ -1,27 +1,33 @@
 // Split-KV paged decode with per-head sinks over a 4-bit cache (append_int4.cu): value = s (code - z)
 // with a scale s and a zero code z for every token and 32 channels.
 //
-// The plan and the products are those of the INT8 decode: every warp takes an equal run of units,
-// S^T = K Q^T and O^T = V^T P^T on m16n8k16 f16 MMAs with the 16 tokens of a page, then head_dim, on
-// the M axis and the query heads on N, and a merge of the split sequences' states.  A page's K and V
-// of a head are one contiguous record of 18 D bytes, copied by one untiled bulk copy.
-// What four bits change is the arithmetic that a byte of the cache brings, so that is what the layout
-// and the kernel save on:
-//   * a code is taken as the f16 subnormal code * 2^-24: a 32-bit word of eight codes becomes four
-//     operand registers with four ANDs and one shift.  Every other pair stays four bits up, 16 times
-//     its value: for K the query's entries are a sixteenth there, for V the output rows are divided
-//     at the end.  The contraction runs over channels in the word's order, which is the query's too;
-//   * V comes by transposing 8x8 loads of 16-bit elements, four channels of a token: a register holds
-//     the same four channels of two neighbouring tokens, and the ANDs part the channels;
-//   * the words of a page come by 8x8 loads whose eight row addresses are the same: transposed,
-//     a lane gets its own token's word twice (the scale as a float: one AND; z as an f16 pair:
-//     another), plain, the words of its two neighbouring tokens (z as the pair that V needs);
-//   * z comes off on the tensor cores: for K a product of z with -sum of the group's q (in two f16
-//     parts), which the group's code products start from; for V one product of z with the group's P,
-//     subtracted once a step;
-//   * a group's K scores are multiplied by s in fp32 pairs; P of a group is taken times s, relative to
-//     the power of two above the largest V scale met, and rounded once to f16, as in the INT8 decode.
-// The running maximum moves only when a score passes it by more than 8 (log2), as there.
+// The plan is that of the INT8 decode: every warp takes an equal run of units of pages, the products
+// run on m16n8k16 f16 MMAs with online softmax, and a merge joins the split sequences' states.  A
+// page's K and V of a head are one contiguous record of 18 D bytes, copied by one untiled bulk copy.
+// What four bits change is the arithmetic that a byte of the cache brings (ALU instructions issue every
+// other cycle, an MMA takes the tensor cores 8 cycles and the ALU some 4 beside them), so that is what
+// the layout and the kernel save on:
+//   * a code is taken as the f16 subnormal code * 2^-24: a 32-bit word of eight codes becomes operand
+//     registers by ANDs alone.  The odd codes of a byte stay four bits up: for K 16 times their value,
+//     against a sixteenth of the query's entries; for V together with the even one beside it (one AND
+//     less), which the output rows are parted from at the end;
+//   * K's contraction runs over channels in the word's order, which is the query's too; V comes by
+//     transposing 8x8 loads of 16-bit elements, four channels of a token: a register holds the same four
+//     channels of two neighbouring tokens, and the ANDs part the channels;
+//   * the words of a page come by 8x8 loads whose eight row addresses are the same: plain, a lane gets
+//     the words of its two neighbouring tokens; transposed, its own token's word twice (the scale as
+//     a float: one AND);
+//   * z comes off K in the products: z times -sum of the group's q, for 16 heads s z for all groups
+//     in one bf16 product.  (Off the codes, one f16 addition for two of them: 162 us where this takes
+//     158 on the 0.71 GB batch below.)  It comes off V's codes by such additions (a product of z with P
+//     and a subtraction a step: 162 us too);
+//   * a group's K scores are multiplied by s in fp32; P of a group is taken times s, relative to the
+//     power of two above the largest V scale met, and rounded once to f16, as in the INT8 decode.
+// Groups of up to 8 heads: S^T = K Q^T and O^T = V^T P^T, tokens and channels on the M axis, heads on N,
+// with P transposed between them.  16 heads fill the M axis themselves: S = Q K^T and O = P V, P in place.
+// The running maximum moves only when a score passes it by more than 8 (log2).
+// FP8 MMAs (a code as the E4M3 subnormal code * 2^-9, half the ANDs, q in three E5M2 parts) are made of
+// conversions and f16 MMAs here: 226 us.
 #include <math.h>
 
 #include <mutex>
@@ -39,8 +45,13 @@ template <int D, int NH>
 struct Int4Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kPPU = D == 64 ? 8 : 4;               // pages of a unit: one copy stage of 9 KB
-    static constexpr int kStep = D == 64 && NH == 1 ? 4 : 2;   // pages whose scores are held at once
+    // Pages of a unit, one copy stage: what a unit costs beside its pages' arithmetic is ~100 instructions, so as
+    // many as two stages for each warp leave room for (head_dim 64: 4 pages 174 us where 8 take 158; 128 and 16
+    // heads, whose registers allow two CTAs an SM: 4 pages 98.7 us, 6 95.4).
+    static constexpr int kPPU = D == 64 ? 8 : NH == 1 ? 4 : 6;
+    // Pages whose scores are held at once: what a step costs beside them, against registers (head_dim 64: 2 pages
+    // 162 us, 4 158, 8 160; 128 and 16 heads: 1 page 105 us, 2 98.7, 3 97.0 (of 6 pages a unit; 2: 95.4), 4 107).
+    static constexpr int kStep = D == 64 && NH == 1 ? 4 : 2;
     static constexpr int kStages = 2;
     static constexpr int kRec = 9 * D;                         // K (or V) of a (page, head)
     static constexpr int kPageBytes = 2 * kRec;
@@ -55,6 +66,50 @@ constexpr float kMaxSlack = 8.f; // the running maximum moves when a score passe
 constexpr float kStateDown = 1.f / 32768.f;  // states leave with their sums over 2^(kPShift + kMaxSlack)
 constexpr float kUp24 = 16777216.f;          // 2^24
 constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;  // pairs of codes in place, and 16 times them
+constexpr uint32_t kBoth = 0x00FF00FFu;                      // pairs of (even code + 16 odd code)
+
+// Scale of the word in the upper or the lower half of a pair.
+__device__ __forceinline__ float scale_hi(uint32_t w) { return __uint_as_float(w & 0xFFF00000u); }
+__device__ __forceinline__ float scale_lo(uint32_t w) { return __uint_as_float((w << 16) & 0xFFF00000u); }
+// Over the four lanes that share lane >> 2.
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+// Bytes 1 and 3 of a word as a pair.
+__device__ __forceinline__ uint32_t high_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
+// x + z * m in f16 pairs (exact here: multiples of 2^-24 below 2^-16).
+__device__ __forceinline__ uint32_t fma_h2(uint32_t z, uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(z), "r"(m), "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
+}
+// D = A B, bf16.
+__device__ __forceinline__ void mma_bf16_16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The product s z of a word, twice, in bf16 (exact: four bits times four).
+__device__ __forceinline__ uint32_t scale_times_z(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 z;\n\tsub.rn.bf16x2 z, %1, %2;\n\tmul.rn.bf16x2 %0, z, %3;\n\t}"
+        : "=r"(r)
+        : "r"(((w & 15u) * 0x10001u) | 0x43004300u), "r"(0x43004300u), "r"((w & 0xFFF0u) * 0x10001u));
+    return r;
+}
 
 // What the arithmetic needs of a unit.
 struct __align__(16) UnitMeta4 {
@@ -156,9 +211,10 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
     uint64_t *wbar = bars + wid * S;
     UnitMeta4 *wunit = s_unit + wid * S;
 
-    // The copy side's position, its sequence's length, the first unit of its segment, and the units
-    // copied so far.
-    Cursor pc;
+    // The copy side: its unit's sequence, KV head and place in the list (pb units in all), the first unit
+    // of its segment and the units copied so far; and what follows from the sequence: its length, the
+    // first visible page, the visible pages and its row of the block table from there.
+    int b, g, p, pb, p_seg0, produced = 0;
     {
         int lo = 0, hi = a.B - 1;
         while (lo < hi) {
@@ -168,82 +224,98 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
             else
                 hi = mid - 1;
         }
-        pc.b = lo;
-        pc.pb = s_prefix[lo + 1] - s_prefix[lo];
+        b = lo;
+        pb = s_prefix[lo + 1] - s_prefix[lo];
         const int local = (int)(u_begin - (int64_t)a.Hkv * s_prefix[lo]);
-        pc.g = local / pc.pb;
-        pc.p = local % pc.pb;
+        g = local / pb;
+        p = p_seg0 = local % pb;
     }
-    int pL = length_of(a, pc.b), p_seg0 = pc.p, produced = 0;
-
-    // Block-table window: lane l holds the entry of visible page win_p0 + l of sequence win_b (-1 past
-    // its last page); the entries of the next 32 pages are loaded with it.
-    int win_b = -1, win_p0 = 0, win_val = -1, nxt_val = -1;
-    auto entry = [&](int b, int first, int npv, int q) {
-        return q < npv ? a.block_table[(int64_t)b * a.max_pages + first + q] : -1;
+    int L, first, npv;
+    const int32_t *row;
+    // Lane l holds the row's entry of visible page win + l (-1 past the last); those of the next window of
+    // kWin pages, whole units, are loaded with it.
+    constexpr int kWin = 32 / U * U;
+    int win, win_val, nxt_val;
+    auto entry = [&](int q) { return q < npv ? row[q] : -1; };
+    auto sequence = [&](int at) {
+        L = length_of(a, b);
+        first = first_page<kWindow>(a, L);
+        npv = (L + kPageSize - 1) / kPageSize - first;
+        row = a.block_table + (int64_t)b * a.max_pages + first;
+        win = at - at % kWin;
+        win_val = entry(win + lane);
+        nxt_val = entry(win + kWin + lane);
     };
+    sequence(p * U);
     const uint64_t policy = l2_policy_evict_first();
     // The next unit, if there is one, into a stage: lanes 0 .. U - 1 take a page each.
     auto produce = [&](int stage) {
         if (produced == n_units) return;
-        const Cursor c = pc;
-        const int L = pL;
         ++produced;
-        int flags = 0;
-        if (c.p == p_seg0) flags |= kStart;
-        if (c.p == c.pb - 1 || produced == n_units) flags |= kEnd;
-        if (c.p == c.pb - 1 && p_seg0 == 0) flags |= kWhole;
-        if (++pc.p == pc.pb) {
-            pc.p = p_seg0 = 0;
-            if (++pc.g == a.Hkv) {
-                pc.g = 0;
-                do {
-                    ++pc.b;
-                    pc.pb = pc.b < a.B ? s_prefix[pc.b + 1] - s_prefix[pc.b] : 1;
-                } while (pc.b < a.B && pc.pb == 0);
-                if (pc.b < a.B) pL = length_of(a, pc.b);
-            }
+        const int pp0 = p * U;
+        if (pp0 >= win + kWin) {  // warp-uniform
+            win += kWin;
+            win_val = nxt_val;
+            nxt_val = entry(win + kWin + lane);
         }
-        const int first = first_page<kWindow>(a, L);
-        const int npv = (L + kPageSize - 1) / kPageSize - first;  // pages the query sees
-        const int pp0 = c.p * U, p0 = pp0 & ~31;
-        if (c.b != win_b || p0 != win_p0) {  // warp-uniform
-            win_val = c.b == win_b && p0 == win_p0 + 32 ? nxt_val : entry(c.b, first, npv, p0 + lane);
-            nxt_val = entry(c.b, first, npv, p0 + 32 + lane);
-            win_b = c.b;
-            win_p0 = p0;
-        }
-        const int pg = __shfl_sync(0xffffffffu, win_val, (pp0 + (lane & (U - 1))) & 31);
-        const bool in = lane < U && pp0 + lane < npv, ok = in && pg >= 0 && pg < a.num_pages;
-        if (in && !ok) set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+        const int pg = __shfl_sync(0xffffffffu, win_val, (pp0 - win + lane) & 31);
+        const bool in = lane < U && pp0 + lane < npv, ok = in && (uint32_t)pg < (uint32_t)a.num_pages;
         const uint32_t oks = __ballot_sync(0xffffffffu, ok);
         uint64_t *bar = &wbar[stage];
+        const bool last = p == pb - 1;
         if (lane == 0) {
+            const int flags = (p == p_seg0 ? kStart : 0) | (last || produced == n_units ? kEnd : 0) |
+                              (last && p_seg0 == 0 ? kWhole : 0);
             const int key0 = kPageSize * (first + pp0);  // position of the unit's first key
             UnitMeta4 &m = wunit[stage];
-            *reinterpret_cast<int4 *>(&m.b) = make_int4(c.b, c.g, flags, (int)oks);
+            *reinterpret_cast<int4 *>(&m.b) = make_int4(b, g, flags, (int)oks);
             *reinterpret_cast<int2 *>(&m.end) = make_int2(L - key0, kWindow ? L - a.window - key0 : 0);
-            if (oks)
-                mbar_arrive_expect_tx(bar, __popc(oks) * C::kPageBytes);
-            else
-                mbar_arrive(bar);
+            mbar_arrive_expect_tx(bar, __popc(oks) * C::kPageBytes);
         }
         __syncwarp();
         if (ok)
             bulk_load_hint(wbuf + stage * C::kStageBytes + lane * C::kPageBytes,
-                           static_cast<const uint8_t *>(a.kv_int4) + ((int64_t)pg * a.Hkv + c.g) * C::kPageBytes,
+                           static_cast<const uint8_t *>(a.kv_int4) + ((int64_t)pg * a.Hkv + g) * C::kPageBytes,
                            C::kPageBytes, bar, policy);
+        else if (in)
+            set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
+        ++p;
+        if (last) {
+            p = p_seg0 = 0;
+            if (++g == a.Hkv) {
+                g = 0;
+                do {
+                    ++b;
+                    pb = b < a.B ? s_prefix[b + 1] - s_prefix[b] : 1;
+                } while (b < a.B && pb == 0);
+                if (b < a.B) sequence(0);
+            } else if (win != 0) {
+                win = 0;
+                win_val = entry(lane);
+                nxt_val = entry(kWin + lane);
+            }
+        }
     };
 
 #pragma unroll 1
     for (int st = 0; st < S; ++st) produce(st);
 
     const int gr = lane >> 2, t4 = lane & 3;
-    uint32_t qf[2 * NG][NH][2];
-    uint32_t qz[NG][NH];              // -sum of the group's q as two f16 parts (lanes t4 = 0, else 0)
-    float acc[2 * NG][NH][4];         // O^T * 2^-24: rows 32g + 8 (gr / 2) + gr % 2 + 4x, 16 times those 2 further
-    float mr[NH][2];                  // running maximum of the scores (log2)
-    float2 nr[NH], ls[NH];            // -(mr - kPShift), 0 before the first key; sums of P
+    // q in the order of its MMA operand: [2 i + x][e NH + nt] of head 8 nt + gr, channels 32 i + 8 t4 + 4 x + (0, 1)
+    // (e 0) and a sixteenth of + (2, 3) (e 1)
+    uint32_t qf[2 * NG][2 * NH];
+    // z of K: -sum of the group's q, of group t4 (else 0): for 8 heads two f16 parts against z; for 16 three
+    // bf16 parts against s z, all groups in one product (six MMAs a page less at head_dim 128)
+    uint32_t qz[NH == 1 ? NG : 2][2];  // (16 heads: [part][nt])
+    const uint32_t zoff = 8 * D + 2 * (16 * min(t4, NG - 1) + gr);  // the lane's word for that
+    // O * 2^-24.  8 heads: [m-tile 2 i + x][.]: channels 32 i + 8 (gr / 2) + gr % 2 + 4 x (and of these plus 16
+    // times the ones 2 further) of heads 2 t4, 2 t4 + 1; 16 heads: [4 i + n]: channels 32 i + 8 t4 + (0, 1) (n even)
+    // + 2 n (and of those plus 16 times the ones 2 further, n odd) of heads gr, gr + 8
+    float acc[2 * NG * NH][4];
+    // of the lane's two heads (8: 2 t4, 2 t4 + 1; 16: gr, gr + 8): running maximum of the scores (log2), a score
+    // above which (before its factor f0) it moves, -(maximum - kPShift) (0 before the first key), sum of P
+    float mr[2], thr[2], nr[2];
+    float2 ls[NH];                    // 8 heads: of both; 16: of each, from even and from odd tokens
     float f0 = 0.f;                   // score factor
     float v_top = 0.f, v_inv = 0.f;   // 2^E and 2^-E
 
@@ -270,10 +342,10 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                 for (int i = 0; i < NG; ++i) {  // channels 32 i + 8 t4 .. + 7
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (h < a.G) w = *reinterpret_cast<const uint4 *>(qg + h * D + 32 * i + 8 * t4);
-                    qf[2 * i][nt][0] = w.x;
-                    qf[2 * i][nt][1] = w.y;
-                    qf[2 * i + 1][nt][0] = w.z;
-                    qf[2 * i + 1][nt][1] = w.w;
+                    qf[2 * i][nt] = w.x;
+                    qf[2 * i][NH + nt] = w.y;
+                    qf[2 * i + 1][nt] = w.z;
+                    qf[2 * i + 1][NH + nt] = w.w;
                     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -291,36 +363,48 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
 #pragma unroll
             for (int kk = 0; kk < 2 * NG; ++kk)
 #pragma unroll
-                for (int nt = 0; nt < NH; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t w = qf[kk][nt][e];
-                        const float d = e ? down * 0.0625f : down;
-                        qf[kk][nt][e] = pack_f16x2(__uint_as_float(w << 16) * d, __uint_as_float(w & 0xFFFF0000u) * d);
-                    }
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int nt = 0; nt < NH; ++nt) {
-                    // sum of the group's q as the codes meet it: every row the same, columns 2 t4, 2 t4 + 1
-                    constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;
-                    float o[4];
-                    mma_f16_16816_from(o, 0.f, 0.f, one, one, one16, one16, qf[2 * i][nt][0], qf[2 * i][nt][1]);
-                    mma_f16_16816(o, one, one, one16, one16, qf[2 * i + 1][nt][0], qf[2 * i + 1][nt][1]);
-                    const float x = __shfl_sync(0xffffffffu, o[0], gr >> 1), y = __shfl_sync(0xffffffffu, o[1], gr >> 1);
-                    const float neg = -((gr & 1) ? y : x) * kUp24, hi = f16_of(neg);
-                    qz[i][nt] = t4 == 0 ? pack_f16x2(hi, neg - hi) : 0u;
+                for (int e = 0; e < 2 * NH; ++e) {
+                    const uint32_t w = qf[kk][e];
+                    const float d = e >= NH ? down * 0.0625f : down;
+                    qf[kk][e] = pack_f16x2(__uint_as_float(w << 16) * d, __uint_as_float(w & 0xFFFF0000u) * d);
                 }
+            if (NH == 2) qz[0][0] = qz[0][1] = qz[1][0] = qz[1][1] = 0u;
 #pragma unroll
-            for (int mt = 0; mt < 2 * NG; ++mt)
+            for (int i = 0; i < NG; ++i) {
+                // sums of the group's q * 2^-24 as the codes meet it
+                constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;
+                float o[4];
+                if (NH == 1) {  // every row the same: heads 2 t4, 2 t4 + 1
+                    mma_f16_16816_from(o, 0.f, 0.f, one, one, one16, one16, qf[2 * i][0], qf[2 * i][1]);
+                    mma_f16_16816(o, one, one, one16, one16, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                    const float x = __shfl_sync(0xffffffffu, o[0], gr >> 1), y = __shfl_sync(0xffffffffu, o[1], gr >> 1);
+                    const float neg = ((gr & 1) ? y : x) * -kUp24, hi = f16_of(neg);
+                    qz[i][0] = t4 == i ? pack_f16x2(hi, 0.f) : 0u;
+                    qz[i][1] = t4 == i ? pack_f16x2(neg - hi, 0.f) : 0u;
+                } else {  // every column the same: heads gr and gr + 8
+                    mma_f16_16816_from(o, 0.f, 0.f, qf[2 * i][0], qf[2 * i][1], qf[2 * i][2 * NH - 2], qf[2 * i][2 * NH - 1], one, one16);
+                    mma_f16_16816(o, qf[2 * i + 1][0], qf[2 * i + 1][1], qf[2 * i + 1][2 * NH - 2], qf[2 * i + 1][2 * NH - 1], one, one16);
 #pragma unroll
-                for (int nt = 0; nt < NH; ++nt)
-                    acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < NH; ++nt) {
-                mr[nt][0] = mr[nt][1] = -INFINITY;
-                nr[nt] = ls[nt] = make_float2(0.f, 0.f);
+                    for (int nt = 0; nt < NH; ++nt) {
+                        const float neg = -o[2 * nt];
+                        const float p0 = __bfloat162float(__float2bfloat16_rn(neg));
+                        const float p1 = __bfloat162float(__float2bfloat16_rn(neg - p0));
+                        if (t4 == i) {
+                            qz[0][nt] = pack_bf16x2(p0, p1);
+                            qz[1][nt] = pack_bf16x2(neg - p0 - p1, 0.f);
+                        }
+                    }
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 2 * NG * NH; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mr[e] = thr[e] = -INFINITY;
+                nr[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < NH; ++e) ls[e] = make_float2(0.f, 0.f);
             v_top = v_inv = 0.f;
         }
 
@@ -337,81 +421,118 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
             auto nv = [&](int j) { return (cur.w >> (j0 + j)) & 1 ? min(kPageSize, vis.x - kPageSize * (j0 + j)) : 0; };
             auto lo = [&](int j) { return kWindow ? vis.y - kPageSize * (j0 + j) : 0; };
 
-            // S^T = K Q^T per page: rows tokens, columns heads; a group's part times its tokens' scales
-            float2 s[W][NH][2];
+            // Scores of the step's pages, a group's part times its tokens' scales, and the V scales.
+            // 8 heads: [.][token half][token gr]: heads 2 t4, 2 t4 + 1.  16: [.][token half][head half]: tokens 2 t4 and + 1.
+            float2 s[W][2][NH];
+            float2 vs[W][NG][2];  // 8 heads: .x and .y of the lane's tokens gr, gr + 8 in [0]; 16: of its pairs of tokens
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t kb = at + j * C::kPageBytes;
-                uint32_t kc[NG][2], kw[NG][2];
+                uint32_t kc[NG][2], kw[NG][2], vw[NG][2];
+                const uint32_t z0 = lds_u16(kb + zoff), z1 = lds_u16(kb + zoff + 16);
 #pragma unroll
                 for (int i = 0; i < NG / 2; ++i) {
                     ldsm_x4(kb + 512 * i + 16 * lane, kc[2 * i][0], kc[2 * i][1], kc[2 * i + 1][0], kc[2 * i + 1][1]);
-                    ldsm_x4_t(kb + 8 * D + 64 * i + 16 * (lane >> 3), kw[2 * i][0], kw[2 * i][1], kw[2 * i + 1][0],
-                              kw[2 * i + 1][1]);
-                }
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    const uint32_t w0 = kc[i][0], w1 = kc[i][1], h0 = w0 >> 8, h1 = w1 >> 8;
-                    const float s0 = __uint_as_float(kw[i][0] & 0xFFF00000u), s1 = __uint_as_float(kw[i][1] & 0xFFF00000u);
-#pragma unroll
-                    for (int nt = 0; nt < NH; ++nt) {
-                        float o[4];
-                        mma_f16_16816_from(o, 0.f, 0.f, kw[i][0] & kEven, kw[i][1] & kEven, 0u, 0u, qz[i][nt], 0u);
-                        mma_f16_16816(o, w0 & kEven, w1 & kEven, w0 & kOdd, w1 & kOdd, qf[2 * i][nt][0], qf[2 * i][nt][1]);
-                        mma_f16_16816(o, h0 & kEven, h1 & kEven, h0 & kOdd, h1 & kOdd, qf[2 * i + 1][nt][0],
-                                      qf[2 * i + 1][nt][1]);
-                        const float2 x = make_float2(o[0], o[1]), y = make_float2(o[2], o[3]);
-                        s[j][nt][0] = i ? ffma2(x, make_float2(s0, s0), s[j][nt][0]) : fmul2(x, make_float2(s0, s0));
-                        s[j][nt][1] = i ? ffma2(y, make_float2(s1, s1), s[j][nt][1]) : fmul2(y, make_float2(s1, s1));
+                    const uint32_t wa = kb + 8 * D + 64 * i + 16 * (lane >> 3);
+                    if (NH == 1) {
+                        ldsm_x4_t(wa, kw[2 * i][0], kw[2 * i][1], kw[2 * i + 1][0], kw[2 * i + 1][1]);
+                        ldsm_x4_t(wa + C::kRec, vw[2 * i][0], vw[2 * i][1], vw[2 * i + 1][0], vw[2 * i + 1][1]);
+                    } else {
+                        ldsm_x4(wa, kw[2 * i][0], kw[2 * i][1], kw[2 * i + 1][0], kw[2 * i + 1][1]);
+                        ldsm_x4(wa + C::kRec, vw[2 * i][0], vw[2 * i][1], vw[2 * i + 1][0], vw[2 * i + 1][1]);
                     }
                 }
-                if (ragged) {
-                    const int n = nv(j), l = lo(j);
-                    const bool ok0 = gr < n && gr >= l, ok1 = gr + 8 < n && gr + 8 >= l;
+                if (NH == 1) {
+                    const uint32_t a0 = z0 & 15u, a1 = z1 & 15u;
 #pragma unroll
-                    for (int nt = 0; nt < NH; ++nt) {
-                        if (!ok0) s[j][nt][0] = make_float2(-INFINITY, -INFINITY);
-                        if (!ok1) s[j][nt][1] = make_float2(-INFINITY, -INFINITY);
+                    for (int i = 0; i < NG; ++i) {
+                        const uint32_t w0 = kc[i][0], w1 = kc[i][1], h0 = w0 >> 8, h1 = w1 >> 8;
+                        const float s0 = scale_hi(kw[i][0]), s1 = scale_hi(kw[i][1]);
+                        float o[4];
+                        mma_f16_16816_from(o, 0.f, 0.f, a0, a1, a0, a1, qz[i][0], qz[i][1]);
+                        mma_f16_16816(o, w0 & kEven, w1 & kEven, w0 & kOdd, w1 & kOdd, qf[2 * i][0], qf[2 * i][1]);
+                        mma_f16_16816(o, h0 & kEven, h1 & kEven, h0 & kOdd, h1 & kOdd, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                        // (one by one: a pair of one scale would be a move)
+                        s[j][0][0].x = i ? fmaf(o[0], s0, s[j][0][0].x) : o[0] * s0;
+                        s[j][0][0].y = i ? fmaf(o[1], s0, s[j][0][0].y) : o[1] * s0;
+                        s[j][1][0].x = i ? fmaf(o[2], s1, s[j][1][0].x) : o[2] * s1;
+                        s[j][1][0].y = i ? fmaf(o[3], s1, s[j][1][0].y) : o[3] * s1;
+                        vs[j][i][0] = make_float2(scale_hi(vw[i][0]), scale_hi(vw[i][1]));
+                    }
+                } else {
+                    const uint32_t sz[2] = {scale_times_z(z0), scale_times_z(z1)};
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float o[4];
+                        mma_bf16_16816_new(o, qz[0][0], qz[0][1], qz[1][0], qz[1][1], sz[n], sz[n]);
+                        s[j][n][0] = make_float2(o[0], o[1]);
+                        s[j][n][NH - 1] = make_float2(o[2], o[3]);
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            const uint32_t w = kc[i][n], h = w >> 8;
+                            const uint32_t(&x)[2 * NH] = qf[2 * i], (&y)[2 * NH] = qf[2 * i + 1];
+                            mma_f16_16816_from(o, 0.f, 0.f, x[0], x[1], x[2 * NH - 2], x[2 * NH - 1], w & kEven, w & kOdd);
+                            mma_f16_16816(o, y[0], y[1], y[2 * NH - 2], y[2 * NH - 1], h & kEven, h & kOdd);
+                            const float2 sc = make_float2(scale_lo(kw[i][n]), scale_hi(kw[i][n]));
+                            s[j][n][0] = ffma2(make_float2(o[0], o[1]), sc, s[j][n][0]);
+                            s[j][n][NH - 1] = ffma2(make_float2(o[2], o[3]), sc, s[j][n][NH - 1]);
+                            vs[j][i][n] = make_float2(scale_lo(vw[i][n]), scale_hi(vw[i][n]));
+                        }
                     }
                 }
             }
-            // V scales of the lane's tokens
-            float vs[W][NG][2];
-            float vmx = 0.f;
+            if (ragged) {  // hidden tokens: no score, and no scale, whatever lies there
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    const int n = nv(j), l = lo(j);
+                    auto hidden = [&](int t) { return t >= n || t < l; };
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (NH == 1) {
+                            if (!hidden(gr + 8 * r)) continue;
+                            s[j][r][0] = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+                            for (int i = 0; i < NG; ++i) (r ? vs[j][i][0].y : vs[j][i][0].x) = 0.f;
+                        } else {
+                            const bool x = hidden(2 * t4 + 8 * r), y = hidden(2 * t4 + 1 + 8 * r);
+#pragma unroll
+                            for (int e = 0; e < NH; ++e) {
+                                if (x) s[j][r][e].x = -INFINITY;
+                                if (y) s[j][r][e].y = -INFINITY;
+                            }
+#pragma unroll
+                            for (int i = 0; i < NG; ++i) {
+                                if (x) vs[j][i][r].x = 0.f;
+                                if (y) vs[j][i][r].y = 0.f;
+                            }
+                        }
+                    }
+                }
+            }
+            // a score too far above the running maximum, or a V scale above every one so far
+            float vmx = 0.f, cm[2];
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                uint32_t w[NG][2];
-#pragma unroll
-                for (int i = 0; i < NG / 2; ++i)
-                    ldsm_x4_t(at + j * C::kPageBytes + C::kRec + 8 * D + 64 * i + 16 * (lane >> 3), w[2 * i][0], w[2 * i][1],
-                              w[2 * i + 1][0], w[2 * i + 1][1]);
-                const int n = nv(j), l = lo(j);
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        if (ragged && (gr + 8 * r >= n || gr + 8 * r < l)) w[i][r] = 0;  // whatever lies there
-                        vs[j][i][r] = __uint_as_float(w[i][r] & 0xFFF00000u);
+                    for (int r = 0; r < NH; ++r) vmx = fmax3(vmx, vs[j][i][r].x, vs[j][i][r].y);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x[4];  // the lane's scores of its head e
+                    if (NH == 1) {
+                        x[0] = e ? s[j][0][0].y : s[j][0][0].x;
+                        x[1] = e ? s[j][1][0].y : s[j][1][0].x;
+                    } else {
+                        x[0] = s[j][0][e * (NH - 1)].x, x[1] = s[j][0][e * (NH - 1)].y;
+                        x[2] = s[j][1][e * (NH - 1)].x, x[3] = s[j][1][e * (NH - 1)].y;
                     }
-#pragma unroll
-                for (int i = 0; i < NG; ++i) vmx = fmax3(vmx, vs[j][i][0], vs[j][i][1]);
-            }
-            // a score too far above the running maximum, or a V scale above every one so far
-            float cm[NH][2];
-            bool raise = vmx > v_top;
-#pragma unroll
-            for (int nt = 0; nt < NH; ++nt) {
-                cm[nt][0] = fmaxf(s[0][nt][0].x, s[0][nt][1].x);
-                cm[nt][1] = fmaxf(s[0][nt][0].y, s[0][nt][1].y);
-#pragma unroll
-                for (int j = 1; j < W; ++j) {
-                    cm[nt][0] = fmax3(cm[nt][0], s[j][nt][0].x, s[j][nt][1].x);
-                    cm[nt][1] = fmax3(cm[nt][1], s[j][nt][0].y, s[j][nt][1].y);
+                    cm[e] = j ? fmax3(cm[e], x[0], x[1]) : fmaxf(x[0], x[1]);
+                    if (NH == 2) cm[e] = fmax3(cm[e], x[2], x[3]);
                 }
-                raise |= cm[nt][0] * f0 > mr[nt][0] + kMaxSlack || cm[nt][1] * f0 > mr[nt][1] + kMaxSlack;
             }
-            if (__any_sync(0xffffffffu, raise)) {
-                // O^T moves by an exact power of two for the scales, and by what the maxima grew
+            if (__any_sync(0xffffffffu, vmx > v_top || cm[0] > thr[0] || cm[1] > thr[1])) {
+                // O moves by an exact power of two for the scales, and by what the maxima grew
                 const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vmx));
                 float move = 1.f;
                 if (__uint_as_float(vb) > v_top) {
@@ -420,29 +541,27 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                     move = v_top * v_inv;
                     v_top = top;
                 }
+                float al[2];
 #pragma unroll
-                for (int nt = 0; nt < NH; ++nt) {
-                    float al[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = col_max(cm[nt][e]) * f0;
-                        const float mn = x > mr[nt][e] + kMaxSlack ? x : mr[nt][e];
-                        al[e] = mr[nt][e] == -INFINITY ? 0.f : fast_exp2(mr[nt][e] - mn);
-                        mr[nt][e] = mn;
-                    }
-                    nr[nt] = make_float2(mr[nt][0] == -INFINITY ? 0.f : kPShift - mr[nt][0],
-                                         mr[nt][1] == -INFINITY ? 0.f : kPShift - mr[nt][1]);
-                    ls[nt] = fmul2(ls[nt], make_float2(al[0], al[1]));
-                    al[0] *= move;
-                    al[1] *= move;
-#pragma unroll
-                    for (int mt = 0; mt < 2 * NG; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[mt][nt][e] *= al[e & 1];
+                for (int e = 0; e < 2; ++e) {
+                    const float x = NH == 1 ? col_max(cm[e]) : quad_max(cm[e]);
+                    const float mn = x > thr[e] ? x * f0 : mr[e];
+                    al[e] = mr[e] == -INFINITY ? 0.f : fast_exp2(mr[e] - mn);
+                    mr[e] = mn;
+                    thr[e] = (mn + kMaxSlack) / f0;
+                    nr[e] = mn == -INFINITY ? 0.f : kPShift - mn;
                 }
+#pragma unroll
+                for (int e = 0; e < NH; ++e)
+                    ls[e] = fmul2(ls[e], NH == 1 ? make_float2(al[0], al[1]) : make_float2(al[e], al[e]));
+                al[0] *= move;
+                al[1] *= move;
+#pragma unroll
+                for (int i = 0; i < 2 * NG * NH; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][e] *= al[NH == 1 ? e & 1 : e >> 1];
             }
-            // P, and O^T += V^T P^T, one 16-token k-step per page
-            float od[NG][NH][4];  // what z takes off, rows all the same
+            // P, and its products with V, one 16-token k-step per page
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t vb = at + j * C::kPageBytes + C::kRec;
@@ -453,44 +572,52 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                     ldsm_x4(vb + 8 * D + 64 * i + 16 * (lane >> 3), vz[2 * i][0], vz[2 * i][1], vz[2 * i + 1][0],
                             vz[2 * i + 1][1]);
                 }
+                const float2 f2 = make_float2(f0, f0), i2 = make_float2(v_inv, v_inv);
+                float2 px[2][NH];
 #pragma unroll
-                for (int nt = 0; nt < NH; ++nt) {
-                    const float2 f2 = make_float2(f0, f0), i2 = make_float2(v_inv, v_inv);
-                    float2 x = ffma2(s[j][nt][0], f2, nr[nt]), y = ffma2(s[j][nt][1], f2, nr[nt]);
-                    x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                    y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                    ls[nt] = fadd2(ls[nt], fadd2(x, y));
-                    x = fmul2(x, i2);
-                    y = fmul2(y, i2);
+                for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        const float2 p = fmul2(x, make_float2(vs[j][i][0], vs[j][i][0]));
-                        const float2 q = fmul2(y, make_float2(vs[j][i][1], vs[j][i][1]));
+                    for (int e = 0; e < NH; ++e) {
+                        const float2 x = ffma2(s[j][r][e], f2, NH == 1 ? make_float2(nr[0], nr[1]) : make_float2(nr[e], nr[e]));
+                        px[r][e] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        ls[e] = fadd2(ls[e], px[r][e]);
+                        px[r][e] = fmul2(px[r][e], i2);
+                    }
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    // codes less z, of the tokens 2 t4, 2 t4 + 1 ([0]) and 8 further ([1]); exact, multiples of 2^-24
+                    uint32_t v[4][2];  // even code of byte 0, with 16 odd, the same of byte 1
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        constexpr uint32_t m1 = 0xBC00BC00u, m17 = 0xCC40CC40u;  // -1, -17
+                        const uint32_t z = vz[i][r] & kEven, hi = high_bytes(vc[i][r]);
+                        v[0][r] = fma_h2(z, m1, vc[i][r] & kEven);
+                        v[1][r] = fma_h2(z, m17, vc[i][r] & kBoth);
+                        v[2][r] = fma_h2(z, m1, hi & kEven);
+                        v[3][r] = fma_h2(z, m17, hi);
+                    }
+                    if (NH == 1) {
                         // P^T fragments: transpose (token, head) blocks to (head, token)
-                        const uint32_t b0 = movmatrix_t(pack_f16x2(p.x, p.y)), b1 = movmatrix_t(pack_f16x2(q.x, q.y));
-                        const uint32_t z0 = vz[i][0] & kEven, z1 = vz[i][1] & kEven;
-                        if (j == 0)
-                            mma_f16_16816_from(od[i][nt], 0.f, 0.f, z0, z0, z1, z1, b0, b1);
-                        else
-                            mma_f16_16816(od[i][nt], z0, z0, z1, z1, b0, b1);
-                        const uint32_t w0 = vc[i][0], w1 = vc[i][1], h0 = w0 >> 8, h1 = w1 >> 8;
-                        mma_f16_16816(acc[2 * i][nt], w0 & kEven, w0 & kOdd, w1 & kEven, w1 & kOdd, b0, b1);
-                        mma_f16_16816(acc[2 * i + 1][nt], h0 & kEven, h0 & kOdd, h1 & kEven, h1 & kOdd, b0, b1);
+                        const float s0 = vs[j][i][0].x, s1 = vs[j][i][0].y;
+                        const uint32_t b0 = movmatrix_t(pack_f16x2(px[0][0].x * s0, px[0][0].y * s0));
+                        const uint32_t b1 = movmatrix_t(pack_f16x2(px[1][0].x * s1, px[1][0].y * s1));
+                        mma_f16_16816(acc[2 * i], v[0][0], v[1][0], v[0][1], v[1][1], b0, b1);
+                        mma_f16_16816(acc[2 * i + 1], v[2][0], v[3][0], v[2][1], v[3][1], b0, b1);
+                    } else {
+                        uint32_t p[2][2];  // [token half][head half]
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int e = 0; e < NH; ++e) {
+                                const float2 x = fmul2(px[r][e], vs[j][i][r]);
+                                p[r][e] = pack_f16x2(x.x, x.y);
+                            }
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            mma_f16_16816(acc[(4 * i + n) % (2 * NG * NH)], p[0][0], p[0][1], p[1][0], p[1][1], v[n][0], v[n][1]);
                     }
                 }
             }
-#pragma unroll
-            for (int mt = 0; mt < 2 * NG; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < NH; ++nt) {
-                    const float2 o = make_float2(od[mt / 2][nt][0], od[mt / 2][nt][1]);
-                    const float2 x = ffma2(o, make_float2(-1.f, -1.f), make_float2(acc[mt][nt][0], acc[mt][nt][1]));
-                    const float2 y = ffma2(o, make_float2(-16.f, -16.f), make_float2(acc[mt][nt][2], acc[mt][nt][3]));
-                    acc[mt][nt][0] = x.x;
-                    acc[mt][nt][1] = x.y;
-                    acc[mt][nt][2] = y.x;
-                    acc[mt][nt][3] = y.y;
-                }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -500,55 +627,63 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
             const bool whole = cur.z & kWhole;
             const int64_t slot = (int64_t)wglob + (int64_t)cur.x * a.Hkv + cur.y;
 #pragma unroll
-            for (int nt = 0; nt < NH; ++nt)
+            for (int e = 0; e < 2; ++e) {
+                const float L = NH == 1 ? col_sum(e ? ls[0].y : ls[0].x) : quad_sum(ls[e * (NH - 1)].x + ls[e * (NH - 1)].y);
+                const int hc = NH == 1 ? 2 * t4 + e : gr + 8 * e;  // head in the group
+                const int h = cur.y * a.G + hc;
+                // reference of the state: probabilities were taken against mr - kPShift
+                const float m = mr[e] == -INFINITY ? -INFINITY : mr[e] - kPShift;
+                float scl = kStateDown, lse2 = -INFINITY;
+                if (whole) {
+                    const float sk = a.sinks && hc < a.G ? a.sinks[h] * kLog2e : -INFINITY;
+                    const float M = fmaxf(m, sk);
+                    scl = 0.f;
+                    if (M != -INFINITY) {
+                        const float wm = m == -INFINITY ? 0.f : exp2f(m - M);
+                        const float den = L * wm + (sk == -INFINITY ? 0.f : exp2f(sk - M));
+                        scl = wm / den;
+                        lse2 = M + log2f(den);
+                    }
+                }
+                const float up = kUp24 * scl;
+                // the channels of an m-tile's (8 heads) or two n-tiles' (16) even codes, and odd ones
+                auto even = [&](float x) { return x * up * v_top; };
+                auto odd = [&](float both, float x) { return (both - x) * 0.0625f * up * v_top; };
+                auto put = [&](int ch, float4 v) {  // four channels from ch on
+                    if (hc >= a.G) return;
+                    if (whole)
+                        *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) + ((int64_t)cur.x * a.Hq + h) * D +
+                                                   ch) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                    else
+                        *reinterpret_cast<float4 *>(a.part_acc + (slot * a.G + hc) * D + ch) = v;
+                };
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float L = col_sum(e ? ls[nt].y : ls[nt].x);
-                    const int hc = nt * 8 + 2 * t4 + e;  // column (head in the group)
-                    const int h = cur.y * a.G + hc;
-                    // reference of the state: probabilities were taken against mr - kPShift
-                    const float m = mr[nt][e] == -INFINITY ? -INFINITY : mr[nt][e] - kPShift;
-                    float scl = kStateDown, lse2 = -INFINITY;
-                    if (whole) {
-                        const float sk = a.sinks && hc < a.G ? a.sinks[h] * kLog2e : -INFINITY;
-                        const float M = fmaxf(m, sk);
-                        scl = 0.f;
-                        if (M != -INFINITY) {
-                            const float wm = m == -INFINITY ? 0.f : exp2f(m - M);
-                            const float den = L * wm + (sk == -INFINITY ? 0.f : exp2f(sk - M));
-                            scl = wm / den;
-                            lse2 = M + log2f(den);
+                for (int i = 0; i < NG; ++i) {
+                    if (NH == 1) {
+                        // this lane's channels of the group: 8 (gr / 2) + gr % 2 + 0, 2, 4, 6; the lane beside
+                        // it has those between.  The even one takes the first four, the odd one the others.
+                        const float c0 = even(acc[2 * i][e]), c2 = odd(acc[2 * i][2 + e], acc[2 * i][e]);
+                        const float c4 = even(acc[2 * i + 1][e]), c6 = odd(acc[2 * i + 1][2 + e], acc[2 * i + 1][e]);
+                        const bool second = gr & 1;
+                        const float r0 = __shfl_xor_sync(0xffffffffu, second ? c0 : c4, 4);
+                        const float r1 = __shfl_xor_sync(0xffffffffu, second ? c2 : c6, 4);
+                        put(32 * i + 4 * gr, second ? make_float4(r0, c4, r1, c6) : make_float4(c0, r0, c2, r1));
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float(&y)[4] = acc[(4 * i + 2 * x) % (2 * NG * NH)], (&b)[4] = acc[(4 * i + 2 * x + 1) % (2 * NG * NH)];
+                            put(32 * i + 8 * t4 + 4 * x, make_float4(even(y[2 * e]), even(y[2 * e + 1]), odd(b[2 * e], y[2 * e]),
+                                                                     odd(b[2 * e + 1], y[2 * e + 1])));
                         }
                     }
-                    const float up = kUp24 * scl;
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        // this lane's channels of the group: 8 (gr / 2) + gr % 2 + 0, 2, 4, 6; the lane
-                        // beside it has those between.  The even one takes the first four, the odd one
-                        // the others.
-                        const float c0 = acc[2 * i][nt][e] * up * v_top, c2 = acc[2 * i][nt][2 + e] * 0.0625f * up * v_top;
-                        const float c4 = acc[2 * i + 1][nt][e] * up * v_top;
-                        const float c6 = acc[2 * i + 1][nt][2 + e] * 0.0625f * up * v_top;
-                        const bool odd = gr & 1;
-                        const float r0 = __shfl_xor_sync(0xffffffffu, odd ? c0 : c4, 4);
-                        const float r1 = __shfl_xor_sync(0xffffffffu, odd ? c2 : c6, 4);
-                        const float4 v = odd ? make_float4(r0, c4, r1, c6) : make_float4(c0, r0, c2, r1);
-                        if (hc >= a.G) continue;
-                        const int ch = 32 * i + 4 * gr;
-                        if (whole)
-                            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.out) +
-                                                       ((int64_t)cur.x * a.Hq + h) * D + ch) =
-                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                        else
-                            *reinterpret_cast<float4 *>(a.part_acc + (slot * a.G + hc) * D + ch) = v;
-                    }
-                    if (hc >= a.G || gr != 0) continue;
-                    if (!whole)
-                        *reinterpret_cast<float2 *>(a.part_ml + (slot * a.G + hc) * 2) =
-                            make_float2(m + kPShift + kMaxSlack, L * kStateDown);
-                    else if (a.lse)
-                        a.lse[(int64_t)cur.x * a.Hq + h] = lse2 * kLn2;
                 }
+                if (hc >= a.G || (NH == 1 ? gr : t4) != 0) continue;
+                if (!whole)
+                    *reinterpret_cast<float2 *>(a.part_ml + (slot * a.G + hc) * 2) =
+                        make_float2(m + kPShift + kMaxSlack, L * kStateDown);
+                else if (a.lse)
+                    a.lse[(int64_t)cur.x * a.Hq + h] = lse2 * kLn2;
+            }
         }
     }
     // Near the end of the grid the merge may take its place on the SMs; it waits for this grid before
