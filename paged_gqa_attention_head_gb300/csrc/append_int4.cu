@@ -31,74 +31,98 @@ constexpr float kScaleFloor4 = 7.888609052210118e-31f;  // 2^-100: smaller scale
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// min and max of bf16 pairs, NaN if either is.
 __device__ __forceinline__ uint32_t min_bf2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 __device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Scale of a group from its low <= 0 <= high.  The range is halved, so that it cannot overflow, and
-// rounded upwards: it passes 7.5 s (eight bits) if and only if the exact one does.
-__device__ __forceinline__ float scale4(float low, float high) {
-    const float half = __fsub_ru(0.5f * high, 0.5f * low);
-    const float s = __uint_as_float((__float_as_uint(__fdiv_ru(half, 7.5f)) + 0xFFFFFu) & 0xFFF00000u);
+// Scale of a group of range high + below (low = -below): the smallest s of four significant bits with
+// 7.5 s >= half the range (halved, so that it cannot overflow, and rounded upwards: it passes 7.5 s, eight
+// bits, if and only if the exact one does).  Half the range times 1/7.5, both rounded upwards, is no
+// less than the quotient and at most a rounding more, so its next number of four bits is s or the one above.
+__device__ __forceinline__ float scale4(float below, float high) {
+    const float half = __fadd_ru(0.5f * high, 0.5f * below);
+    const uint32_t up = (__float_as_uint(__fmul_ru(half, 0.13333334f)) + 0xFFFFFu) & 0xFFF00000u;
+    const float under = __uint_as_float(up - 0x100000u);
+    const float s = 7.5f * under >= half ? under : __uint_as_float(up);
     return s >= kScaleFloor4 ? s : 0.f;
 }
+static_assert(0.13333334f >= 1.0 / 7.5, "1/7.5 rounded upwards");
 
-// rint(x r + z) in the low bits; the sum snapped to multiples of 2^-11 first (6144 = 1.5 * 2^12).  It is
-// -0.5 or more but for an infinity, whose low bits are those of the code 0.
+// x r + z, snapped to multiples of 2^-11 by the exponent of z6144 = 6144 + z (1.5 * 2^12), then rounded:
+// the integer in the low bits.  (An approximate reciprocal will do: the snap takes off up to 2^-12.)
 __device__ __forceinline__ uint32_t code4(float x, float r, float z6144) {
-    const float q = fminf(fmaf(x, r, z6144) - 6144.f, 15.f);
-    return __float_as_uint(q + 12582912.f);
+    return __float_as_uint(fmaf(x, r, z6144) + (12582912.f - 6144.f));
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// High and -low of the finite elements among a lane's eight, as a bf16 pair.
+__device__ __noinline__ uint32_t finite_range(uint4 x) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    float low = 0.f, high = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t v = (u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+        if ((v & 0x7FFFu) >= 0x7F80u) continue;
+        low = fminf(low, __uint_as_float(v << 16));
+        high = fmaxf(high, __uint_as_float(v << 16));
+    }
+    return pack_bf16x2(high, -low);
+}
+// The codes w with those of infinities and NaN put right: 15 and 0, and z.
+__device__ __noinline__ uint32_t mend_codes(uint4 x, uint32_t w, uint32_t z) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t v = (u[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+        const int bit = 4 * (i >> 1) + 16 * (i & 1);
+        if ((v & 0x7FFFu) < 0x7F80u) continue;
+        const uint32_t code = (v & 0x7FFFu) > 0x7F80u ? z : v & 0x8000u ? 0u : 15u;
+        w = (w & ~(15u << bit)) | code << bit;
+    }
+    return w;
 }
 
 // Eight channels of one lane and their group's word; the four lanes of a group call it together.
-__device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t &word, bool &bad) {
-    const uint32_t mag = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-    bad = (mag & 0xFFFFu) >= 0x7F80u || (mag >> 16) >= 0x7F80u;
-    uint32_t lo2 = min_bf2(min_bf2(x.x, x.y), min_bf2(x.z, x.w));
-    uint32_t hi2 = max_bf2(max_bf2(x.x, x.y), max_bf2(x.z, x.w));
-    if (bad) {  // of the finite values alone; NaN becomes 0, infinities stay and take the last codes
-        uint32_t *u = &x.x;
-        lo2 = hi2 = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t fin = 0, keep = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t v = (u[i] >> (16 * h)) & 0xFFFFu, m = v & 0x7FFFu;
-                if (m < 0x7F80u) fin |= v << (16 * h);
-                if (m <= 0x7F80u) keep |= v << (16 * h);
-            }
-            lo2 = min_bf2(lo2, fin);
-            hi2 = max_bf2(hi2, fin);
-            u[i] = keep;
-        }
+__device__ __forceinline__ uint32_t quantise8(const uint4 &x, uint32_t &word, bool &bad) {
+    const uint32_t lo2 = min_bf2(min_bf2(x.x, x.y), min_bf2(x.z, x.w));
+    const uint32_t hi2 = max_bf2(max_bf2(x.x, x.y), max_bf2(x.z, x.w));
+    // (high, -low) as a pair, 0 counted in
+    uint32_t span = max_bf2(max_bf2(__byte_perm(hi2, lo2 ^ 0x80008000u, 0x5410), __byte_perm(hi2, lo2 ^ 0x80008000u, 0x7632)), 0u);
+    span = max_bf2(span, __shfl_xor_sync(0xffffffffu, span, 1));
+    span = max_bf2(span, __shfl_xor_sync(0xffffffffu, span, 2));
+    bad = (span & 0x7F80u) == 0x7F80u || (span & 0x7F800000u) == 0x7F800000u;  // all four lanes alike
+    if (__any_sync(0xffffffffu, bad)) {
+        uint32_t fin = finite_range(x);
+        fin = max_bf2(fin, __shfl_xor_sync(0xffffffffu, fin, 1));
+        fin = max_bf2(fin, __shfl_xor_sync(0xffffffffu, fin, 2));
+        if (bad) span = fin;
     }
-    float low = fminf(fminf(bf_lo(lo2), bf_hi(lo2)), 0.f), high = fmaxf(fmaxf(bf_lo(hi2), bf_hi(hi2)), 0.f);
-    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, 1));
-    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 1));
-    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, 2));
-    high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, 2));
-    const float s = scale4(low, high);
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    const uint32_t z = __float_as_uint(fmaf(-low, r, 6144.f) - 6144.f + 12582912.f) & 15u;
+    const float below = bf_hi(span), s = scale4(below, bf_lo(span));
+    const float r = s > 0.f ? rcp_approx(s) : 0.f;
+    const uint32_t z = code4(below, r, 6144.f) & 15u;
     word = (__float_as_uint(s) >> 16) | z;
-    if (s == 0.f) x = make_uint4(0, 0, 0, 0);  // infinities among zeros: times 0 they would be NaN
     const float zf = (float)z + 6144.f;
     uint32_t w = 0;
     const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t a = code4(bf_lo(u[i]), r, zf), b = code4(bf_hi(u[i]), r, zf);
-        w |= __byte_perm(a, b, 0x5410) << (4 * i);
+        w |= __vminu2(__byte_perm(a, b, 0x5410), 0x000F000Fu) << (4 * i);
     }
+    if (bad) w = s > 0.f ? mend_codes(x, w, z) : 0u;
     return w;
 }
 

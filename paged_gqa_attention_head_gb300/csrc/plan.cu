@@ -11,9 +11,10 @@
 // that releasing what the last plan took leaves the list as it was.
 //
 // Both are bound by latency: the lengths, the list's entry and the stores one after the other.
-// The blocks are one cluster, whose barrier lies between the reads of the lengths and the list's
-// size and the writes of their new values: they may be the same memory, so that a captured step
-// carries them on from replay to replay.
+// A captured step carries the lengths and the list's size on from replay to replay, so their new
+// values may lie where the old ones are.  Then the blocks are one cluster, and its barrier lies
+// between the reads and the writes; otherwise they are a plain grid, which is launched sooner (a cluster's
+// launch takes some 6 us more of host time).
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -21,7 +22,8 @@ namespace sinkattn {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCluster = 8;    // blocks at most (the portable cluster size)
+constexpr int kPlanCluster = 8;    // blocks of a call that updates in place at most (the portable cluster size)
+constexpr int kPlanBlocks = 152;   // blocks of another at most
 
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -68,11 +70,10 @@ __device__ __forceinline__ void block_scan(int64_t &x, int64_t &y, int64_t *tx, 
     y = iy - y + s_y[warp];
 }
 
-// Entries of the list, clamped to what it can hold.
-__device__ __forceinline__ int list_size(const PlanArgs &a) {
-    const int n = *a.num_free;
+// Entries of a list whose size reads n, held to what it can be.
+__device__ __forceinline__ int list_size(const PlanArgs &a, int n, uint32_t &bad) {
     if (n >= 0 && n <= a.num_pages) return n;
-    set_status(a.status, SINKATTN_STATUS_BAD_LENGTH);
+    bad |= SINKATTN_STATUS_BAD_LENGTH;
     return n < 0 ? 0 : a.num_pages;
 }
 
@@ -89,6 +90,13 @@ __device__ __forceinline__ int last_at_most(const int *s, int n, int x) {
     return lo;
 }
 
+// The same from an i that is not past it: mostly that one or the next.
+__device__ __forceinline__ int next_at_most(const int *s, int n, int i, int x) {
+    if (i + 1 >= n || s[i + 1] > x) return i;
+    ++i;
+    return i + 1 >= n || s[i + 1] > x ? i : last_at_most(s, n, x);
+}
+
 __device__ __forceinline__ int pages_of(int64_t tokens) { return (int)((tokens + kPageSize - 1) / kPageSize); }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
@@ -100,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     __shared__ int s_taken;
     const int tid = threadIdx.x, rank = blockIdx.x;
     const int64_t cap = min((int64_t)a.max_pages * kPageSize, (int64_t)INT32_MAX);
-    const int nfree = list_size(a);
+    const int free_now = *a.num_free;  // on its way while the lengths are read
     if (tid == 0) s_taken = 0;
 
     // Every request's tokens and new pages; a thread sums a run of requests.
@@ -108,15 +116,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int64_t tokens = 0, pages = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = max(a.new_lens[b], 0), L = a.seq_lens[b];
+        const int raw = a.new_lens[b], L = a.seq_lens[b], n = max(raw, 0);
+        s_off[b] = raw;
+        s_len[b] = L;
         tokens += n;
         if (L >= 0 && (int64_t)L + n <= cap) pages += pages_of((int64_t)L + n) - pages_of(L);
     }
     block_scan(tokens, pages, &s_total[0], &s_total[1]);
     uint32_t bad = 0;
+    const int nfree = list_size(a, free_now, bad);
     int taken = 0;
     for (int b = b0; b < b1; ++b) {
-        const int raw = a.new_lens[b], n = max(raw, 0), L = a.seq_lens[b];
+        const int raw = s_off[b], n = max(raw, 0), L = s_len[b];
         const bool fits = L >= 0 && (int64_t)L + n <= cap;
         const int need = fits ? pages_of((int64_t)L + n) - pages_of(L) : 0;
         const bool rows = n == 0 || tokens + n <= a.max_tokens;
@@ -127,7 +138,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
         // the served requests that need pages are the first of those that do: what they take has no gaps
         if (served && need > 0) taken = (int)pages + need;
         s_cu[b] = (int)min(tokens, (int64_t)a.max_tokens);
-        s_len[b] = L;
         s_off[b] = served ? (int)min(pages, (int64_t)nfree) : -1;
         tokens += n;
         pages += need;
@@ -136,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
     if (tid == 0) s_cu[a.B] = (int)min(s_total[0], (int64_t)a.max_tokens);
     if (rank == 0 && bad) set_status(a.status, bad);
     __syncthreads();
-    cluster_barrier();  // every block has read what may be written now
+    cluster_barrier();  // in place: every block has read what may be written now
 
     if (rank == 0) {
         for (int b = tid; b < a.B; b += blockDim.x) {
@@ -151,34 +161,41 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
         }
     }
 
-    // Four tokens a thread and step: one look-up, wide stores.
+    // Four tokens a thread and step: one look-up, the pages' loads side by side, wide stores.
     const int total = s_cu[a.B];
     for (int64_t t0 = 4 * ((int64_t)rank * blockDim.x + tid); t0 < a.max_tokens;
          t0 += 4 * (int64_t)gridDim.x * blockDim.x) {
-        int pos[4];
-        int64_t slot[4];
+        int pos[4], pg[4];
+        const int32_t *from[4];
+        int32_t *begins[4];  // the table's entry of a page that begins with the token
         int i = t0 < total ? last_at_most(s_cu, a.B, (int)t0) : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t t = t0 + e;
             pos[e] = -1;
-            slot[e] = -1;
+            from[e] = nullptr;
+            begins[e] = nullptr;
             if (t >= total) continue;
-            while (i + 1 < a.B && s_cu[i + 1] <= t) ++i;
+            i = next_at_most(s_cu, a.B, i, (int)t);
             const int off = s_off[i], L = s_len[i];
             if (off < 0) continue;
             const int p = L + (int)(t - s_cu[i]);
             const int page = p / kPageSize, first_new = pages_of(L);
-            int pg;
-            if (page < first_new) {
-                pg = a.block_table[(int64_t)i * a.max_pages + page];
-            } else {
-                pg = a.free_pages[nfree - 1 - (off + page - first_new)];
-                if (p % kPageSize == 0) a.block_table[(int64_t)i * a.max_pages + page] = pg;
-            }
+            int32_t *entry = a.block_table + (int64_t)i * a.max_pages + page;
+            from[e] = page < first_new ? entry : a.free_pages + (nfree - 1 - (off + page - first_new));
+            if (page >= first_new && p % kPageSize == 0) begins[e] = entry;
             pos[e] = p;
-            if (pg >= 0 && pg < a.num_pages)
-                slot[e] = (int64_t)pg * kPageSize + p % kPageSize;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pg[e] = from[e] ? *from[e] : 0;
+        int64_t slot[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            slot[e] = -1;
+            if (!from[e]) continue;
+            if (begins[e]) *begins[e] = pg[e];
+            if (pg[e] >= 0 && pg[e] < a.num_pages)
+                slot[e] = (int64_t)pg[e] * kPageSize + pos[e] % kPageSize;
             else
                 set_status(a.status, SINKATTN_STATUS_BAD_PAGE);
         }
@@ -204,30 +221,27 @@ __global__ void __launch_bounds__(kPlanThreads) release_pages_kernel(const PlanA
     __shared__ int64_t s_total[2];
     const int tid = threadIdx.x, rank = blockIdx.x;
     const int64_t cap = (int64_t)a.max_pages * kPageSize;
-    const int nfree = list_size(a);
+    const int free_now = *a.num_free;
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int64_t pages = 0, none = 0;
     uint32_t bad = 0;
-    auto released = [&](int b, int &L) {  // pages of request b to push
-        L = a.seq_lens[b];
-        if (!a.done[b]) return 0;
-        if (L < 0 || L > cap) {
-            bad |= SINKATTN_STATUS_BAD_LENGTH;
-            return 0;
-        }
-        return pages_of(L);
-    };
     for (int b = b0; b < b1; ++b) {
-        int L;
-        pages += released(b, L);
+        const int L = a.seq_lens[b];
+        int n = 0;  // pages of the request to push
+        if (a.done[b]) {
+            if (L < 0 || L > cap) bad |= SINKATTN_STATUS_BAD_LENGTH;
+            else n = pages_of(L);
+        }
+        s_off[b] = n;
+        s_len[b] = a.done[b] ? 0 : L;
+        pages += n;
     }
+    const int nfree = list_size(a, free_now, bad);
     block_scan(pages, none, &s_total[0], &s_total[1]);
     for (int b = b0; b < b1; ++b) {
-        int L;
-        const int n = released(b, L);
+        const int n = s_off[b];
         s_off[b] = (int)pages;
-        s_len[b] = a.done[b] ? 0 : L;
         pages += n;
     }
     __syncthreads();
@@ -242,15 +256,16 @@ __global__ void __launch_bounds__(kPlanThreads) release_pages_kernel(const PlanA
     // the pages' places from the list's new top down, a run of four a thread and step
     for (int64_t o0 = 4 * ((int64_t)rank * blockDim.x + tid); o0 < total; o0 += 4 * (int64_t)gridDim.x * blockDim.x) {
         int i = last_at_most(s_off, a.B, (int)o0);
+        const int32_t *from[4];
         int pg[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int o = (int)o0 + e;
-            pg[e] = -1;
-            if (o >= total) continue;
-            while (i + 1 < a.B && s_off[i + 1] <= o) ++i;
-            pg[e] = a.block_table[(int64_t)i * a.max_pages + (o - s_off[i])];
+            const int o = (int)min(o0 + e, (int64_t)total - 1);
+            i = next_at_most(s_off, a.B, i, o);
+            from[e] = a.block_table + (int64_t)i * a.max_pages + (o - s_off[i]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pg[e] = *from[e];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t at = (int64_t)nfree + total - 1 - (o0 + e);
@@ -262,39 +277,52 @@ __global__ void __launch_bounds__(kPlanThreads) release_pages_kernel(const PlanA
 }
 
 template <typename Kernel>
-cudaError_t launch_cluster(Kernel kernel, const PlanArgs &a, int64_t items, int smem, cudaStream_t stream) {
-    // A block for each 4096 tokens (four a thread), as many as a cluster holds.
-    int blocks = (int)((items + 4 * kPlanThreads - 1) / (4 * kPlanThreads));
-    blocks = blocks < 1 ? 1 : blocks > kPlanCluster ? kPlanCluster : blocks;
+cudaError_t launch_plan(Kernel kernel, const PlanArgs &a, bool in_place, int64_t items, int smem, cudaStream_t stream) {
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
+    // Few requests, few threads: they are set up sooner.  Four items a thread.
+    const int threads = a.B <= 512 ? 256 : kPlanThreads;
+    int64_t blocks = (items + 4 * threads - 1) / (4 * threads);
+    blocks = blocks < 1 ? 1 : blocks > kPlanBlocks ? kPlanBlocks : blocks;
+    if (!in_place || blocks == 1) {  // one block is a cluster of its own
+        kernel<<<(unsigned)blocks, threads, smem, stream>>>(a);
+        return cudaGetLastError();
+    }
+    // values updated in place: the blocks wait for one another before they write
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)(blocks > kPlanCluster ? kPlanCluster : blocks));
     cfg.blockDim = dim3(kPlanThreads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks;
+    attr[0].val.clusterDim.x = cfg.gridDim.x;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// Whether the outputs lie on the values that every block reads first.
+bool in_place(const PlanArgs &a) {
+    const uintptr_t in = reinterpret_cast<uintptr_t>(a.seq_lens), out = reinterpret_cast<uintptr_t>(a.seq_lens_out);
+    const uintptr_t bytes = 4 * (uintptr_t)a.B;
+    return a.num_free == a.num_free_out || (in < out + bytes && out < in + bytes);
+}
+
 }  // namespace
 
 cudaError_t launch_plan_step(const PlanArgs &a, cudaStream_t stream) {
-    return launch_cluster(plan_step_kernel, a, a.max_tokens, (3 * a.B + 1) * 4, stream);
+    return launch_plan(plan_step_kernel, a, in_place(a), a.max_tokens, (3 * a.B + 1) * 4, stream);
 }
 
 cudaError_t launch_release_pages(const PlanArgs &a, cudaStream_t stream) {
     // how many pages there are to release only the device knows: at most every page
     const int64_t most = (int64_t)a.B * a.max_pages;
-    return launch_cluster(release_pages_kernel, a, most < a.num_pages ? most : a.num_pages, 2 * a.B * 4, stream);
+    return launch_plan(release_pages_kernel, a, in_place(a), most < a.num_pages ? most : a.num_pages, 2 * a.B * 4, stream);
 }
 
 }  // namespace sinkattn

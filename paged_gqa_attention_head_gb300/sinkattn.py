@@ -943,19 +943,19 @@ def unpack_kv_int4(kv_pages, pages=None, k_out=None, v_out=None, workspace_buf=N
         _need_dense(pages, "pages", torch.int32, dev, 1)
         n, wanted = pages.shape[0], pages.data_ptr()
     shape = (n, Hkv, PAGE_SIZE, D)
-    outs = []
     for name, o in (("k_out", k_out), ("v_out", v_out)):
-        if o is None:
-            o = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
-        else:
+        if o is not None:
             _need_dense(o, name, torch.bfloat16, dev, 4)
             if o.shape != shape:
                 raise ValueError(f"{name} must be [n, Hkv, 16, D] = {shape}")
-        outs.append(o)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
     ws, nbytes = _status_args(dev) if workspace_buf is None else _workspace_args(workspace_buf, dev)
-    _call(dev, "sinkattn_unpack_kv_int4", kv_pages.data_ptr(), wanted, n, outs[0].data_ptr(), outs[1].data_ptr(),
+    _call(dev, "sinkattn_unpack_kv_int4", kv_pages.data_ptr(), wanted, n, k_out.data_ptr(), v_out.data_ptr(),
           _desc_ref(0, Hkv, Hkv, D, num_pages, 0, 0, 0, 0), ws, nbytes, _raw_stream(dev))
-    return outs[0], outs[1]
+    return k_out, v_out
 
 
 def decode_int4_workspace_size(desc: PagedDesc) -> int:
