@@ -512,7 +512,8 @@ int sinkattn_prefill_int4(const void *q, const void *k, const void *v, const int
  * cu_seqlens:    int32 [num_seqs + 1] (written): prefix sums of the new lengths, at most max_tokens
  * start_pos:     int32 [num_seqs] (written), a copy of seq_lens; or NULL
  * seq_lens_out, num_free_out: int32 [num_seqs] and [1] (written): the values after the step.  They may
- *                be seq_lens and num_free themselves
+ *                be seq_lens and num_free themselves; nothing else that is written may share memory
+ *                with what is read, or with another output (SINKATTN_ERR_INVALID_ARG)
  * positions, slots: int32 and int64 [max_tokens] (written), 16-byte aligned: each row's position in
  *                its request and its slot in the cache (page * 16 + position % 16); -1 for rows behind the
  *                last request.  A page outside [0, num_pages) sets SINKATTN_STATUS_BAD_PAGE, its slots are -1

@@ -1022,6 +1022,27 @@ int check_plan(const sinkattn_paged_desc *desc, const int32_t *seq_lens, const i
     if (workspace && (ws_bytes < kStatusBytes || !aligned(workspace, kAlign))) return SINKATTN_ERR_INVALID_ARG;
     return SINKATTN_OK;
 }
+
+struct Range {
+    const void *at;
+    int64_t bytes;
+};
+bool share(const Range &a, const Range &b) {
+    if (!a.at || !b.at || a.bytes <= 0 || b.bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// Whether what is written (the first `outs` ranges) shares no byte with what is read, or with what else
+// is written, but for out[i] that is in[i] itself where may_be[i] says so.
+bool apart(const Range *out, int outs, const Range *in, int ins, const bool *may_be) {
+    for (int i = 0; i < outs; ++i) {
+        for (int j = 0; j < ins; ++j)
+            if (share(out[i], in[j]) && !(i == j && may_be[i] && out[i].at == in[j].at)) return false;
+        for (int j = 0; j < i; ++j)
+            if (share(out[i], out[j])) return false;
+    }
+    return true;
+}
 }  // namespace
 
 int sinkattn_plan_step(const int32_t *new_lens, const int32_t *seq_lens, int32_t *block_table,
@@ -1036,7 +1057,12 @@ int sinkattn_plan_step(const int32_t *new_lens, const int32_t *seq_lens, int32_t
     if (!aligned(new_lens, 4) || !aligned(cu_seqlens, 4) || !aligned(start_pos, 4) || !aligned(positions, 16) ||
         !aligned(slots, 16))
         return SINKATTN_ERR_INVALID_ARG;
-    if (start_pos && (start_pos == seq_lens || start_pos == seq_lens_out)) return SINKATTN_ERR_INVALID_ARG;
+    const int64_t B = desc->num_seqs, T = max_tokens;
+    const Range in[4] = {{seq_lens, 4 * B}, {num_free, 4}, {new_lens, 4 * B}, {free_pages, 4 * (int64_t)desc->num_pages}};
+    const Range out[7] = {{seq_lens_out, 4 * B}, {num_free_out, 4}, {cu_seqlens, 4 * B + 4}, {start_pos, 4 * B},
+                          {positions, 4 * T}, {slots, 8 * T}, {block_table, 4 * B * desc->max_pages_per_seq}};
+    const bool may_be[7] = {true, true};
+    if (!apart(out, 7, in, 4, may_be)) return SINKATTN_ERR_INVALID_ARG;
     PlanArgs a = {};
     a.new_lens = new_lens;
     a.seq_lens = seq_lens;
@@ -1064,6 +1090,11 @@ int sinkattn_release_pages(const uint8_t *done, const int32_t *seq_lens, const i
     int rc = check_plan(desc, seq_lens, block_table, free_pages, num_free, seq_lens_out, num_free_out, workspace, ws_bytes);
     if (rc) return rc;
     if (desc->num_seqs > 0 && !done) return SINKATTN_ERR_INVALID_ARG;
+    const int64_t B = desc->num_seqs;
+    const Range in[4] = {{seq_lens, 4 * B}, {num_free, 4}, {done, B}, {block_table, 4 * B * desc->max_pages_per_seq}};
+    const Range out[3] = {{seq_lens_out, 4 * B}, {num_free_out, 4}, {free_pages, 4 * (int64_t)desc->num_pages}};
+    const bool may_be[3] = {true, true};
+    if (!apart(out, 3, in, 4, may_be)) return SINKATTN_ERR_INVALID_ARG;
     PlanArgs a = {};
     a.done = done;
     a.seq_lens = seq_lens;

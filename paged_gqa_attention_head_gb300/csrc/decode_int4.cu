@@ -130,7 +130,7 @@ int int4_smem_bytes(int B) {
 
 // Length of a sequence, held to what its block table can name.
 __device__ __forceinline__ int length_of(const DecodeArgs &a, int b) {
-    return min(max(a.seq_lens[b], 0), a.max_pages * kPageSize);
+    return (int)min((int64_t)max(a.seq_lens[b], 0), (int64_t)a.max_pages * kPageSize);
 }
 template <bool kWindow>
 __device__ __forceinline__ int first_page(const DecodeArgs &a, int L) {

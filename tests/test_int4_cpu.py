@@ -176,22 +176,29 @@ def test_prefill_int4_rejects(sa):
 def test_plan_and_release_reject(sa):
     lib, (buf, p) = sa.load(), _host()
 
-    def plan(new=p, sl=p, bt=p, fr=p, nf=p, T=8, cu=p, st=None, lo=p, no=p, pos=p, slots=p, d=_desc(sa), ws=None, wb=0):
+    # arrays of their own, 256 bytes apart (4 requests of 4 columns, 10 pages, 8 rows)
+    new, sl, bt, fr, nf, cu, lo, no, pos, slots, st = (p + 256 * i for i in range(11))
+
+    def plan(new=new, sl=sl, bt=bt, fr=fr, nf=nf, T=8, cu=cu, st=st, lo=lo, no=no, pos=pos, slots=slots, d=_desc(sa), ws=None, wb=0):
         return lib.sinkattn_plan_step(new, sl, bt, fr, nf, T, cu, st, lo, no, pos, slots, ctypes.byref(d), ws, wb, None)
 
-    def release(done=p, sl=p, bt=p, fr=p, nf=p, lo=p, no=p, d=_desc(sa), ws=None, wb=0):
+    def release(done=new, sl=sl, bt=bt, fr=fr, nf=nf, lo=lo, no=no, d=_desc(sa), ws=None, wb=0):
         return lib.sinkattn_release_pages(done, sl, bt, fr, nf, lo, no, ctypes.byref(d), ws, wb, None)
-    both = [dict(sl=None), dict(bt=None), dict(fr=None), dict(nf=None), dict(lo=None), dict(no=None), dict(sl=p + 2),
-            dict(bt=p + 2), dict(fr=p + 1), dict(nf=p + 2), dict(lo=p + 2), dict(no=p + 2), dict(ws=p, wb=128),
+    both = [dict(sl=None), dict(bt=None), dict(fr=None), dict(nf=None), dict(lo=None), dict(no=None), dict(sl=sl + 2),
+            dict(bt=bt + 2), dict(fr=fr + 1), dict(nf=nf + 2), dict(lo=lo + 2), dict(no=no + 2), dict(ws=p, wb=128),
             dict(ws=p + 16, wb=256), dict(d=_desc(sa, num_pages=0)), dict(d=_desc(sa, max_pages_per_seq=0)),
-            dict(d=_desc(sa, num_seqs=-1))]
+            dict(d=_desc(sa, num_seqs=-1)),
+            # memory shared in other ways than the two that are allowed
+            dict(lo=sl + 4), dict(no=sl), dict(lo=nf), dict(no=lo + 8), dict(lo=fr + 36), dict(fr=bt + 60)]
     for kw in both:
         assert plan(**kw) == 1, kw
         assert release(**kw) == 1, kw
-    for kw in (dict(new=None), dict(cu=None), dict(pos=None), dict(slots=None), dict(T=-1), dict(pos=p + 4),
-               dict(slots=p + 8), dict(st=p), dict(new=p + 2), dict(cu=p + 2)):
+    for kw in (dict(new=None), dict(cu=None), dict(pos=None), dict(slots=None), dict(T=-1), dict(pos=pos + 4),
+               dict(slots=slots + 8), dict(st=sl), dict(st=lo), dict(new=new + 2), dict(cu=cu + 2), dict(cu=new), dict(pos=slots),
+               dict(lo=new), dict(slots=bt), dict(cu=lo - 16), dict(bt=new)):
         assert plan(**kw) == 1, kw
-    assert release(done=None) == 1
+    for kw in (dict(done=None), dict(done=lo + 3), dict(done=fr)):
+        assert release(**kw) == 1, kw
     for call in (plan, release):
         assert call(d=_desc(sa, num_seqs=8193)) == 2
         assert call(d=_desc(sa, num_seqs=8192, max_pages_per_seq=1 << 18)) == 2
