@@ -468,7 +468,7 @@ int sinkattn_unpack_kv_int4(const void *kv_pages, const int32_t *pages, int32_t 
  * times its token's V scale of the group, relative to a power of two of the largest V scale met, and
  * the product is rounded once to fp16 (relative 2^-11 at most; from 2^20 below the largest product on,
  * 2^-31 of that).  q is taken in fp16 times a power of two of its (sequence, KV head): an entry keeps
- * its 8 bits unless it is more than 2^22 times smaller than the largest of its group.  (With a
+ * its 8 bits unless it is more than 2^27 times smaller than the largest of its group.  (With a
  * sliding window it runs the split-KV kernel too, over the visible pages.) */
 int sinkattn_decode_int4_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
 

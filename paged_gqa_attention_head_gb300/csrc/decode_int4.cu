@@ -16,11 +16,11 @@
 //     channels of two neighbouring tokens, and the ANDs part the channels;
 //   * the words of a page come by 8x8 loads whose eight row addresses are the same: plain, a lane gets
 //     the words of its two neighbouring tokens; transposed, its own token's word twice (the scale as
-//     a float: one AND);
-//   * z comes off K in the products: z times -sum of the group's q, for 16 heads s z for all groups
-//     in one bf16 product.  (Off the codes, one f16 addition for two of them: 162 us where this takes
-//     158 on the 0.71 GB batch below.)  It comes off V's codes by such additions (a product of z with P
-//     and a subtraction a step: 162 us too);
+//     a float: one AND; z as an f16 pair: another);
+//   * z comes off the codes, exactly, by one f16 multiplication and addition for two of them.  (Off the
+//     products - z times -sum of the group's q, and z times P, as MMAs of their own - the batch below takes 160
+//     us where this takes 165, but the sums that cancel leave the scores of single keys 4e-6 off, ten times
+//     as much as this);
 //   * a group's K scores are multiplied by s in fp32; P of a group is taken times s, relative to the
 //     power of two above the largest V scale met, and rounded once to f16, as in the INT8 decode.
 // Groups of up to 8 heads: S^T = K Q^T and O^T = V^T P^T, tokens and channels on the M axis, heads on N,
@@ -28,6 +28,10 @@
 // The running maximum moves only when a score passes it by more than 8 (log2).
 // FP8 MMAs (a code as the E4M3 subnormal code * 2^-9, half the ANDs, q in three E5M2 parts) are made of
 // conversions and f16 MMAs here: 226 us.
+// Measured: 64 sequences up to 131072 tokens, 64/8 heads of 64 (0.71 GB) 165 us, 4.3 TB/s; 64 sequences up to
+// 16384, 64/4 heads of 128 (0.31 GB) 97 us, 3.2 TB/s.  Each instruction added to the first shows (an AND 2.0
+// cycles a page and scheduler, an MMA 6, an f16 multiplication and addition 1.4, of ~275): it is bound by
+// their issue.  The second is bound by the latencies of the two warps a scheduler that its registers allow.
 #include <math.h>
 
 #include <mutex>
@@ -46,12 +50,14 @@ struct Int4Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
     // Pages of a unit, one copy stage: what a unit costs beside its pages' arithmetic is ~100 instructions, so as
-    // many as two stages for each warp leave room for (head_dim 64: 4 pages 174 us where 8 take 158; 128 and 16
-    // heads, whose registers allow two CTAs an SM: 4 pages 98.7 us, 6 95.4).
+    // many as two stages for each warp leave room for (head_dim 64: 4 pages 176 us where 8 take 165; 128 and 16
+    // heads, whose registers allow two CTAs an SM: 4 pages 99.9 us, 6 96.8).
     static constexpr int kPPU = D == 64 ? 8 : NH == 1 ? 4 : 6;
-    // Pages whose scores are held at once: what a step costs beside them, against registers (head_dim 64: 2 pages
-    // 162 us, 4 158, 8 160; 128 and 16 heads: 1 page 105 us, 2 98.7, 3 97.0 (of 6 pages a unit; 2: 95.4), 4 107).
+    // Pages whose scores are held at once: what a step costs beside them, against registers and the time of a
+    // short sequence (head_dim 64: 2 pages 167 us, 4 165, 8 164, where one sequence of 4097 tokens takes 9.8, 10.3 and
+    // 10.7; 128 and 16 heads: 1 page 101 us, 2 96.8, 3 97.4).
     static constexpr int kStep = D == 64 && NH == 1 ? 4 : 2;
+    static_assert(kPPU % kStep == 0, "a step stays inside its unit");
     static constexpr int kStages = 2;
     static constexpr int kRec = 9 * D;                         // K (or V) of a (page, head)
     static constexpr int kPageBytes = 2 * kRec;
@@ -61,9 +67,9 @@ struct Int4Cfg {
     static constexpr int kCtas = NH == 2 && D == 128 ? 2 : 3;  // CTAs an SM, by registers
 };
 
-constexpr float kPShift = 7.f;   // P = 2^(s - m + kPShift)
-constexpr float kMaxSlack = 8.f; // the running maximum moves when a score passes it by more
-constexpr float kStateDown = 1.f / 32768.f;  // states leave with their sums over 2^(kPShift + kMaxSlack)
+constexpr float kMaxSlack = 8.f;  // the running maximum, a whole number, moves when a score passes it by more
+constexpr float kPUp = 128.f;     // P = 2^(s - m), at most 2^8, enters its product 2^7 times as large: f16's range
+constexpr float kStateDown = 1.f / 256.f;  // states leave with their sums over 2^kMaxSlack, the largest P
 constexpr float kUp24 = 16777216.f;          // 2^24
 constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;  // pairs of codes in place, and 16 times them
 constexpr uint32_t kBoth = 0x00FF00FFu;                      // pairs of (even code + 16 odd code)
@@ -88,27 +94,15 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t z, uint32_t m, uint32_t x) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(z), "r"(m), "r"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return v;
-}
-// D = A B, bf16.
-__device__ __forceinline__ void mma_bf16_16816_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                   uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-        "{%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-// The product s z of a word, twice, in bf16 (exact: four bits times four).
-__device__ __forceinline__ uint32_t scale_times_z(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b32 z;\n\tsub.rn.bf16x2 z, %1, %2;\n\tmul.rn.bf16x2 %0, z, %3;\n\t}"
-        : "=r"(r)
-        : "r"(((w & 15u) * 0x10001u) | 0x43004300u), "r"(0x43004300u), "r"((w & 0xFFF0u) * 0x10001u));
-    return r;
+// The codes of a word less z: pairs in place [0], [2] and 16 times their value [1], [3], of the lower and the
+// upper bytes.
+__device__ __forceinline__ void less_z(uint32_t (&c)[4], uint32_t w, uint32_t z) {
+    constexpr uint32_t m1 = 0xBC00BC00u, m16 = 0xCC00CC00u;  // -1, -16
+    const uint32_t h = w >> 8;
+    c[0] = fma_h2(z, m1, w & kEven);
+    c[1] = fma_h2(z, m16, w & kOdd);
+    c[2] = fma_h2(z, m1, h & kEven);
+    c[3] = fma_h2(z, m16, h & kOdd);
 }
 
 // What the arithmetic needs of a unit.
@@ -169,12 +163,6 @@ __device__ void scan_units(const DecodeArgs &a, int *s_prefix) {
     }
     if (tid == 0) s_prefix[a.B] = s_warp_tot[0] + s_warp_tot[1] + s_warp_tot[2] + s_warp_tot[3];
     __syncthreads();
-}
-
-__device__ __forceinline__ float f16_of(float x) {  // rounded to f16
-    float y;
-    asm("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // NH: 8-head tiles of the query group (1 for G <= 8, 2 for G = 16).
@@ -304,16 +292,12 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
     // q in the order of its MMA operand: [2 i + x][e NH + nt] of head 8 nt + gr, channels 32 i + 8 t4 + 4 x + (0, 1)
     // (e 0) and a sixteenth of + (2, 3) (e 1)
     uint32_t qf[2 * NG][2 * NH];
-    // z of K: -sum of the group's q, of group t4 (else 0): for 8 heads two f16 parts against z; for 16 three
-    // bf16 parts against s z, all groups in one product (six MMAs a page less at head_dim 128)
-    uint32_t qz[NH == 1 ? NG : 2][2];  // (16 heads: [part][nt])
-    const uint32_t zoff = 8 * D + 2 * (16 * min(t4, NG - 1) + gr);  // the lane's word for that
     // O * 2^-24.  8 heads: [m-tile 2 i + x][.]: channels 32 i + 8 (gr / 2) + gr % 2 + 4 x (and of these plus 16
     // times the ones 2 further) of heads 2 t4, 2 t4 + 1; 16 heads: [4 i + n]: channels 32 i + 8 t4 + (0, 1) (n even)
     // + 2 n (and of those plus 16 times the ones 2 further, n odd) of heads gr, gr + 8
     float acc[2 * NG * NH][4];
     // of the lane's two heads (8: 2 t4, 2 t4 + 1; 16: gr, gr + 8): running maximum of the scores (log2), a score
-    // above which (before its factor f0) it moves, -(maximum - kPShift) (0 before the first key), sum of P
+    // above which (before its factor f0) it moves, -maximum (0 before the first key), sum of P
     float mr[2], thr[2], nr[2];
     float2 ls[NH];                    // 8 heads: of both; 16: of each, from even and from odd tokens
     float f0 = 0.f;                   // score factor
@@ -354,12 +338,12 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                     }
                 }
             }
-            // q times 2^(9 - e), e the exponent of the group's largest entry (kept where both powers are
-            // normal floats), with the sign of the score scale: sums of 32 stay in f16
+            // q times 2^(14 - e), e the exponent of the group's largest entry (kept where both powers are
+            // normal floats), with the sign of the score scale
             const int ex = min(max((int)(__reduce_max_sync(0xffffffffu, mx) >> 7), 20), 254);
-            const float down = copysignf(__uint_as_float((uint32_t)(263 - ex) << 23), a.scale_log2);
+            const float down = copysignf(__uint_as_float((uint32_t)(268 - ex) << 23), a.scale_log2);
             // (never 0, so that a hidden key's -inf stays one)
-            f0 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(ex - 9) << 23) * kUp24, 1e-37f);
+            f0 = fmaxf(fabsf(a.scale_log2) * __uint_as_float((uint32_t)(ex - 14) << 23) * kUp24, 1e-37f);
 #pragma unroll
             for (int kk = 0; kk < 2 * NG; ++kk)
 #pragma unroll
@@ -368,34 +352,6 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                     const float d = e >= NH ? down * 0.0625f : down;
                     qf[kk][e] = pack_f16x2(__uint_as_float(w << 16) * d, __uint_as_float(w & 0xFFFF0000u) * d);
                 }
-            if (NH == 2) qz[0][0] = qz[0][1] = qz[1][0] = qz[1][1] = 0u;
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                // sums of the group's q * 2^-24 as the codes meet it
-                constexpr uint32_t one = 0x00010001u, one16 = 0x00100010u;
-                float o[4];
-                if (NH == 1) {  // every row the same: heads 2 t4, 2 t4 + 1
-                    mma_f16_16816_from(o, 0.f, 0.f, one, one, one16, one16, qf[2 * i][0], qf[2 * i][1]);
-                    mma_f16_16816(o, one, one, one16, one16, qf[2 * i + 1][0], qf[2 * i + 1][1]);
-                    const float x = __shfl_sync(0xffffffffu, o[0], gr >> 1), y = __shfl_sync(0xffffffffu, o[1], gr >> 1);
-                    const float neg = ((gr & 1) ? y : x) * -kUp24, hi = f16_of(neg);
-                    qz[i][0] = t4 == i ? pack_f16x2(hi, 0.f) : 0u;
-                    qz[i][1] = t4 == i ? pack_f16x2(neg - hi, 0.f) : 0u;
-                } else {  // every column the same: heads gr and gr + 8
-                    mma_f16_16816_from(o, 0.f, 0.f, qf[2 * i][0], qf[2 * i][1], qf[2 * i][2 * NH - 2], qf[2 * i][2 * NH - 1], one, one16);
-                    mma_f16_16816(o, qf[2 * i + 1][0], qf[2 * i + 1][1], qf[2 * i + 1][2 * NH - 2], qf[2 * i + 1][2 * NH - 1], one, one16);
-#pragma unroll
-                    for (int nt = 0; nt < NH; ++nt) {
-                        const float neg = -o[2 * nt];
-                        const float p0 = __bfloat162float(__float2bfloat16_rn(neg));
-                        const float p1 = __bfloat162float(__float2bfloat16_rn(neg - p0));
-                        if (t4 == i) {
-                            qz[0][nt] = pack_bf16x2(p0, p1);
-                            qz[1][nt] = pack_bf16x2(neg - p0 - p1, 0.f);
-                        }
-                    }
-                }
-            }
 #pragma unroll
             for (int i = 0; i < 2 * NG * NH; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
@@ -428,8 +384,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t kb = at + j * C::kPageBytes;
-                uint32_t kc[NG][2], kw[NG][2], vw[NG][2];
-                const uint32_t z0 = lds_u16(kb + zoff), z1 = lds_u16(kb + zoff + 16);
+                uint32_t kc[NG][2], kw[NG][2], kz[NG][2], vw[NG][2];
 #pragma unroll
                 for (int i = 0; i < NG / 2; ++i) {
                     ldsm_x4(kb + 512 * i + 16 * lane, kc[2 * i][0], kc[2 * i][1], kc[2 * i + 1][0], kc[2 * i + 1][1]);
@@ -439,19 +394,20 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                         ldsm_x4_t(wa + C::kRec, vw[2 * i][0], vw[2 * i][1], vw[2 * i + 1][0], vw[2 * i + 1][1]);
                     } else {
                         ldsm_x4(wa, kw[2 * i][0], kw[2 * i][1], kw[2 * i + 1][0], kw[2 * i + 1][1]);
+                        ldsm_x4_t(wa, kz[2 * i][0], kz[2 * i][1], kz[2 * i + 1][0], kz[2 * i + 1][1]);
                         ldsm_x4(wa + C::kRec, vw[2 * i][0], vw[2 * i][1], vw[2 * i + 1][0], vw[2 * i + 1][1]);
                     }
                 }
                 if (NH == 1) {
-                    const uint32_t a0 = z0 & 15u, a1 = z1 & 15u;
 #pragma unroll
                     for (int i = 0; i < NG; ++i) {
-                        const uint32_t w0 = kc[i][0], w1 = kc[i][1], h0 = w0 >> 8, h1 = w1 >> 8;
+                        uint32_t c0[4], c1[4];
+                        less_z(c0, kc[i][0], kw[i][0] & kEven);
+                        less_z(c1, kc[i][1], kw[i][1] & kEven);
                         const float s0 = scale_hi(kw[i][0]), s1 = scale_hi(kw[i][1]);
                         float o[4];
-                        mma_f16_16816_from(o, 0.f, 0.f, a0, a1, a0, a1, qz[i][0], qz[i][1]);
-                        mma_f16_16816(o, w0 & kEven, w1 & kEven, w0 & kOdd, w1 & kOdd, qf[2 * i][0], qf[2 * i][1]);
-                        mma_f16_16816(o, h0 & kEven, h1 & kEven, h0 & kOdd, h1 & kOdd, qf[2 * i + 1][0], qf[2 * i + 1][1]);
+                        mma_f16_16816_from(o, 0.f, 0.f, c0[0], c1[0], c0[1], c1[1], qf[2 * i][0], qf[2 * i][1]);
+                        mma_f16_16816(o, c0[2], c1[2], c0[3], c1[3], qf[2 * i + 1][0], qf[2 * i + 1][1]);
                         // (one by one: a pair of one scale would be a move)
                         s[j][0][0].x = i ? fmaf(o[0], s0, s[j][0][0].x) : o[0] * s0;
                         s[j][0][0].y = i ? fmaf(o[1], s0, s[j][0][0].y) : o[1] * s0;
@@ -460,25 +416,22 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                         vs[j][i][0] = make_float2(scale_hi(vw[i][0]), scale_hi(vw[i][1]));
                     }
                 } else {
-                    const uint32_t sz[2] = {scale_times_z(z0), scale_times_z(z1)};
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        float o[4];
-                        mma_bf16_16816_new(o, qz[0][0], qz[0][1], qz[1][0], qz[1][1], sz[n], sz[n]);
-                        s[j][n][0] = make_float2(o[0], o[1]);
-                        s[j][n][NH - 1] = make_float2(o[2], o[3]);
+                    for (int n = 0; n < 2; ++n)
 #pragma unroll
                         for (int i = 0; i < NG; ++i) {
-                            const uint32_t w = kc[i][n], h = w >> 8;
                             const uint32_t(&x)[2 * NH] = qf[2 * i], (&y)[2 * NH] = qf[2 * i + 1];
-                            mma_f16_16816_from(o, 0.f, 0.f, x[0], x[1], x[2 * NH - 2], x[2 * NH - 1], w & kEven, w & kOdd);
-                            mma_f16_16816(o, y[0], y[1], y[2 * NH - 2], y[2 * NH - 1], h & kEven, h & kOdd);
+                            uint32_t c[4];
+                            less_z(c, kc[i][n], kz[i][n] & kEven);
+                            float o[4];
+                            mma_f16_16816_from(o, 0.f, 0.f, x[0], x[1], x[2 * NH - 2], x[2 * NH - 1], c[0], c[1]);
+                            mma_f16_16816(o, y[0], y[1], y[2 * NH - 2], y[2 * NH - 1], c[2], c[3]);
                             const float2 sc = make_float2(scale_lo(kw[i][n]), scale_hi(kw[i][n]));
-                            s[j][n][0] = ffma2(make_float2(o[0], o[1]), sc, s[j][n][0]);
-                            s[j][n][NH - 1] = ffma2(make_float2(o[2], o[3]), sc, s[j][n][NH - 1]);
+                            const float2 u = make_float2(o[0], o[1]), v = make_float2(o[2], o[3]);
+                            s[j][n][0] = i ? ffma2(u, sc, s[j][n][0]) : fmul2(u, sc);
+                            s[j][n][NH - 1] = i ? ffma2(v, sc, s[j][n][NH - 1]) : fmul2(v, sc);
                             vs[j][i][n] = make_float2(scale_lo(vw[i][n]), scale_hi(vw[i][n]));
                         }
-                    }
                 }
             }
             if (ragged) {  // hidden tokens: no score, and no scale, whatever lies there
@@ -537,19 +490,19 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                 float move = 1.f;
                 if (__uint_as_float(vb) > v_top) {
                     const float top = __uint_as_float((vb + 0x7FFFFFu) & 0x7F800000u);
-                    v_inv = 1.0f / top;
-                    move = v_top * v_inv;
+                    v_inv = kPUp / top;
+                    move = v_top / top;
                     v_top = top;
                 }
                 float al[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float x = NH == 1 ? col_max(cm[e]) : quad_max(cm[e]);
-                    const float mn = x > thr[e] ? x * f0 : mr[e];
+                    const float mn = x > thr[e] ? ceilf(x * f0) : mr[e];
                     al[e] = mr[e] == -INFINITY ? 0.f : fast_exp2(mr[e] - mn);
                     mr[e] = mn;
                     thr[e] = (mn + kMaxSlack) / f0;
-                    nr[e] = mn == -INFINITY ? 0.f : kPShift - mn;
+                    nr[e] = mn == -INFINITY ? 0.f : -mn;
                 }
 #pragma unroll
                 for (int e = 0; e < NH; ++e)
@@ -631,8 +584,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                 const float L = NH == 1 ? col_sum(e ? ls[0].y : ls[0].x) : quad_sum(ls[e * (NH - 1)].x + ls[e * (NH - 1)].y);
                 const int hc = NH == 1 ? 2 * t4 + e : gr + 8 * e;  // head in the group
                 const int h = cur.y * a.G + hc;
-                // reference of the state: probabilities were taken against mr - kPShift
-                const float m = mr[e] == -INFINITY ? -INFINITY : mr[e] - kPShift;
+                const float m = mr[e];
                 float scl = kStateDown, lse2 = -INFINITY;
                 if (whole) {
                     const float sk = a.sinks && hc < a.G ? a.sinks[h] * kLog2e : -INFINITY;
@@ -645,7 +597,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                         lse2 = M + log2f(den);
                     }
                 }
-                const float up = kUp24 * scl;
+                const float up = kUp24 / kPUp * scl;
                 // the channels of an m-tile's (8 heads) or two n-tiles' (16) even codes, and odd ones
                 auto even = [&](float x) { return x * up * v_top; };
                 auto odd = [&](float both, float x) { return (both - x) * 0.0625f * up * v_top; };
@@ -680,7 +632,7 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                 if (hc >= a.G || (NH == 1 ? gr : t4) != 0) continue;
                 if (!whole)
                     *reinterpret_cast<float2 *>(a.part_ml + (slot * a.G + hc) * 2) =
-                        make_float2(m + kPShift + kMaxSlack, L * kStateDown);
+                        make_float2(m + kMaxSlack, L * kStateDown);
                 else if (a.lse)
                     a.lse[(int64_t)cur.x * a.Hq + h] = lse2 * kLn2;
             }

@@ -232,6 +232,37 @@ def test_a_cache_past_two_gigabytes(sa, cuda_dev):
     assert torch.equal(torch.isfinite(sa.unpack_kv_int4(big[at:].contiguous())[0].float()), keep)
 
 
+@pytest.mark.parametrize("G", [2, 16])
+def test_nothing_to_see(sa, cuda_dev, G):
+    """No token in any sequence: the sink alone, or nothing; an empty batch."""
+    w = inputs.make_decode([0, 0, 0], 3, G, 1, 64, seed=17)
+    a = list(_dev(w, cuda_dev))
+    out, lse = sa.decode_int4(*a)
+    assert not out.any() and torch.equal(lse, a[4].expand(3, G))
+    a[4] = None
+    out, lse = sa.decode_int4(*a)
+    assert not out.any() and bool((lse == -float("inf")).all())
+    out, lse = sa.decode_int4(a[0][:0], a[1], a[2][:0], a[3][:0])
+    assert out.shape == (0, G, 64) and lse.shape == (0, G)
+
+
+def test_many_sequences(sa, cuda_dev):
+    """More sequences than a block has threads, most of a page or less."""
+    lens = np.random.default_rng(2).integers(0, 40, 900).tolist()
+    w = inputs.make_decode(lens, len(lens), 8, 2, 64, seed=18)
+    out, lse = sa.decode_int4(*_dev(w, cuda_dev))
+    check(out, lse, _ref(w))
+
+
+def test_the_same_page_for_several_sequences(sa, cuda_dev):
+    """A shared prefix: rows of the block table that name the same pages."""
+    w = inputs.make_decode([600, 640, 64], 3, 8, 1, 128, seed=19, poison=False)
+    w.cache.block_table[1, :30] = w.cache.block_table[0, :30]
+    w.cache.block_table[2, :4] = w.cache.block_table[0, :4]
+    out, lse = sa.decode_int4(*_dev(w, cuda_dev))
+    check(out, lse, _ref(w))
+
+
 def test_bad_pages_and_lengths_set_the_status(sa, cuda_dev):
     w = inputs.make_decode([100, 40, 60], 3, 16, 2, 64, seed=8)
     ref = _ref(w)
@@ -339,6 +370,24 @@ def test_prefill_split(sa, cuda_dev, D, Hq, Hkv, pre):
     check(*sa.prefill_int4(*a, workspace_buf=ws), ref)
     check(*sa.prefill_int4(*a, max_sms=3), ref)
     assert sa.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("pre", [[300, 20], [2000, 0]])
+def test_prefill_leaves_the_rows_behind(sa, cuda_dev, pre):
+    """Rows behind the last request stay as they were, whole and in parts; what the pages and the padding
+    hold there does not matter."""
+    p = inputs.make_prefill([9, 5, 6], 8, 1, 64, seed=21, prefix_lens=pre + [40])
+    a = list(_pre(p, cuda_dev))
+    ref = _pre_ref(p)
+    a[3] = a[3][:3].contiguous()  # two requests; the third's rows are padding
+    for i in (0, 1, 2):
+        a[i][14:] = float("nan")
+    a[5], a[6] = a[5][:2].contiguous(), a[6][:2].contiguous()
+    out = torch.full_like(a[0], 7.0)
+    lse = torch.full((20, 8), 5.0, device=cuda_dev)
+    sa.prefill_int4(*a, out=out, lse=lse)
+    check(out[:14], lse[:14], tuple(x[:14] for x in ref))
+    assert bool((out[14:] == 7.0).all()) and bool((lse[14:] == 5.0).all())
 
 
 def test_prefill_of_many_requests(sa, cuda_dev):
