@@ -26,6 +26,7 @@ constexpr int kPlanCluster = 8;    // blocks of a call that updates in place at 
 constexpr int kPlanBlocks = 152;   // blocks of another at most
 
 __device__ __forceinline__ void cluster_barrier() {
+    __syncwarp();  // .aligned: a warp's threads come together
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

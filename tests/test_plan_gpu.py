@@ -58,6 +58,23 @@ def test_plan(sa, cuda_dev, B, new, held, extra):
     assert not (want["short"] or want["long"] or want["bad"])
 
 
+def test_the_largest_batch(sa, cuda_dev):
+    """8192 requests; in place, the most shared memory that the blocks of a cluster take."""
+    r = np.random.default_rng(4)
+    new, lens = r.integers(0, 12, 8192), r.integers(0, 40, 8192)
+    table, free, spare = _pool(lens, 4, 8192, 5)
+    want = _compare(sa, cuda_dev, new, lens, table, free, spare, int(new.sum()) + 9)
+    assert not (want["short"] or want["long"] or want["bad"])
+    done = r.random(8192) < 0.5
+    want = plain.release_pages(done, want["seq_lens"], want["block_table"], free, want["num_free"])
+    for update in (False, True):
+        f, held, left, t = _i32(free, cuda_dev), _i32(lens, cuda_dev), _i32([spare], cuda_dev), _i32(table, cuda_dev)
+        sa.plan_step(_i32(new, cuda_dev), held, t, f, left, int(new.sum()), update=True)
+        held, left = sa.release_pages(torch.from_numpy(done).to(cuda_dev), held, t, f, left, update=update)
+        assert np.array_equal(held.cpu().numpy(), want[0]) and np.array_equal(f.cpu().numpy(), want[1])
+        assert int(left) == want[2] and sa.default_status() == 0
+
+
 def test_no_requests_and_no_tokens(sa, cuda_dev):
     _compare(sa, cuda_dev, [0, 0], [5, 0], [[3], [-1]], [0, 1, 2, 3], 2, 0)
     _compare(sa, cuda_dev, [], [], np.zeros((0, 4)), [0, 1, 2], 2, 5)
