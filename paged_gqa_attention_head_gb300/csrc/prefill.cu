@@ -55,6 +55,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPSumLimit = 256.0f;  // P values (times 2^-k) stay at most 2^8
+constexpr float kPTopLimit = 32768.0f;  // 4-bit prefix: P values stay at most 2^15
 constexpr int kBM = 128;                   // query rows per tile
 constexpr int kBN = 128;                   // keys per tile
 constexpr int kThreads = 512;              // 16 warps = 4 warpgroups
@@ -360,11 +361,17 @@ __device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t zz, uint32_t zo, ui
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// 4-bit prefix: a key tile whose V values are all held times a power of two, 2^-k with k < 0 in each quarter,
+// would take P's bits with the scales, so a running maximum taken from it lies lower by the least -k: P, the row's
+// sum and O are larger by 2^that, and stay so until a tile's P passes fp16.
+__device__ __forceinline__ float lift_int4(const int4 &k) { return (float)max(0, -max(max(k.x, k.y), max(k.z, k.w))); }
+
 // One converter warp's quarter of a 4-bit prefix tile, in place: a lane takes the 32 channels of a token's
 // group at a time, 16 bytes of codes to four chunks of its row (neighbouring lanes: neighbouring tokens,
 // whose swizzled chunks meet no bank conflict).  Tokens from `rows` on (of the quarter) become zeros,
-// whatever lies there.  K: bf16 values, exactly.  V: fp16 values times 2^-k, |value| 2^-k < 2^15, k from
-// the quarter's largest scale; returns k (8 or more: out of range).
+// whatever lies there.  K: bf16 values, exactly.  V: fp16 values times 2^-k, k from the quarter's largest
+// scale: |value| 2^-k < 2^15, and a largest scale below 2^-10 is raised to it, so that fp16's steps stay below
+// its 2^-14th.  Returns k (8 or more: out of range).
 template <int D, bool kV>
 __device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane, int rows) {
     using C = PrefillCfg<D>;
@@ -380,7 +387,8 @@ __device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane,
                 const uint32_t w = *reinterpret_cast<const uint16_t *>(t + C::kOffInt4Page(2 * q + i) + 8 * D + 2 * (lane + 32 * e));
                 if (16 * i + tok < rows) mx = max(mx, w);
             }
-        kexp = max(0, (int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127 - 10);  // |code - z| <= 15
+        const int e = (int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127;  // of the largest scale
+        kexp = max(e - 10, min(0, max(e, kVScaleMinExp) + 10));              // |code - z| <= 15
     }
     const float down = __uint_as_float((uint32_t)(127 - min(kexp, 7)) << 23);
 #pragma unroll 1
@@ -727,7 +735,7 @@ static_assert(sizeof(ItemSlot) == 64, "item slot");
 // looked up by the producer with the pages and applied by the softmax page by page (16 columns
 // of S), so that no code or scale is rounded.  kInt4: it is a 4-bit cache (append_int4.cu): the
 // converters make its values, K in bf16 exactly, V in fp16 like the bf16 V tiles, so that the softmax
-// has nothing to do for it.
+// has only their exponents to do with.
 template <int D, bool kWindow, bool kFp8, bool kCausal, bool kInt8, bool kInt4>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -1479,7 +1487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                  fmaxf(mx8[6], mx8[7]));
                 };
-                if (kInt8 && j == 0 &&  // the page scales are in place once the V tile is
+                if (kSplit && j == 0 &&  // the page scales, or 4-bit's exponents, are in place once the V tile is
                     !wait_or_abort<false, kSplit>(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
                                    a.wait_limit_cycles)) {
                     ok = false;
@@ -1487,7 +1495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (j == 0) {
                     const float mt = kInt8 ? row_max() : row_max() * sc;
-                    const float mn = fmaxf(m_used, mt);
+                    float mn = fmaxf(m_used, mt);
+                    if (kInt4) mn -= lift_int4(*reinterpret_cast<const int4 *>(s_vscale + (tcount - 1) % NS * 4));
                     l = (m_used == -INFINITY) ? 0.f : l * fast_exp2(m_used - mn);
                     m_used = mn;
                 }
@@ -1504,11 +1513,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool pwait = C::kSplitP && i >= (uint32_t)NBP, pfail = false;
                 const int4 kq = *reinterpret_cast<const int4 *>(s_vscale + vst * 4);
                 const float2 sc2 = make_float2(sc, sc);
+                float p_top = 0.f;  // 4-bit: the largest sum of a chunk's P * 2^k
                 // writes P against the running max m_used; returns the row's sum of P * 2^-k
                 const bool f8 = kFp8 && fold8 && tt < gm.n_pre;  // warp-uniform
                 auto emit = [&](bool again) {
                     const float neg0 = m_used == -INFINITY ? 0.f : -m_used;
                     float tl = 0.f;
+                    p_top = 0.f;
 #pragma unroll
                     for (int ch = 0; ch < kBN / 32; ++ch) {
                         const int kc = ch == 0 ? kq.x : ch == 1 ? kq.y : ch == 2 ? kq.z : kq.w;
@@ -1552,10 +1563,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kInt8)
                             tl += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) * pmul.x +
                                   ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y)) * pmul.y;
-                        else
-                            tl += (((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
-                                   ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y))) *
-                                  (f8 ? mul8 : __uint_as_float((uint32_t)(127 - kc) << 23));
+                        else {
+                            const float sum = ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
+                                              ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
+                            if (kInt4) p_top = fmaxf(p_top, sum);
+                            tl += sum * (f8 ? mul8 : __uint_as_float((uint32_t)(127 - kc) << 23));
+                        }
                     }
                     return tl;
                 };
@@ -1565,8 +1578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 if (j > 0) {
-                    // every P * 2^-k at most 2^8 (so P fits fp16) unless the row's sum passes it
-                    const bool need = !(tl <= kPSumLimit) || m_used == -INFINITY;
+                    // every P * 2^-k at most 2^8 (so P fits fp16) unless the row's sum passes it; 4-bit: P
+                    // itself, since the maximum may be lifted
+                    const bool need = !(kInt4 ? p_top <= kPTopLimit : tl <= kPSumLimit) || m_used == -INFINITY;
                     if (__any_sync(0xffffffffu, need)) {
                         const float drop = kInt8 ? s_page[vst].drop : 1.f;
                         // the row max, a rescale of O and l, and P again (the P written above is
@@ -1579,7 +1593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         tc::fence_after_sync();
-                        const float mn = fmaxf(m_used, mt);
+                        const float mn = fmaxf(m_used, kInt4 ? mt - lift_int4(kq) : mt);
                         float alpha = need && mn > m_used ? fast_exp2(m_used - mn) : 1.f;
                         if (need && mn > m_used) {
                             l *= alpha;
