@@ -16,9 +16,11 @@
 // word, channel c at bit 4 (c / 2) + 16 (c % 2): masking a word with 0x000f000f leaves a pair of
 // neighbouring channels, or, after a transposing load, one channel of two neighbouring tokens.
 //
-// Bound by HBM for long appends and for unpacking, by latency for a decode step.  A warp holds eight
-// tokens of one head, four lanes to a group, all groups of K and V at once: reads of 64 bytes and,
-// where the tokens' slots follow each other, writes of 128.
+// Bound by HBM and instruction issue alike for long appends and for unpacking, by latency for a decode step.  A
+// warp holds eight tokens of one head, four lanes to a group, all groups of K and V at once: reads of 64 bytes
+// and, where the tokens' slots follow each other, writes of 128.  Measured: 16381 tokens of 4 heads of 128
+// appended in 9.5 us (4.5 TB/s, issue slots 0.63; 14.1 us with exact divisions and single elements in the
+// range), their 1033 pages unpacked in 7.7 us (5.6 TB/s); 64 single tokens of 8 heads of 64 in 2.3 us.
 #include "internal.h"
 #include "ptx.cuh"
 

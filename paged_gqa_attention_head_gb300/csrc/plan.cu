@@ -10,7 +10,8 @@
 // token that begins a page writes the page's table entry.  Releases push in the opposite order, so
 // that releasing what the last plan took leaves the list as it was.
 //
-// Both are bound by latency: the lengths, the list's entry and the stores one after the other.
+// Both are bound by latency: the lengths, the list's entry and the stores one after the other.  Measured: 24
+// prompts with 43 k new tokens 4.5 us, 256 single tokens 4.6 us, 64 requests' 104 k pages released 3.6 us.
 // A captured step carries the lengths and the list's size on from replay to replay, so their new
 // values may lie where the old ones are.  Then the blocks are one cluster, and its barrier lies
 // between the reads and the writes; otherwise they are a plain grid, which is launched sooner (a cluster's
