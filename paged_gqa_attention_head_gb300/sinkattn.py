@@ -689,9 +689,9 @@ def _status_args(index: int) -> tuple:
 def default_status(device=None) -> int:
     """Read and clear the status bits (STATUS_*) of the calls on a CUDA device (default: the current
     one) that were given no workspace_buf: append_kv, append_kv_fp8, append_kv_int8, qk_norm_rope,
-    decode_int8, prefill_int8, the 4-bit cache's calls and the page plan, from any thread or stream, eager or replayed from a graph.  It waits
-    for the current stream; work on others counts once it has run.  Call it once before a first
-    capture, so that the captured calls have a word to report to."""
+    decode_int8, prefill_int8, the 4-bit cache's calls and the page plan, from any thread or stream,
+    eager or replayed from a graph.  It waits for the current stream; work on others counts once it has
+    run.  Call it once before a first capture, so that the captured calls have a word to report to."""
     index = torch.device("cuda" if device is None else device).index
     return get_status(_status_buffer(_current_device() if index is None else index))
 
@@ -1069,11 +1069,12 @@ def plan_step(new_lens, seq_lens, block_table, free_pages, num_free, max_tokens,
               workspace_buf=None) -> StepPlan:
     """Block-table entries, slots, positions and lengths of a serving step, on the device
     (sinkattn_plan_step).  new_lens, seq_lens int32 [B]: tokens that each request brings and holds;
-    block_table int32 [B, columns] is updated in place; free_pages int32 [num_pages], num_free int32 [1]:
-    the free pages, a stack; max_tokens: rows of the packed step (those behind the last request are
-    padding).  update: seq_lens and num_free take their new values in place, as a captured step needs;
-    else they stay, and the plan holds the new ones.  STATUS_NO_PAGES in workspace_buf's header, without one in
-    default_status, tells that some request was not served."""
+    block_table int32 [B, columns] is updated in place; free_pages int32 [num_pages] (as long as the
+    pool, however few are free), num_free int32 [1]: the free pages, a stack; max_tokens: rows of the
+    packed step (those behind the last request are padding).  update: seq_lens and num_free take their
+    new values in place, as a captured step needs; else they stay, and the plan holds the new ones.
+    STATUS_NO_PAGES in workspace_buf's header, without one in default_status, tells that some request was
+    not served."""
     dev = _need_cuda(new_lens, "new_lens")
     _need_dense(new_lens, "new_lens", torch.int32, dev, 1)
     B, columns, pages = _need_page_list(seq_lens, block_table, free_pages, num_free, dev)
