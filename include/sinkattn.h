@@ -76,7 +76,8 @@ typedef enum sinkattn_error {
                                              * INT8 append: a K or V value not finite;
                                              * INT8 prefill: a V scale of 2^15 or more;
                                              * 4-bit append: a K or V value not finite;
-                                             * 4-bit prefill: a V scale of 2^18 or more */
+                                             * 4-bit prefill: a V scale of 2^18 or more, a K scale of
+                                             * 2^34 or more */
 #define SINKATTN_STATUS_NO_PAGES 0x20u      /* page plan: too few free pages for a request */
 
 /* Shapes of a paged KV cache and of the heads that read it. */
@@ -478,10 +479,12 @@ int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *blo
 
 /* Chunked prefill over such a prefix: sinkattn_prefill with the prefix pages in 4 bits (the pages, the
  * block table and the prefix lengths are required; prefix lengths may be 0); the new tokens' k, v stay
- * bf16.  It computes what sinkattn_prefill does over a bf16 prefix of the same values: K exactly, V in
- * fp16 under a power of two for each 32 keys, which holds the values of the largest scale among them
- * exactly and the others to 2^-15 of it, whatever its size (from 2^-100 on).  V scales of 2^18 or more set
- * SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified).  status: as for the decode.  Other arguments
+ * bf16.  It computes what sinkattn_prefill does over a bf16 prefix of the same values: K exactly (scales
+ * from 2^-60 on), V in fp16 under a power of two for each 32 keys, which holds the values of the largest
+ * scale among them exactly and the others to 2^-15 of it, whatever its size (from 2^-100 on; the new
+ * tokens' V likewise).  K scales of 2^34 or more and V scales of 2^18 or more set
+ * SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be below 2^80 (else
+ * SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.  Other arguments
  * and errors as for sinkattn_prefill, the workspace as for sinkattn_prefill_int8 (with
  * sinkattn_prefill_int4_workspace_size bytes, calls with few query rows split their prefixes). */
 int sinkattn_prefill_int4_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,

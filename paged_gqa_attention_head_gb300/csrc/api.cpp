@@ -3,6 +3,7 @@
 // memory is allocated here; scratch lives in the caller's workspace.
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 #include <math.h>
 #include <stdio.h>
@@ -945,6 +946,7 @@ int sinkattn_prefill_int4(const void *q, const void *k, const void *v, const int
     if (total_tokens < 0) return SINKATTN_ERR_INVALID_ARG;
     if (desc->num_seqs == 0 || total_tokens == 0) return SINKATTN_OK;  // no tokens: a no-op
     if (!kv_pages || !prefix_block_table || !prefix_lens || !aligned(status, 4)) return SINKATTN_ERR_INVALID_ARG;
+    if (scale >= 1.2089258e24f && scale <= FLT_MAX) return SINKATTN_ERR_UNSUPPORTED;  // 2^80: the kernel takes it times 2^40 log2(e)
     return prefill_common(q, k, v, cu_seqlens, total_tokens, kv_pages, kv_pages, prefix_block_table, prefix_lens, sinks,
                           scale, out, lse, desc, workspace, ws_bytes, false, nullptr, nullptr, true, stream, nullptr,
                           status, true);

@@ -99,6 +99,7 @@ struct PageScales {
     float pad[3];
 };
 constexpr int kPageScaleBytes = 240;
+constexpr int kInt4MaxExp = 26;      // 4-bit prefix: k of V scales below 2^18
 constexpr int kVScaleMinExp = -100;  // a V scale below 2^-100 (the append writes none) counts as 0
 static_assert(sizeof(PageScales) == kPageScaleBytes, "page scales");
 
@@ -332,46 +333,37 @@ __device__ __forceinline__ void convert_int8_quarter(uint8_t *t, int q, int lane
     }
 }
 
-// Eight 4-bit codes (a word) less z, times their group's scale, as one 16-byte vector.  kV false: bf16
-// for K: 128 + code and 128 + z are bf16 numbers, and so are the difference (four bits) and its product
-// with a scale of four bits.  kV true: fp16 for V: 1024 + code, or 1024 + 16 code for every other pair,
-// which one multiplication and addition brings down to the difference.  zz and zo: pairs of what comes
-// off; ss: a pair of the scale.
+// Eight 4-bit codes (a word) less z, times their group's scale, as one 16-byte vector: bf16 for K, fp16 (kV)
+// for V.  Four bits in place, or four bits up, are the subnormal code * u or 16 * code * u (u = 2^-133 in
+// bf16, 2^-24 in fp16), so one multiplication and addition makes each pair of values, exactly: times the
+// scale over u (sa), or a sixteenth of it (sb), less z times the scale (c, of four and four bits).
 template <bool kV>
-__device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t zz, uint32_t zo, uint32_t ss) {
+__device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t sa, uint32_t sb, uint32_t c) {
     uint32_t o[4];
-    if (!kV) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm("{\n\t.reg .b32 d;\n\tsub.rn.bf16x2 d, %1, %2;\n\tmul.rn.bf16x2 %0, d, %3;\n\t}"
-                : "=r"(o[j])
-                : "r"(((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u), "r"(zz), "r"(ss));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            const uint32_t h = w >> (4 * j);
-            asm("{\n\t.reg .b32 d;\n\tsub.rn.f16x2 d, %1, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
-                : "=r"(o[j])
-                : "r"((h & 0x000F000Fu) | 0x64006400u), "r"(zz), "r"(ss));
-            asm("{\n\t.reg .b32 d;\n\tfma.rn.f16x2 d, %1, %4, %2;\n\tmul.rn.f16x2 %0, d, %3;\n\t}"
-                : "=r"(o[j + 1])
-                : "r"((h & 0x00F000F0u) | 0x64006400u), "r"(zo), "r"(ss), "r"(0x2C002C00u));  // 1/16
-        }
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t h = j < 2 ? w : w >> 8, x = h & (j & 1 ? 0x00F000F0u : 0x000F000Fu), m = j & 1 ? sb : sa;
+        if (kV)
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(o[j]) : "r"(x), "r"(m), "r"(c));
+        else
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[j]) : "r"(x), "r"(m), "r"(c));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
+constexpr float kInt4KUp = 1099511627776.f;  // 2^40: K tiles hold values over it, so that the scale over 2^-133 is a bf16 number
+constexpr uint32_t kInt4KMax = 0x5080u;      // 2^34: K scales from here on do not fit
 
-// 4-bit prefix: a key tile whose V values are all held times a power of two, 2^-k with k < 0 in each quarter,
-// would take P's bits with the scales, so a running maximum taken from it lies lower by the least -k: P, the row's
-// sum and O are larger by 2^that, and stay so until a tile's P passes fp16.
-__device__ __forceinline__ float lift_int4(const int4 &k) { return (float)max(0, -max(max(k.x, k.y), max(k.z, k.w))); }
+// 4-bit prefix: a tile's V values are held times 2^-k, k of each quarter, and P times 2^k.  A running maximum
+// taken from the tile lies higher by the largest k, so that P * 2^k starts at 1 whatever the values' size; it
+// stays until a tile's P passes fp16.
+__device__ __forceinline__ float rise_int4(const int4 &k) { return (float)max(max(k.x, k.y), max(k.z, k.w)); }
 
 // One converter warp's quarter of a 4-bit prefix tile, in place: a lane takes the 32 channels of a token's
 // group at a time, 16 bytes of codes to four chunks of its row (neighbouring lanes: neighbouring tokens,
 // whose swizzled chunks meet no bank conflict).  Tokens from `rows` on (of the quarter) become zeros,
-// whatever lies there.  K: bf16 values, exactly.  V: fp16 values times 2^-k, k from the quarter's largest
-// scale: |value| 2^-k < 2^15, and a largest scale below 2^-10 is raised to it, so that fp16's steps stay below
-// its 2^-14th.  Returns k (8 or more: out of range).
+// whatever lies there.  K: bf16 values over 2^40, exactly; returns whether a scale is out of range.  V: fp16 values
+// times 2^-k, k from the quarter's largest scale, which becomes 2^-9 and more: the largest that fp16 holds over
+// 2^-24, and its values exactly, smaller ones' to 2^-16 of it.  Returns k.
 template <int D, bool kV>
 __device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane, int rows) {
     using C = PrefillCfg<D>;
@@ -387,10 +379,11 @@ __device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane,
                 const uint32_t w = *reinterpret_cast<const uint16_t *>(t + C::kOffInt4Page(2 * q + i) + 8 * D + 2 * (lane + 32 * e));
                 if (16 * i + tok < rows) mx = max(mx, w);
             }
-        const int e = (int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127;  // of the largest scale
-        kexp = max(e - 10, min(0, max(e, kVScaleMinExp) + 10));              // |code - z| <= 15
+        kexp = max((int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127, kVScaleMinExp) + 9;
     }
-    const float down = __uint_as_float((uint32_t)(127 - min(kexp, 7)) << 23);
+    // 2^(24 - k) and 2^-k (k out of range is the caller's to report)
+    const float up = __uint_as_float((uint32_t)(151 - min(kexp, kInt4MaxExp)) << 23);
+    bool bad = false;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const int p = 2 * q + i;
@@ -408,26 +401,29 @@ __device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane,
             const int g = 2 * e + (lane >> 4);
             if (16 * i + tok >= rows) w[e] = 0;
             const uint32_t z = (w[e] & 15u) * 0x10001u;
-            uint32_t zz, zo = 0, ss;
+            uint32_t sa, sb, c;
             if (kV) {
-                zz = z | 0x64006400u;                                                          // 1024 + z
-                asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(zo) : "r"(0x63806380u), "r"(zz));  // 960 - (1024 + z)
-                const float s = __uint_as_float((w[e] & 0xFFF0u) << 16) * down;
-                ss = pack_f16x2(s, s);
+                const float s = __uint_as_float((w[e] & 0xFFF0u) << 16) * up;
+                sa = pack_f16x2(s, s);
+                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(sb) : "r"(sa), "r"(0x2C002C00u));             // 1/16
+                asm("{\n\t.reg .b32 n;\n\tneg.f16x2 n, %1;\n\tmul.rn.f16x2 %0, n, %2;\n\t}" : "=r"(c) : "r"(sa), "r"(z));
             } else {
-                zz = z | 0x43004300u;  // 128 + z
-                ss = (w[e] & 0xFFF0u) * 0x10001u;
+                const uint32_t s = (w[e] & 0xFFF0u) * 0x10001u;
+                bad |= w[e] >= kInt4KMax;
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(sa) : "r"(s), "r"(0x6E006E00u));  // 2^93
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(sb) : "r"(s), "r"(0x6C006C00u));  // 2^89
+                asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %1;\n\tmul.rn.bf16x2 %0, n, %2;\n\t}" : "=r"(c) : "r"(sa), "r"(z));
             }
             uint8_t *dst = t + (g >> 1) * 16384;
             const int row = kPageSize * p + tok, c0 = 4 * (g & 1);
-            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 0)) = int4x8<kV>(x[e].x, zz, zo, ss);
-            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 1)) = int4x8<kV>(x[e].y, zz, zo, ss);
-            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 2)) = int4x8<kV>(x[e].z, zz, zo, ss);
-            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 3)) = int4x8<kV>(x[e].w, zz, zo, ss);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 0)) = int4x8<kV>(x[e].x, sa, sb, c);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 1)) = int4x8<kV>(x[e].y, sa, sb, c);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 2)) = int4x8<kV>(x[e].z, sa, sb, c);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 3)) = int4x8<kV>(x[e].w, sa, sb, c);
         }
         __syncwarp();
     }
-    return kexp;
+    return kV ? kexp : (int)bad;
 }
 
 // Work list, in two parts.  (A) Requests with a paged prefix, request by request (each
@@ -1278,9 +1274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (fp8_tile && kInt4)
-                        convert_int4_quarter<D, false>(sK + st * C::kKVBytes, q, lane, gm.P - (gm.t0 + j) * kBN - 32 * q);
-                    else if (fp8_tile && kInt8)
+                    if (fp8_tile && kInt4) {
+                        if (convert_int4_quarter<D, false>(sK + st * C::kKVBytes, q, lane, gm.P - (gm.t0 + j) * kBN - 32 * q))
+                            set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
+                    } else if (fp8_tile && kInt8)
                         convert_int8_quarter<D, 3>(sK + st * C::kKVBytes, q, lane);
                     else if (fp8_tile)
                         convert_fp8_quarter<D, 0>(sK + st * C::kKVBytes, q, lane, 1.f);
@@ -1299,9 +1296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     int kexp4 = 0;
                     if (kInt4) {
                         kexp4 = convert_int4_quarter<D, true>(sV + st * C::kKVBytes, q, lane, gm.P - (gm.t0 + j) * kBN - 32 * q);
-                        if (kexp4 > 7) {
+                        if (kexp4 > kInt4MaxExp) {
                             if (lane == 0) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
-                            kexp4 = 7;
+                            kexp4 = kInt4MaxExp;
                         }
                     } else if (kInt8)
                         convert_int8_quarter<D, 4>(sV + st * C::kKVBytes, q, lane, s_page[st].v2);
@@ -1343,10 +1340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
                     kexp = min(kexp, 7);
                 }
+                // 4-bit: the values come to lie as the prefix's do, the largest at 2^-6 and more, so that either's
+                // P keeps its bits beside the other
+                if (kInt4) kexp = min(max((int)(mx >> 7) - 127, kVScaleMinExp), 21) + 6;
                 const float sc = __uint_as_float((uint32_t)(127 - kexp) << 23);  // 2^-k
 #pragma unroll 1
                 for (int hf = 0; hf < C::kHalves; ++hf) {
-                    if (kexp == 0) {
+                    if (!kInt4 && kexp == 0) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             uint4 *pw = vt + hf * 1024 + e * 32;
@@ -1405,7 +1405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t = it.qb * kBM + r;  // position among the request's new tokens
             const float sink2 = s_slot[k % kItemRing].sink2[x];
             // score scale of FP8 prefix tiles: their K holds code values, the K scale joins here
-            const float sc_pre = kFp8 ? a.scale_log2 * s_slot[k % kItemRing].kscale : a.scale_log2;
+            const float sc_pre = kFp8 ? a.scale_log2 * s_slot[k % kItemRing].kscale : kInt4 ? a.scale_log2 * kInt4KUp : a.scale_log2;
             // FP8 prefix V in the converters' power-of-two form: P of those keys times m8, the
             // mantissa of v_scale (m8 in [1, 2), so P * m8 < 2^9 stays in fp16)
             const float vsc8 = kFp8 ? s_slot[k % kItemRing].vscale : 1.f;
@@ -1466,7 +1466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                const float sc = kFp8 && tt < gm.n_pre ? sc_pre : a.scale_log2;
+                const float sc = (kFp8 || kInt4) && tt < gm.n_pre ? sc_pre : a.scale_log2;
                 // row max: eight chains of three-input maxima over 16 keys each
                 auto row_max = [&]() {
                     float mx8[8];
@@ -1496,7 +1496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j == 0) {
                     const float mt = kInt8 ? row_max() : row_max() * sc;
                     float mn = fmaxf(m_used, mt);
-                    if (kInt4) mn -= lift_int4(*reinterpret_cast<const int4 *>(s_vscale + (tcount - 1) % NS * 4));
+                    if (kInt4) mn += rise_int4(*reinterpret_cast<const int4 *>(s_vscale + (tcount - 1) % NS * 4));
                     l = (m_used == -INFINITY) ? 0.f : l * fast_exp2(m_used - mn);
                     m_used = mn;
                 }
@@ -1593,7 +1593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         tc::fence_after_sync();
-                        const float mn = fmaxf(m_used, kInt4 ? mt - lift_int4(kq) : mt);
+                        const float mn = fmaxf(m_used, kInt4 ? mt + rise_int4(kq) : mt);
                         float alpha = need && mn > m_used ? fast_exp2(m_used - mn) : 1.f;
                         if (need && mn > m_used) {
                             l *= alpha;

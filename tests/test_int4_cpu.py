@@ -166,6 +166,7 @@ def test_prefill_int4_rejects(sa):
                dict(scale=float("nan")), dict(d=_desc(sa, num_pages=0))):
         assert pre(**kw) == 1, kw
     assert pre(wb=128) == 3
+    assert pre(scale=float("inf")) == 1 and pre(scale=2.0 ** 80) == 2
     assert pre(d=_desc(sa, head_dim=32)) == 2
     assert pre(T=0, q=None, kv=None) == 0 and pre(d=_desc(sa, num_seqs=0), q=None) == 0
     n = ctypes.c_size_t()

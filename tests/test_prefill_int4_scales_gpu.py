@@ -4,8 +4,8 @@ precision whatever their size, as the decode's over the same cache does.
 Tolerance: that of test_int4_gpu.py, relative to the largest |v| a row sees, so it shrinks with the
 scales.  (What the powers of two add: fp16's steps of V, 2^-15 of the largest scale in 32 keys, and of P where
 a tile's scales are smaller than those met, 2^-25 of the largest |v| for each key: 2^-14 for the 1400 here,
-together within the fp32 scores' 2^-12, which these small scores do not use up.)  The new rows' V are
-zeros (in fp16 they have no such range), and their keys count."""
+together within the fp32 scores' 2^-12, which these small scores do not use up.)  Where the prefix alone is
+small the new rows' V are zeros, and their keys count."""
 import numpy as np
 import pytest
 import torch
@@ -93,3 +93,43 @@ def test_scores_that_rise_and_sinks_above_them(sa, cuda_dev, D, top):
     check(*sa.prefill_int4(*_pre(p, cuda_dev, kv)), ref)
     ws = torch.zeros(256, dtype=torch.uint8, device=cuda_dev)
     check(*sa.prefill_int4(*_pre(p, cuda_dev, kv), workspace_buf=ws), ref)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e", [-60, -20, 0, 12, 20])
+def test_k_scales_of_every_size(sa, cuda_dev, D, e):
+    """K scales times 2^e against queries and new keys times powers of two that keep the scores' size."""
+    p = inputs.make_prefill([40, 9], 8, 2, D, seed=15, prefix_lens=[700, 130], poison=False)
+    kv = _scaled(inputs.pack_int4(p.prefix.k_pages, p.prefix.v_pages), D,
+                 lambda shape: np.exp2(np.array([e, 0.0]))[None, None, :, None] * np.ones(shape))
+    p.q = (p.q.double() * 2.0 ** -e).to(torch.bfloat16)
+    p.k = (p.k.double() * 2.0 ** e).to(torch.bfloat16)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv)), _pre_ref(p, kv=kv))
+    assert sa.default_status() == 0
+
+
+@pytest.mark.parametrize("e", [-100, -50, -20, -3, 10])
+def test_new_values_of_every_size(sa, cuda_dev, e):
+    """The new tokens' V times 2^e, alone and beside a prefix of the same size."""
+    p = inputs.make_prefill([200, 30], 8, 2, 64, seed=16, prefix_lens=[0, 700], poison=False)
+    kv = _v_times(p, np.full(p.prefix.num_pages, float(e)))
+    p.v = (inputs.make_prefill([200, 30], 8, 2, 64, seed=16, prefix_lens=[0, 700], poison=False).v.double() * 2.0 ** e).to(
+        torch.bfloat16)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv)), _pre_ref(p, kv=kv))
+    assert sa.default_status() == 0
+
+
+def test_k_scales_out_of_range(sa, cuda_dev):
+    """2^34 is reported, where a token's word is; in a slot that holds none it is nothing."""
+    p = inputs.make_prefill([20], 8, 1, 64, seed=17, prefix_lens=[100], poison=False)
+    kv = inputs.pack_int4(p.prefix.k_pages, p.prefix.v_pages)
+    ref = _pre_ref(p, kv=kv)
+    last = int(p.prefix.block_table[0, 6])
+    words = kv.view(torch.int16)[:, :, 0, 8].view(-1, 1, 2, 16)  # [page, head, group, token]
+    words[last, 0, 1, 4:] = 0x5080
+    sa.default_status()
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv)), ref)
+    assert sa.default_status() == 0
+    words[last, 0, 1, 3] = 0x5080
+    sa.prefill_int4(*_pre(p, cuda_dev, kv))
+    assert sa.default_status() == sa.STATUS_VALUE_RANGE
