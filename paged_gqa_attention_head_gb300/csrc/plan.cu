@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(kPlanThreads) release_pages_kernel(const PlanA
 
 template <typename Kernel>
 cudaError_t launch_plan(Kernel kernel, const PlanArgs &a, bool in_place, int64_t items, int smem, cudaStream_t stream) {
-    if (smem > 48 * 1024) {
+    // up to 48 KB, static and dynamic together, need no leave
+    if (smem > 40 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
