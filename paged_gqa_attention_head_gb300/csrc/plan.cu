@@ -278,12 +278,17 @@ __global__ void __launch_bounds__(kPlanThreads) release_pages_kernel(const PlanA
     }
 }
 
+// Shared memory of a plan's and of a release's lengths and offsets.
+constexpr int plan_smem(int B) { return (3 * B + 1) * 4; }
+constexpr int release_smem(int B) { return 2 * B * 4; }
+
 template <typename Kernel>
 cudaError_t launch_plan(Kernel kernel, const PlanArgs &a, bool in_place, int64_t items, int smem, cudaStream_t stream) {
-    // up to 48 KB, static and dynamic together, need no leave
+    // Up to 48 KB, static and dynamic together, need no leave.  What is asked for is the most that any call takes, so
+    // that no call lowers what another thread is about to launch with.
     if (smem > 40 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, plan_smem(kPlanMaxSeqs));
         if (e != cudaSuccess) return e;
     }
     // Few requests, few threads: they are set up sooner.  Four items a thread.
@@ -315,13 +320,13 @@ bool in_place(const PlanArgs &a) { return a.num_free == a.num_free_out || a.seq_
 }  // namespace
 
 cudaError_t launch_plan_step(const PlanArgs &a, cudaStream_t stream) {
-    return launch_plan(plan_step_kernel, a, in_place(a), a.max_tokens, (3 * a.B + 1) * 4, stream);
+    return launch_plan(plan_step_kernel, a, in_place(a), a.max_tokens, plan_smem(a.B), stream);
 }
 
 cudaError_t launch_release_pages(const PlanArgs &a, cudaStream_t stream) {
     // how many pages there are to release only the device knows: at most every page
     const int64_t most = (int64_t)a.B * a.max_pages;
-    return launch_plan(release_pages_kernel, a, in_place(a), most < a.num_pages ? most : a.num_pages, 2 * a.B * 4, stream);
+    return launch_plan(release_pages_kernel, a, in_place(a), most < a.num_pages ? most : a.num_pages, release_smem(a.B), stream);
 }
 
 }  // namespace sinkattn
