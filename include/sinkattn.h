@@ -483,9 +483,10 @@ int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *blo
  * from 2^-60 on), V in fp16 under a power of two for each 32 keys, which holds the values of the largest
  * scale among them exactly and the others to 2^-15 of it, whatever its size (from 2^-100 on; the new
  * tokens' V likewise).  A probability enters times that power of two, rounded to fp16: relative 2^-11 at
- * most, and from 2^14 below the largest of its row on 2^-25 of that.  K scales of 2^34 or more and V
- * scales of 2^18 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be below
- * 2^80 (else SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.  Other arguments and errors as for
+ * most, and from 2^20 below the largest such product of the keys that its row sees on (a sink counts with
+ * the power of that product) 2^-31 of that.  K scales of 2^34 or more and V scales of 2^18 or more set
+ * SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be below 2^80 (else
+ * SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.  Other arguments and errors as for
  * sinkattn_prefill, the workspace as for sinkattn_prefill_int8 (with sinkattn_prefill_int4_workspace_size
  * bytes, calls with few query rows split their prefixes). */
 int sinkattn_prefill_int4_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,

@@ -56,7 +56,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPSumLimit = 256.0f;  // P values (times 2^-k) stay at most 2^8
-constexpr float kPTopLimit = 32768.0f;  // 4-bit prefix: P values stay at most 2^15
+// 4-bit prefix: P * 2^k of a row's largest product starts at 2^6, and its maximum moves once one passes fp16's largest
+// number.  (From 2^8 on, rows that begin with few keys move often: 8 x 512 over 16385, window 128, 78.5 us where 2^6
+// takes 72.2 and 1 71.5.)
+constexpr float kInt4Start = 6.f, kInt4PLimit = 65504.f;
 constexpr int kBM = 128;                   // query rows per tile
 constexpr int kBN = 128;                   // keys per tile
 constexpr int kThreads = 512;              // 16 warps = 4 warpgroups
@@ -354,11 +357,6 @@ __device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t sa, uint32_t sb, ui
 }
 constexpr float kInt4KUp = 1099511627776.f;  // 2^40: K tiles hold values over it, so that the scale over 2^-133 is a bf16 number
 constexpr uint32_t kInt4KMax = 0x5080u;      // 2^34: K scales from here on do not fit
-
-// 4-bit prefix: a tile's V values are held times 2^-k, k of each quarter, and P times 2^k.  A running maximum
-// taken from the tile lies higher by the largest k, so that P * 2^k starts at 1 whatever the values' size; it
-// stays until a tile's P passes fp16.
-__device__ __forceinline__ float rise_int4(const int4 &k) { return (float)max(max(k.x, k.y), max(k.z, k.w)); }
 
 // One converter warp's quarter of a 4-bit prefix tile, in place: a lane takes the 32 channels of a token's
 // group at a time, 16 bytes of codes to four chunks of its row (neighbouring lanes: neighbouring tokens,
@@ -1417,6 +1415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float add8 = log2f(m8), mul8 = 1.f / m8;
             float m_used = sink2;                      // running max, seeded with the sink
             float l = sink2 == -INFINITY ? 0.f : 1.f;  // running denominator: e^(sink - m) = 1
+            bool fresh = true;                         // 4-bit: the row has seen no key yet
             for (int j = 0; j < gm.n_kv; ++j) {
                 const uint32_t i = tcount * ntiles + x;  // number of this S product
                 const int b = i % NBS, pb = i % NBP;
@@ -1469,7 +1468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float sc = (kFp8 || kInt4) && tt < gm.n_pre ? sc_pre : a.scale_log2;
-                // row max: eight chains of three-input maxima over 16 keys each
+                // row max (4-bit: of P * 2^k): eight chains of three-input maxima over 16 keys each
+                float top_score = 0.f;  // 4-bit: of the scores alone, over 2^kInt4Start too
                 auto row_max = [&]() {
                     float mx8[8];
                     float kf[8];
@@ -1486,21 +1486,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mx8[e] = fmaxf(m, sf[15]);
                         if (kInt8) mx8[e] *= kf[e];
                     }
+                    if (kInt4) {  // over 2^kInt4Start; of a quarter's scores and k (-inf where the row sees nothing of it)
+                        const int4 k = *reinterpret_cast<const int4 *>(s_vscale + (tcount - 1) % NS * 4);
+                        const float x[4] = {fmaf(fmaxf(mx8[0], mx8[1]), sc, -kInt4Start), fmaf(fmaxf(mx8[2], mx8[3]), sc, -kInt4Start),
+                                            fmaf(fmaxf(mx8[4], mx8[5]), sc, -kInt4Start), fmaf(fmaxf(mx8[6], mx8[7]), sc, -kInt4Start)};
+                        top_score = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                        return fmaxf(fmaxf(x[0] + (float)k.x, x[1] + (float)k.y), fmaxf(x[2] + (float)k.z, x[3] + (float)k.w));
+                    }
                     return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                  fmaxf(mx8[6], mx8[7]));
                 };
-                if (kSplit && j == 0 &&  // the page scales, or 4-bit's exponents, are in place once the V tile is
+                const bool begins = kInt4 && kWindow ? __any_sync(0xffffffffu, fresh) : j == 0;
+                if (kSplit && begins &&  // the page scales, or 4-bit's exponents, are in place once the V tile is
                     !wait_or_abort<false, kSplit>(&bars.v_conv[(tcount - 1) % NS], ((tcount - 1) / NS) & 1, s_abort, a.status,
                                    a.wait_limit_cycles)) {
                     ok = false;
                     break;
                 }
-                if (j == 0) {
-                    const float mt = kInt8 ? row_max() : row_max() * sc;
+                if (begins) {
+                    const float mt = kInt8 || kInt4 ? row_max() : row_max() * sc;
                     float mn = fmaxf(m_used, mt);
-                    if (kInt4) mn += rise_int4(*reinterpret_cast<const int4 *>(s_vscale + (tcount - 1) % NS * 4));
-                    l = (m_used == -INFINITY) ? 0.f : l * fast_exp2(m_used - mn);
-                    m_used = mn;
+                    if (kInt4) mn = fmaxf(m_used - kInt4Start, top_score) + (mt - top_score);  // the sink with the same k
+                    if (!kInt4 || (fresh && mt > -INFINITY)) {
+                        l = (m_used == -INFINITY) ? 0.f : l * fast_exp2(m_used - mn);
+                        m_used = mn;
+                        fresh = false;
+                    }
                 }
                 // P * 2^k = exp2(s * scale - m + k) in fp16 in the 64 columns of the P buffer
                 // (keys 2c, 2c + 1 in column c); 2^-k is the scale of the V quarter holding
@@ -1581,13 +1592,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (j > 0) {
                     // every P * 2^-k at most 2^8 (so P fits fp16) unless the row's sum passes it; 4-bit: P
-                    // itself, since the maximum may be lifted
-                    const bool need = !(kInt4 ? p_top <= kPTopLimit : tl <= kPSumLimit) || m_used == -INFINITY;
+                    // itself, whose maximum has the k in it (of a row that has seen no key it is 0)
+                    const bool need = kInt4 ? !(p_top <= kInt4PLimit) || (!kWindow && m_used == -INFINITY)
+                                            : !(tl <= kPSumLimit) || m_used == -INFINITY;
                     if (__any_sync(0xffffffffu, need)) {
                         const float drop = kInt8 ? s_page[vst].drop : 1.f;
                         // the row max, a rescale of O and l, and P again (the P written above is
                         // overwritten before p_full; rows that need nothing write the same P)
-                        const float mt = kInt8 ? row_max() : row_max() * sc;
+                        const float mt = kInt8 || kInt4 ? row_max() : row_max() * sc;
                         // O_x must hold the P.V of this query tile's previous key tile, product i - ntiles
                         const uint32_t ip = i - ntiles;
                         if (!wait_or_abort<false, kSplit>(&bars.pv_done[ip % NBP], (ip / NBP) & 1, s_abort, a.status, a.wait_limit_cycles)) {
@@ -1595,10 +1607,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         tc::fence_after_sync();
-                        const float mn = fmaxf(m_used, kInt4 ? mt + rise_int4(kq) : mt);
+                        const float mn = fmaxf(m_used, mt);
                         float alpha = need && mn > m_used ? fast_exp2(m_used - mn) : 1.f;
                         if (need && mn > m_used) {
-                            l *= alpha;
+                            if (kInt4) {  // l may be far larger than O, and the step smaller than a float
+                                const float half = fast_exp2(0.5f * (m_used - mn));
+                                l = l * half * half;
+                            } else {
+                                l *= alpha;
+                            }
                             m_used = mn;
                         }
                         if (kInt8) alpha *= drop;
