@@ -104,6 +104,7 @@ struct PageScales {
 };
 constexpr int kPageScaleBytes = 240;
 constexpr int kInt4MaxExp = 26;      // 4-bit prefix: k of V scales below 2^18
+constexpr int kInt4MinExp = -92;     // and the lowest, which the sums of P over 2^k allow
 constexpr int kVScaleMinExp = -100;  // a V scale below 2^-100 (the append writes none) counts as 0
 static_assert(sizeof(PageScales) == kPageScaleBytes, "page scales");
 
@@ -1340,9 +1341,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
                     kexp = min(kexp, 7);
                 }
-                // 4-bit: the values come to lie as the prefix's do, the largest at 2^-6 and more, so that either's
-                // P keeps its bits beside the other
-                if (kInt4) kexp = min(max((int)(mx >> 7) - 127, kVScaleMinExp), 21) + 6;
+                // 4-bit: k = 0 for a largest value from 2^-8 to 2^4, so that one far larger (which some rows may not see) costs
+                // the others few bits; half the exponent more above, since the P of a prefix of that size lies the
+                // whole exponent higher; and values of any size below
+                if (kInt4) {
+                    const int e = min((int)(mx >> 7) - 127, 21);
+                    kexp = e > 2 ? (e - 2) >> 1 : max(min(e + 8, 0), kInt4MinExp);
+                }
                 const float sc = __uint_as_float((uint32_t)(127 - kexp) << 23);  // 2^-k
 #pragma unroll 1
                 for (int hf = 0; hf < C::kHalves; ++hf) {

@@ -75,6 +75,48 @@ def test_a_later_token_of_another_quarter(sa, cuda_dev, D, pre, e):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pre", [0, 300])
+@pytest.mark.parametrize("e", [8, 14, 17, 20])
+def test_later_and_earlier_tokens_of_the_same_quarter(sa, cuda_dev, D, pre, e):
+    """Of 32 new tokens that share a power of two the last is large, or, with a window, the first."""
+    p = inputs.make_prefill([128, 60], 8, 2, D, seed=36, prefix_lens=[pre, 40], poison=False)
+    kv = inputs.pack_int4(p.prefix.k_pages, p.prefix.v_pages)
+    v = p.v.clone()
+    p.v[[31, 95, 127]] = _large(p.v[:3].shape, e, 4)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv)), _pre_ref(p, kv=kv))
+    p.v = v
+    p.v[[0, 64]] = _large(p.v[:2].shape, e, 5)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv), window=20), _pre_ref(p, 20, kv))
+    assert sa.default_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("pre", [0, 300])
+@pytest.mark.parametrize("e", [0, 10, 13, 17])
+def test_a_large_channel(sa, cuda_dev, D, pre, e):
+    """One channel of the new V is large: the others keep the precision of their own size."""
+    p = inputs.make_prefill([150, 20], 8, 2, D, seed=37, sinks=pre > 0, prefix_lens=[pre, 0], poison=False)
+    p.v[:, :, 5] = _large(p.v[:, :, 5].shape, e, 6)
+    kv = inputs.pack_int4(p.prefix.k_pages, p.prefix.v_pages)
+    ref = _pre_ref(p, kv=kv)
+    out, lse = sa.prefill_int4(*_pre(p, cuda_dev, kv))
+    check(out, lse, ref)
+    rest = [i for i in range(D) if i != 5]
+    v = p.v.clone()
+    p.v[:, :, 5] = 0.0
+    check(out[..., rest], lse, (ref[0][..., rest], ref[1], _pre_ref(p, kv=kv)[2]))
+    if not pre:
+        # a row that sees one key, no sink: that key's V.  V lies in fp16 over 2^k (k = 0 for a largest below 2^4, (e - 2) / 2
+        # for one from 2^e on), whose steps are 2^-24: eight bits are exact from 2^(k - 17) on, below that half a step
+        # of 2^(k - 24) is lost at most, and then a rounding to bf16
+        k = max(0, (e - 2) // 2)
+        for got, want in ((out[0, :4], v[0, :1]), (out[150, 4:], v[150, 1:])):
+            err = (got.cpu().double() - want.double()).abs()
+            assert bool((err <= torch.where(want.double().abs() >= 2.0 ** (k - 17), 0.0, 2.0 ** (k - 25) * (1 + 2.0 ** -8)
+                                            + 2.0 ** (k - 25))).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("sinks", [True, False])
 @pytest.mark.parametrize("e", [8, 14, 17])
 def test_tokens_before_the_window(sa, cuda_dev, D, sinks, e):
