@@ -481,8 +481,8 @@ int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *blo
  * block table and the prefix lengths are required; prefix lengths may be 0); the new tokens' k, v stay
  * bf16.  It computes what sinkattn_prefill does over a bf16 prefix of the same values: K exactly (scales
  * from 2^-60 on), V in fp16 over a power of two 2^k for each 32 keys, whatever its size (from 2^-100 on).
- * The prefix's values come to lie below 2^-4: those of the largest scale among the 32 exactly, the others to
- * 2^-15 of it.  Of the new tokens' V, whose largest lies between 2^e and 2^(e + 1), those from 2^(k - 17) on
+ * The prefix's values come to lie below 2^-4, or below 2^11 where the scales of 32 keys lie more than 2^8
+ * apart: those of scales up to 2^27 below the largest are exact, the others to 2^-31 of it.  Of the new tokens' V, whose largest lies between 2^e and 2^(e + 1), those from 2^(k - 17) on
  * are exact and the others off by 2^(k - 25) at most, k = 0 for e from -8 to 3, (e - 2) / 2 above, e + 8 below.
  * A probability enters times 2^k, rounded to fp16: relative 2^-11 at most, and from 2^20 below the largest
  * such product of the keys that its row sees on (a sink counts with the k of that product) 2^-31 of that.  K scales of 2^34 or more and V scales of 2^18 or more set

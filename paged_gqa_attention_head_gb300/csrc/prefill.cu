@@ -356,34 +356,95 @@ __device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t sa, uint32_t sb, ui
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
+// The same for fp16 values above what that reaches: code less z over 2^9 (c: less z over 2^9), times the scale times 2^9.
+__device__ __forceinline__ uint4 int4x8_wide(uint32_t w, uint32_t s9, uint32_t c) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t h = j < 2 ? w : w >> 8, x = h & (j & 1 ? 0x00F000F0u : 0x000F000Fu), m = j & 1 ? 0x68006800u : 0x78007800u;  // 2^11, 2^15
+        asm("{\n\t.reg .b32 d;\n\tfma.rn.f16x2 d, %1, %2, %3;\n\tmul.rn.f16x2 %0, d, %4;\n\t}" : "=r"(o[j]) : "r"(x), "r"(m), "r"(c), "r"(s9));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
 constexpr float kInt4KUp = 1099511627776.f;  // 2^40: K tiles hold values over it, so that the scale over 2^-133 is a bf16 number
 constexpr uint32_t kInt4KMax = 0x5080u;      // 2^34: K scales from here on do not fit
+
+// The loop over the quarter's pages where V's scales lie far apart; up: 2^(9 - k).  (Apart from the other: with both in
+// one loop the long chunks take 1413 us where this takes 1308.)
+template <int D>
+__device__ __forceinline__ void convert_int4_wide(uint8_t *t, int q, int lane, int rows, float up) {
+    using C = PrefillCfg<D>;
+    constexpr int N = D / 64;
+    const int tok = lane & 15;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int p = 2 * q + i;
+        const uint8_t *src = t + C::kOffInt4Page(p);
+        uint4 x[N];
+        uint32_t w[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            x[e] = *reinterpret_cast<const uint4 *>(src + 16 * (lane + 32 * e));
+            w[e] = *reinterpret_cast<const uint16_t *>(src + 8 * D + 2 * (lane + 32 * e));
+        }
+        __syncwarp();  // a page's rows cover its codes
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int g = 2 * e + (lane >> 4);
+            const uint32_t word = 16 * i + tok < rows ? w[e] : 0, z = (word & 15u) * 0x10001u;
+            const float s = __uint_as_float((word & 0xFFF0u) << 16) * up;
+            const uint32_t s9 = pack_f16x2(s, s);
+            uint32_t c;
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(c) : "r"(z), "r"(0xF800F800u));  // -2^15
+            uint8_t *dst = t + (g >> 1) * 16384;
+            const int row = kPageSize * p + tok, c0 = 4 * (g & 1);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 0)) = int4x8_wide(x[e].x, s9, c);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 1)) = int4x8_wide(x[e].y, s9, c);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 2)) = int4x8_wide(x[e].z, s9, c);
+            *reinterpret_cast<uint4 *>(dst + sw128(row, c0 + 3)) = int4x8_wide(x[e].w, s9, c);
+        }
+        __syncwarp();
+    }
+}
 
 // One converter warp's quarter of a 4-bit prefix tile, in place: a lane takes the 32 channels of a token's
 // group at a time, 16 bytes of codes to four chunks of its row (neighbouring lanes: neighbouring tokens,
 // whose swizzled chunks meet no bank conflict).  Tokens from `rows` on (of the quarter) become zeros,
 // whatever lies there.  K: bf16 values over 2^40, exactly; returns whether a scale is out of range.  V: fp16 values
 // times 2^-k, k from the quarter's largest scale, which becomes 2^-9 and more: the largest that fp16 holds over
-// 2^-24, and its values exactly, smaller ones' to 2^-16 of it.  Returns k.
+// 2^-24, and the values of scales 2^12 times smaller are exact too.  With scales more than 2^8 apart (a token that not
+// every row sees, or some channels, may be the large one) it becomes 2^6, and those 2^27 times smaller are exact, for
+// one more multiplication.  Returns k.
 template <int D, bool kV>
 __device__ __forceinline__ int convert_int4_quarter(uint8_t *t, int q, int lane, int rows) {
     using C = PrefillCfg<D>;
     constexpr int N = D / 64;  // token groups of a lane and page
     const int tok = lane & 15;
     int kexp = 0;
+    bool wide = false;
     if (kV) {
-        uint32_t mx = 0;
+        uint32_t mx = 0, mn = 0xFFFFu;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const uint32_t w = *reinterpret_cast<const uint16_t *>(t + C::kOffInt4Page(2 * q + i) + 8 * D + 2 * (lane + 32 * e));
-                if (16 * i + tok < rows) mx = max(mx, w);
+                if (16 * i + tok < rows) {
+                    mx = max(mx, w);
+                    if (w >= (uint32_t)(127 + kVScaleMinExp) << 7) mn = min(mn, w);
+                }
             }
-        kexp = max((int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127, kVScaleMinExp) + 9;
+        const int top = (int)(__reduce_max_sync(0xffffffffu, mx) >> 7) - 127;
+        kexp = max(top, kVScaleMinExp) + 9;
+        wide = __any_sync(0xffffffffu, (int)(mn >> 7) - 127 < top - 8) && kexp <= kInt4MaxExp;
+        if (wide) kexp = max(top - 6, kInt4MinExp);
     }
-    // 2^(24 - k) and 2^-k (k out of range is the caller's to report)
-    const float up = __uint_as_float((uint32_t)(151 - min(kexp, kInt4MaxExp)) << 23);
+    // 2^(24 - k), or 2^(9 - k) (k out of range is the caller's to report)
+    const float up = __uint_as_float((uint32_t)((wide ? 136 : 151) - min(kexp, kInt4MaxExp)) << 23);
+    if (kV && wide) {
+        convert_int4_wide<D>(t, q, lane, rows, up);
+        return kexp;
+    }
     bool bad = false;
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import plain
 from paged_gqa_attention_head_gb300 import inputs
 from test_int4_gpu import _pre, _pre_ref, _scaled, check
 
@@ -45,6 +46,15 @@ def _times(p, exponents):
         x[:, :, 1] = np.exp2(up)[:, None, None]
         return x
     return _scaled(inputs.pack_int4(c.k_pages, c.v_pages), p.q.shape[2], f)
+
+
+def _words_times(p, up):
+    """The prefix's cache with V scales times 2^up, up [pages, heads, groups of 32 channels, tokens]."""
+    def f(shape):
+        x = np.ones(shape)
+        x[:, :, 1] = np.exp2(up).reshape(shape[0], shape[1], shape[3])
+        return x
+    return _scaled(inputs.pack_int4(p.prefix.k_pages, p.prefix.v_pages), p.q.shape[2], f)
 
 
 def _quiet_ref(p, kv, window=0, new_rows=(), kv_small=None):
@@ -87,6 +97,67 @@ def test_later_and_earlier_tokens_of_the_same_quarter(sa, cuda_dev, D, pre, e):
     p.v = v
     p.v[[0, 64]] = _large(p.v[:2].shape, e, 5)
     check(*sa.prefill_int4(*_pre(p, cuda_dev, kv), window=20), _pre_ref(p, 20, kv))
+    assert sa.default_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sinks", [True, False])
+@pytest.mark.parametrize("e", [8, 13, 18])
+def test_a_prefix_token_before_the_window(sa, cuda_dev, D, sinks, e):
+    """Window 70: one token of the 32 that share a power of two is large, and hidden from the rows that see the rest."""
+    p = inputs.make_prefill([60], 8, 2, D, seed=38, sinks=sinks, prefix_lens=[400], poison=False)
+    up = np.zeros((p.prefix.num_pages, 2, D // 32, 16))
+    for j in (352, 384):
+        up[int(p.prefix.block_table[0, j // 16]), :, :, j % 16] = e
+    kv = _words_times(p, up)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv), window=70), _pre_ref(p, 70, kv))
+    assert sa.default_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [3, 60, 1000])
+@pytest.mark.parametrize("e", [6, 9, 13, 18])
+def test_a_prefix_token_of_no_weight(sa, cuda_dev, D, at, e):
+    """One large token of the prefix that every row sees with a weight below 2^-60; whole and in parts."""
+    p = inputs.make_prefill([60, 3], 8, 2, D, seed=39, prefix_lens=[1100, 64], poison=False)
+    _hide(p, [(0, at)])
+    up = np.zeros((p.prefix.num_pages, 2, D // 32, 16))
+    page = int(p.prefix.block_table[0, at // 16])
+    up[page, :, :, at % 16] = e
+    kv = _words_times(p, up)
+    up[page, :, :, at % 16] = -np.inf
+    ref = _quiet_ref(p, kv, kv_small=_words_times(p, up))
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv)), ref)
+    ws = torch.zeros(256, dtype=torch.uint8, device=cuda_dev)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv), workspace_buf=ws), ref)
+    assert sa.get_status(ws) == 0 and sa.default_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e", [6, 9, 13, 18])
+@pytest.mark.parametrize("base", [0, -40])
+def test_large_channels_of_the_prefix(sa, cuda_dev, D, e, base):
+    """The first 32 channels of every token are large: the others keep the precision of their own size, to the
+    last bit where a row sees one token."""
+    p = inputs.make_prefill([40, 1], 8, 2, D, seed=40, sinks=False, prefix_lens=[700, 0], poison=False)
+    p.v[:] = 0.0
+    up = np.full((p.prefix.num_pages, 2, D // 32, 16), float(base))
+    small = up.copy()
+    up[:, :, 0] += e
+    small[:, :, 0] = -np.inf
+    kv = _words_times(p, up)
+    ref = _pre_ref(p, kv=kv)
+    out, lse = sa.prefill_int4(*_pre(p, cuda_dev, kv))
+    check(out, lse, ref)
+    check(out[..., 32:], lse, (ref[0][..., 32:], ref[1], _pre_ref(p, kv=_words_times(p, small))[2]))
+    # a window of two: the first new row sees the prefix's last token and itself, whose weight is nothing
+    p.q[:, :, 0] = 8.0
+    p.k[:, :, 0] = -64.0
+    p.prefix.k_pages[..., 0] = 0.0
+    kv = _words_times(p, up)
+    want = plain.values_int4(kv)[1][int(p.prefix.block_table[0, 43]), :, 699 % 16]
+    out = sa.prefill_int4(*_pre(p, cuda_dev, kv), window=2)[0][0].double().cpu().numpy()
+    assert np.array_equal(out, np.repeat(want, 4, axis=0))
     assert sa.default_status() == 0
 
 
