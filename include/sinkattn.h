@@ -430,8 +430,8 @@ int sinkattn_prefill_int8_report(const void *q, const void *k, const void *v, co
  *     bytes are words [D / 32][16]: a bf16 scale s with four significant bits (its low four bits
  *     zero) and in their place the code z of the value 0.
  *   - value = s * (code - z), codes and z in 0 .. 15.  It is a bf16 number (sinkattn_unpack_kv_int4).
- * Scales must be finite and not negative, for the attention below 2^100; words of slots that hold no
- * tokens are not used.
+ * Scales must be finite and not negative, for the attention below 2^100 (those below 2^-100, which the
+ * append does not write, may count as 0); words of slots that hold no tokens are not used.
  *
  * sinkattn_append_kv_int4: new bf16 rows into the slots given (for example by sinkattn_plan_step).
  * For a token's group of 32 channels, low = min(0, min x) and high = max(0, max x) of its finite

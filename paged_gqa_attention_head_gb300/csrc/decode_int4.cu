@@ -71,6 +71,7 @@ constexpr float kMaxSlack = 8.f;  // the running maximum, a whole number, moves 
 constexpr float kPUp = 128.f;     // P = 2^(s - m), at most 2^8, enters its product 2^7 times as large: f16's range
 constexpr float kStateDown = 1.f / 256.f;  // states leave with their sums over 2^kMaxSlack, the largest P
 constexpr float kUp24 = 16777216.f;          // 2^24
+constexpr float kScaleLeast = 7.888609052210118e-31f;  // 2^-100, the least V scale that P is taken relative to
 constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;  // pairs of codes in place, and 16 times them
 constexpr uint32_t kBoth = 0x00FF00FFu;                      // pairs of (even code + 16 odd code)
 
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(Int4Cfg<D, NH>::kThreads, Int4Cfg<D, NH>::kCta
                 const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vmx));
                 float move = 1.f;
                 if (__uint_as_float(vb) > v_top) {
-                    const float top = __uint_as_float((vb + 0x7FFFFFu) & 0x7F800000u);
+                    // (not below 2^-100, where its inverse would leave fp32)
+                    const float top = fmaxf(__uint_as_float((vb + 0x7FFFFFu) & 0x7F800000u), kScaleLeast);
                     v_inv = kPUp / top;
                     move = v_top / top;
                     v_top = top;
