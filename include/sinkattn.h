@@ -542,6 +542,10 @@ int sinkattn_plan_step(const int32_t *new_lens, const int32_t *seq_lens, int32_t
  * A length that is negative or passes the table sets SINKATTN_STATUS_BAD_LENGTH (no page of it is
  * released), and so does a list that would pass num_pages entries (the pages past it are dropped); an
  * entry outside [0, num_pages) is pushed as it is and sets SINKATTN_STATUS_BAD_PAGE.
+ * Pages are not counted or compared: each page of a request that is released must be that request's alone
+ * and not in the list yet.  One that another row of the table names too (the attention and the unpacking
+ * read such tables) would be handed out while the other request still reads it, and, were both released,
+ * to two requests; whoever shares pages counts their holders and releases rows without them.
  * Other arguments as for sinkattn_plan_step. */
 int sinkattn_release_pages(const uint8_t *done, const int32_t *seq_lens, const int32_t *block_table,
                            int32_t *free_pages, const int32_t *num_free, int32_t *seq_lens_out, int32_t *num_free_out,

@@ -1098,8 +1098,9 @@ def plan_step(new_lens, seq_lens, block_table, free_pages, num_free, max_tokens,
 
 def release_pages(done, seq_lens, block_table, free_pages, num_free, update=False, workspace_buf=None):
     """The pages of the requests with done (bool [B]) back to the list of free pages, which is updated in
-    place, and their lengths to 0 (sinkattn_release_pages).  update as for plan_step.  Returns
-    (seq_lens, num_free)."""
+    place, and their lengths to 0 (sinkattn_release_pages).  A page must be its request's alone and not in
+    the list yet: one that rows of the table share would come to two requests.  update as for plan_step.
+    Returns (seq_lens, num_free)."""
     dev = _need_cuda(done, "done")
     _need_dense(done, "done", torch.bool, dev, 1)
     B, columns, pages = _need_page_list(seq_lens, block_table, free_pages, num_free, dev)
