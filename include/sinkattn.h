@@ -438,7 +438,7 @@ int sinkattn_prefill_int8_report(const void *q, const void *k, const void *v, co
  * elements:
  *     s    = the smallest number of four significant bits with 15 s >= high - low (below 2^-100: 0)
  *     z    = -low / s rounded,  code = min(15, x / s + z rounded), ties to even (both 0 if s is 0)
- * so a finite element is off by at most s / 2, and 0 stays 0.  Infinities take the codes 15 and 0 and
+ * so a finite element is off by at most s / 2 (where s is 0, by its own size, below 2^-96), and 0 stays 0.  Infinities take the codes 15 and 0 and
  * NaN the value 0, and both set SINKATTN_STATUS_VALUE_RANGE.
  * k, v:          bf16, row t at k + t * k_row_stride elements (>= Hkv * D, a multiple of 8):
  *                [Hkv, D] dense, so K and V may lie inside a fused projection's rows
@@ -466,9 +466,10 @@ int sinkattn_unpack_kv_int4(const void *kv_pages, const int32_t *pages, int32_t 
  * 256-byte header zero before the first call; calls that share one must be ordered on the GPU.
  * status: as in sinkattn_decode_int8_report (NULL: bits go to the workspace's header).
  * Codes and z enter the products exactly, scales of K multiply fp32 scores.  A probability is taken
- * times its token's V scale of the group, relative to a power of two of the largest V scale met, and
- * the product is rounded once to fp16 (relative 2^-11 at most; from 2^20 below the largest product on,
- * 2^-31 of that).  q is taken in fp16 times a power of two of its (sequence, KV head): an entry keeps
+ * times its token's V scale of the group, relative to a power of two above the largest V scale that its
+ * run of the sequence has met, and the product is rounded once to fp16: relative 2^-11 at most, and from 2^20
+ * below the largest probability times that power of two on, 2^-31 of that (a V scale 2^22 times the others
+ * costs them bits, whatever its weight).  q is taken in fp16 times a power of two of its (sequence, KV head): an entry keeps
  * its 8 bits unless it is more than 2^27 times smaller than the largest of its group.  (With a
  * sliding window it runs the split-KV kernel too, over the visible pages.) */
 int sinkattn_decode_int4_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
