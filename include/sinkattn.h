@@ -438,8 +438,8 @@ int sinkattn_prefill_int8_report(const void *q, const void *k, const void *v, co
  * elements:
  *     s    = the smallest number of four significant bits with 15 s >= high - low (below 2^-100: 0)
  *     z    = -low / s rounded,  code = min(15, x / s + z rounded), ties to even (both 0 if s is 0)
- * so a finite element is off by at most s / 2 (where s is 0, by its own size, below 2^-96), and 0 stays 0.  Infinities take the codes 15 and 0 and
- * NaN the value 0, and both set SINKATTN_STATUS_VALUE_RANGE.
+ * so a finite element is off by at most s / 2 (where s is 0, by its own size, below 2^-96), and 0 stays
+ * 0.  Infinities take the codes 15 and 0 and NaN the value 0, and both set SINKATTN_STATUS_VALUE_RANGE.
  * k, v:          bf16, row t at k + t * k_row_stride elements (>= Hkv * D, a multiple of 8):
  *                [Hkv, D] dense, so K and V may lie inside a fused projection's rows
  * slots:         int64 [total_tokens], page * 16 + place in the page; a negative one marks padding,
@@ -469,9 +469,9 @@ int sinkattn_unpack_kv_int4(const void *kv_pages, const int32_t *pages, int32_t 
  * times its token's V scale of the group, relative to a power of two above the largest V scale that its
  * run of the sequence has met, and the product is rounded once to fp16: relative 2^-11 at most, and from 2^20
  * below the largest probability times that power of two on, 2^-31 of that (a V scale 2^22 times the others
- * costs them bits, whatever its weight).  q is taken in fp16 times a power of two of its (sequence, KV head): an entry keeps
- * its 8 bits unless it is more than 2^27 times smaller than the largest of its group.  (With a
- * sliding window it runs the split-KV kernel too, over the visible pages.) */
+ * costs them bits, whatever its weight).  q is taken in fp16 times a power of two of its (sequence, KV
+ * head): an entry keeps its 8 bits unless it is more than 2^27 times smaller than the largest of its
+ * group.  (With a sliding window it runs the split-KV kernel too, over the visible pages.) */
 int sinkattn_decode_int4_workspace_size(const sinkattn_paged_desc *desc, size_t *bytes);
 
 int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *block_table, const int32_t *seq_lens,
@@ -483,12 +483,14 @@ int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *blo
  * bf16.  It computes what sinkattn_prefill does over a bf16 prefix of the same values: K exactly (scales
  * from 2^-60 on), V in fp16 over a power of two 2^k for each 32 keys, whatever its size (from 2^-100 on).
  * The prefix's values come to lie below 2^-4, or below 2^11 where the scales of 32 keys lie more than 2^8
- * apart: those of scales up to 2^27 below the largest are exact, the others to 2^-31 of it.  Of the new tokens' V, whose largest lies between 2^e and 2^(e + 1), those from 2^(k - 17) on
- * are exact and the others off by 2^(k - 25) at most, k = 0 for e from -8 to 3, (e - 2) / 2 above, e + 8 below.
- * A probability enters times 2^k, rounded to fp16: relative 2^-11 at most, and from 2^20 below the largest
- * such product of the keys that its row sees on (a sink counts with the k of that product) 2^-31 of that.  K scales of 2^34 or more and V scales of 2^18 or more set
- * SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be below 2^80 (else
- * SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.  Other arguments and errors as for
+ * apart: those of scales up to 2^27 below the largest are exact, the others to 2^-31 of it.  Of the new
+ * tokens' V, the largest of 32 tokens between 2^e and 2^(e + 1), those from 2^(k - 17) on are exact and the
+ * others off by 2^(k - 25) at most: k = 0 for e from -8 to 3, (e - 2) / 2 above, e + 8 below.  A probability
+ * enters times 2^k, rounded to fp16: relative 2^-11 at most, and from 2^20 below the largest such product
+ * of the keys that its row sees on (a sink counts with the k of that product) 2^-31 of that; what keys that
+ * the row does not see hold decides nothing but the k of the 32 that they share.  K scales of 2^34 or more
+ * and V scales of 2^18 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be
+ * below 2^80 (else SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.  Other arguments and errors as for
  * sinkattn_prefill, the workspace as for sinkattn_prefill_int8 (with sinkattn_prefill_int4_workspace_size
  * bytes, calls with few query rows split their prefixes). */
 int sinkattn_prefill_int4_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,

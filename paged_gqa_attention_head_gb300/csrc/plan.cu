@@ -15,7 +15,8 @@
 // A captured step carries the lengths and the list's size on from replay to replay, so their new
 // values may lie where the old ones are.  Then the blocks are one cluster, and its barrier lies
 // between the reads and the writes; otherwise they are a plain grid, which is launched sooner (a cluster's
-// launch takes some 6 us more of host time).
+// launch takes some 6 us more of host time) and may be wider.  In place, inside a graph: the prompts 8.8 us, the long
+// release 9.3 (eight blocks, a cluster launch), the single tokens 4.3 (one block).
 #include "internal.h"
 #include "ptx.cuh"
 

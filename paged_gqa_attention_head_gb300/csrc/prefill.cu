@@ -34,8 +34,10 @@
 //   warps 12..15 convert each V tile in shared memory from bf16 to fp16, one 32-key
 //               quarter per warp (one warp per SM sub-partition), each quarter scaled by
 //               its own power of two 2^-k that keeps it in fp16 range (k = 0 unless
-//               |v| >= 2^15; 4-bit prefix: k from every quarter's largest scale or value); the
-//               softmax multiplies P by 2^k over the same 32 keys.
+//               |v| >= 2^15; 4-bit prefix: k from every quarter's largest scale or value, and a
+//               row's m from P * 2^k of the keys that it sees, so that values of any size keep P's
+//               bits and hidden ones change nothing); the softmax multiplies P by 2^k over the
+//               same 32 keys.
 // TMEM columns.  S products are numbered i = 0, 1, ... over the CTA's lifetime (key tile
 // by key tile, query tile x = i % ntiles).  At head_dim 64: two S buffers of 128 columns,
 // two P buffers of 64 (fp16 pairs), O_A and O_B of 64.  S(i) goes to S buffer i % 2 as
@@ -58,7 +60,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPSumLimit = 256.0f;  // P values (times 2^-k) stay at most 2^8
 // 4-bit prefix: P * 2^k of a row's largest product starts at 2^6, and its maximum moves once one passes fp16's largest
 // number.  (From 2^8 on, rows that begin with few keys move often: 8 x 512 over 16385, window 128, 78.5 us where 2^6
-// takes 72.2 and 1 71.5.)
+// takes 72.2 and 2^4 71.7.)
 constexpr float kInt4Start = 6.f, kInt4PLimit = 65504.f;
 constexpr int kBM = 128;                   // query rows per tile
 constexpr int kBN = 128;                   // keys per tile
@@ -342,7 +344,8 @@ __device__ __forceinline__ void convert_int8_quarter(uint8_t *t, int q, int lane
 // for V.  Four bits in place, or four bits up, are the subnormal code * u or 16 * code * u (u = 2^-133 in
 // bf16, 2^-24 in fp16), so one multiplication and addition makes each pair of values, exactly: times the
 // scale over u (sa), or a sixteenth of it (sb), less z times the scale (c, of four and four bits).  (8 x 512
-// over 16384 1315 us; 1414 with 128 + code, 1024 + code: a difference and a product for each pair.)
+// over 16384 1315 us when it was built, 1309 now; 1414 with 128 + code, 1024 + code: a difference and a product
+// for each pair.)
 template <bool kV>
 __device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t sa, uint32_t sb, uint32_t c) {
     uint32_t o[4];
@@ -356,7 +359,7 @@ __device__ __forceinline__ uint4 int4x8(uint32_t w, uint32_t sa, uint32_t sb, ui
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// The same for fp16 values above what that reaches: code less z over 2^9 (c: less z over 2^9), times the scale times 2^9.
+// The same for fp16 values above what that reaches: (code - z) / 2^9, exactly (c: -z / 2^9), times the scale times 2^9.
 __device__ __forceinline__ uint4 int4x8_wide(uint32_t w, uint32_t s9, uint32_t c) {
     uint32_t o[4];
 #pragma unroll
@@ -370,7 +373,7 @@ constexpr float kInt4KUp = 1099511627776.f;  // 2^40: K tiles hold values over i
 constexpr uint32_t kInt4KMax = 0x5080u;      // 2^34: K scales from here on do not fit
 
 // The loop over the quarter's pages where V's scales lie far apart; up: 2^(9 - k).  (Apart from the other: with both in
-// one loop the long chunks take 1413 us where this takes 1308.)
+// one loop the long chunks take 1413 us where this takes 1309; 1393 where every quarter comes here.)
 template <int D>
 __device__ __forceinline__ void convert_int4_wide(uint8_t *t, int q, int lane, int rows, float up) {
     using C = PrefillCfg<D>;
