@@ -485,8 +485,8 @@ int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *blo
  * The prefix's values come to lie below 2^-4, or below 2^11 where the scales of 32 keys lie more than 2^8
  * apart: those of scales up to 2^27 below the largest are exact, the others to 2^-31 of it.  Of the new
  * tokens' V, the largest of 32 tokens between 2^e and 2^(e + 1), those from 2^(k - 17) on are exact and the
- * others off by 2^(k - 25) at most: k = 0 for e from -8 to 3, (e - 2) / 2 above, e + 8 below.  A probability
- * enters times 2^k, rounded to fp16: relative 2^-11 at most, and from 2^20 below the largest such product
+ * others off by 2^(k - 25) at most: k = e - 2, or half of that where it is positive.  A probability enters
+ * times 2^k, rounded to fp16: relative 2^-11 at most, and from 2^20 below the largest such product
  * of the keys that its row sees on (a sink counts with the k of that product) 2^-31 of that; what keys that
  * the row does not see hold decides nothing but the k of the 32 that they share.  K scales of 2^34 or more
  * and V scales of 2^18 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be

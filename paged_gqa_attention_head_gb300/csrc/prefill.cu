@@ -1405,12 +1405,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) set_status(a.status, SINKATTN_STATUS_VALUE_RANGE);
                     kexp = min(kexp, 7);
                 }
-                // 4-bit: k = 0 for a largest value from 2^-8 to 2^4, so that one far larger (which some rows may not see) costs
-                // the others few bits; half the exponent more above, since the P of a prefix of that size lies the
-                // whole exponent higher; and values of any size below
+                // 4-bit: the largest value comes to lie above 2^2, so that one far larger than the others (which some rows
+                // may not see) costs them few bits; above 2^3 half its exponent remains, for those bits against P's,
+                // which lie the whole exponent higher for a prefix of that size
                 if (kInt4) {
                     const int e = min((int)(mx >> 7) - 127, 21);
-                    kexp = e > 2 ? (e - 2) >> 1 : max(min(e + 8, 0), kInt4MinExp);
+                    kexp = e > 2 ? (e - 2) >> 1 : max(e - 2, kInt4MinExp);
                 }
                 const float sc = __uint_as_float((uint32_t)(127 - kexp) << 23);  // 2^-k
 #pragma unroll 1

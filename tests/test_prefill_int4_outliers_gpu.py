@@ -101,6 +101,22 @@ def test_later_and_earlier_tokens_of_the_same_quarter(sa, cuda_dev, D, pre, e):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [-60, -20, -9, 5])
+@pytest.mark.parametrize("window", [0, 2, 40])
+def test_large_tokens_among_values_of_any_size(sa, cuda_dev, D, size, window):
+    """Tokens 2^14 times the others, whatever the others' size; two of 32 among the new ones, one of 64 in the prefix."""
+    p = inputs.make_prefill([150, 70], 4, 2, D, seed=42, sinks=window == 2, prefix_lens=[0, 300], poison=False)
+    v = p.v.double() * 2.0 ** size
+    v[5::16] *= 2.0 ** 14
+    p.v = v.to(torch.bfloat16)
+    up = np.full((p.prefix.num_pages, 2, D // 32, 16), float(size))
+    up[::4, :, :, 9] += 12.0
+    kv = _words_times(p, up)
+    check(*sa.prefill_int4(*_pre(p, cuda_dev, kv), window=window), _pre_ref(p, window, kv))
+    assert sa.default_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("sinks", [True, False])
 @pytest.mark.parametrize("e", [8, 13, 18])
 def test_a_prefix_token_before_the_window(sa, cuda_dev, D, sinks, e):
@@ -177,9 +193,9 @@ def test_a_large_channel(sa, cuda_dev, D, pre, e):
     p.v[:, :, 5] = 0.0
     check(out[..., rest], lse, (ref[0][..., rest], ref[1], _pre_ref(p, kv=kv)[2]))
     if not pre:
-        # a row that sees one key, no sink: that key's V.  V lies in fp16 over 2^k (k = 0 for a largest below 2^4, (e - 2) / 2
-        # for one from 2^e on), whose steps are 2^-24: eight bits are exact from 2^(k - 17) on, below that half a step
-        # of 2^(k - 24) is lost at most, and then a rounding to bf16
+        # a row that sees one key, no sink: that key's V.  V lies in fp16 over 2^k (k at most 0 for a largest below 2^4,
+        # (e - 2) / 2 for one from 2^e on), whose steps are 2^-24: eight bits are exact from 2^(k - 17) on, below that
+        # half a step of 2^(k - 24) is lost at most, and then a rounding to bf16
         k = max(0, (e - 2) // 2)
         for got, want in ((out[0, :4], v[0, :1]), (out[150, 4:], v[150, 1:])):
             err = (got.cpu().double() - want.double()).abs()
