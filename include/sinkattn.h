@@ -488,11 +488,12 @@ int sinkattn_decode_int4(const void *q, const void *kv_pages, const int32_t *blo
  * others off by 2^(k - 25) at most: k = e - 2, or half of that where it is positive.  A probability enters
  * times 2^k, rounded to fp16: relative 2^-11 at most, and from 2^20 below the largest such product
  * of the keys that its row sees on (a sink counts with the k of that product) 2^-31 of that; what keys that
- * the row does not see hold decides nothing but the k of the 32 that they share.  K scales of 2^34 or more
- * and V scales of 2^18 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then unspecified); scale must be
- * below 2^80 (else SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.  Other arguments and errors as for
- * sinkattn_prefill, the workspace as for sinkattn_prefill_int8 (with sinkattn_prefill_int4_workspace_size
- * bytes, calls with few query rows split their prefixes). */
+ * the row does not see hold decides nothing but the k of the 32 that they share.  (Keys whose 32 V are all 0
+ * count in lse and the denominator from 2^(c - 32) of the largest weight on, 2^c the largest V scale met.)
+ * K scales of 2^34 or more and V scales of 2^18 or more set SINKATTN_STATUS_VALUE_RANGE (outputs then
+ * unspecified); scale must be below 2^80 (else SINKATTN_ERR_UNSUPPORTED).  status: as for the decode.
+ * Other arguments and errors as for sinkattn_prefill, the workspace as for sinkattn_prefill_int8 (with
+ * sinkattn_prefill_int4_workspace_size bytes, calls with few query rows split their prefixes). */
 int sinkattn_prefill_int4_workspace_size(const sinkattn_paged_desc *desc, int32_t total_tokens,
                                          size_t *bytes);
 
